@@ -341,6 +341,183 @@ int rar_trace(rar_handle h, unsigned long long *work_ns, unsigned long long *wai
  * Errors: RAR_EINVAL (null handle), RAR_ECUDA. */
 int rar_debug_set_epoch(rar_handle h, unsigned epoch);
 
+/* ---------------------------------------------------------------------------
+ * Operators of a tensor-parallel language model.
+ *
+ * Such a model meets the reduction over its p ranks in three places: the
+ * residual stream joins the sum of the ranks' partial outputs and is
+ * normalised (rar_add_rmsnorm); the output layer's vocabulary is cut into one
+ * piece per rank, over which the softmax is reduced (rar_vocab_xent); and the
+ * input table is cut the same way (rar_embedding).  The source pages have no
+ * such calls.  Here the reduction is part of the operator, and what every rank
+ * would hold afterwards is written once, since the ranks share one memory.
+ *
+ * Conventions of these calls, beyond those at the top of this file:
+ *   - dtype is RAR_FLOAT32, RAR_BFLOAT16 or RAR_FLOAT16 where nothing else is
+ *     said; RAR_INT32 is refused with RAR_EUNSUPPORTED.
+ *   - Matrices are row-major with contiguous rows; *_stride is the distance
+ *     between rows in elements, 0 means densely packed rows, any other value
+ *     must be at least the row's length.  Addresses need the alignment of
+ *     their type only, where nothing else is said.
+ *   - "Piece r" of a vocabulary is rows [start_r, start_(r+1)) by
+ *     chunk_bounds(vocab, p), as a matrix of its own; an empty piece may be
+ *     NULL.
+ *   - Indices (tokens, targets) are signed 32 or 64 bits wide (index_bytes 4 or
+ *     8).  An index outside [0, vocab) marks a place that is left out.
+ *   - Sums, norms and softmax statistics are held in 32 bits; a result is
+ *     rounded once, where it is written.  Results do not depend on timing:
+ *     the same call gives the same bits.
+ *   - An output may not overlap an input or another output, except where a
+ *     call names the pairs that may be the same matrix.
+ *   - Argument errors are RAR_EINVAL (null handle, struct or matrix, a size,
+ *     stride, dtype or pointer out of its range, a pointer that is not device
+ *     memory of the handle's device) and launch nothing.  rar_status covers
+ *     these calls too.  They may be captured into CUDA graphs, unless p is above
+ *     64.  They allocate nothing: what they need beyond the results is the
+ *     caller's workspace, 256-byte aligned, whose size a call of its own gives
+ *     and whose contents mean nothing between calls.
+ */
+
+/* s = residual + x_0 + ... + x_(p-1), y = s / sqrt(mean(s^2) + eps) * weight,
+ * row by row: the join of the residual stream with the ranks' partial results,
+ * and the norm that the next layer begins with.  The partials are added in the
+ * ring's hop order of the flat rows x dim buffer (so with RAR_FLOAT32 and
+ * without residual `sum` has rar_allreduce's bits), in 32 bits throughout, then the
+ * residual; y is taken from the unrounded s.
+ * 8-bit output: for each row and each run of `group` columns,
+ * scale = max(min(max|y|, FLT_MAX) / 448, FLT_MIN) over the values that are not
+ * NaN, and code = y / scale rounded to nearest even to float8 e4m3 (finite
+ * codes up to +-448, which also takes infinities; NaN stays NaN). */
+typedef struct {
+    const void *const *parts; /* host array of p matrices rows x dim */
+    int p;                    /* 1 .. RAR_MAX_P */
+    int dtype;                /* of parts, residual, weight, sum and out */
+    size_t rows, dim;         /* 0 rows: nothing is done; dim 1 .. RAR_NORM_MAX_DIM */
+    size_t part_stride;
+    const void *residual;     /* rows x dim, or NULL */
+    size_t residual_stride;
+    const void *weight;       /* dim, or NULL: ones */
+    float eps;                /* >= 0 */
+    void *sum;                /* out: s, or NULL; may be the residual or a part itself */
+    size_t sum_stride;
+    void *out;                /* out: y, or NULL; may be a part itself, or the residual */
+    size_t out_stride;
+    float *rstd;              /* out: rows values 1 / sqrt(mean(s^2) + eps), or NULL */
+    void *out8;               /* out: codes, one byte each, or NULL */
+    size_t out8_stride;
+    float *scales;            /* out: rows x ceil(dim / group), needed with out8 */
+    size_t group;             /* columns per scale; 0: the whole row; else a multiple of 32 */
+} rar_rmsnorm_args;
+
+#define RAR_NORM_MAX_DIM 32768
+
+int rar_add_rmsnorm(rar_handle h, const rar_rmsnorm_args *a, void *stream);
+
+/* Gradient of rar_add_rmsnorm, from the gradients of y (dout) and of s (dsum):
+ *   dx = dsum + rstd (weight dout - s rstd^2 mean(weight dout s)),
+ * which is the gradient of the residual and of every part alike, and
+ *   dweight = sum over the rows of dout s rstd, added in a fixed order. */
+typedef struct {
+    int dtype;                /* of every matrix and of weight and dweight */
+    size_t rows, dim;         /* 0 rows: dweight is zeros */
+    const void *dout;         /* rows x dim */
+    size_t dout_stride;
+    const void *dsum;         /* rows x dim, or NULL: zeros */
+    size_t dsum_stride;
+    const void *sum;          /* s as rar_add_rmsnorm wrote it */
+    size_t sum_stride;
+    const float *rstd;
+    const void *weight;       /* dim, or NULL: ones */
+    void *dx;                 /* out: rows x dim, or NULL; may be dout or dsum itself */
+    size_t dx_stride;
+    void *dweight;            /* out: dim, or NULL */
+    void *workspace;          /* needed with dweight */
+    size_t workspace_bytes;
+} rar_rmsnorm_grad_args;
+
+size_t rar_add_rmsnorm_grad_workspace(size_t rows, size_t dim);
+int rar_add_rmsnorm_grad(rar_handle h, const rar_rmsnorm_grad_args *a, void *stream);
+
+/* Softmax cross entropy over a vocabulary in p pieces, from the hidden states:
+ *   z = hidden W^T, lse = log sum exp(z), loss = lse - z[target],
+ * and, where dhidden or dweights is given, the gradients of
+ * sum over the tokens of token_weight x loss:
+ *   G = (exp(z - lse) - onehot(target)) token_weight,
+ *   dhidden = G W,  dweights = G^T hidden.
+ * The logits are never kept: they are computed a tile at a time, once for lse and
+ * once more for G, which is held in the dtype for a window of the vocabulary at a
+ * time.  A token whose target is left out has loss 0 and no gradient, whatever its
+ * hidden state holds; its lse is computed.
+ * dtype: RAR_BFLOAT16 or RAR_FLOAT16 (RAR_FLOAT32: RAR_EUNSUPPORTED).  dim is a
+ * multiple of 8, matrices are 16-byte aligned with strides that are multiples of
+ * 8, p is at most 64. */
+typedef struct {
+    const void *hidden;          /* tokens x dim */
+    size_t hidden_stride;
+    const void *const *weights;  /* host array of p pieces, rows x dim */
+    size_t weight_stride;        /* of every piece */
+    int p;
+    int dtype;
+    size_t tokens, dim, vocab;   /* tokens may be 0, dim and vocab at least 1 */
+    const void *targets;         /* tokens indices */
+    int index_bytes;
+    const float *token_weight;   /* tokens, or NULL: ones */
+    float *loss;                 /* out: tokens, or NULL */
+    float *lse;                  /* out: tokens, or NULL */
+    void *dhidden;               /* out: tokens x dim, or NULL */
+    size_t dhidden_stride;
+    void *const *dweights;       /* out: host array of p pieces, or NULL */
+    size_t dweight_stride;
+    void *workspace;
+    size_t workspace_bytes;
+} rar_vocab_xent_args;
+
+/* grad: whether dhidden or dweights will be asked for.  0 where the sizes are refused. */
+size_t rar_vocab_xent_workspace(size_t tokens, size_t dim, size_t vocab, int p, int grad);
+int rar_vocab_xent(rar_handle h, const rar_vocab_xent_args *a, void *stream);
+
+/* out[t] = scale x table[tokens[t]] over a table in p pieces; zeros where a
+ * token is left out. */
+typedef struct {
+    const void *const *tables; /* host array of p pieces, rows x dim */
+    size_t table_stride;       /* of every piece */
+    int p;                     /* 1 .. RAR_MAX_P */
+    int dtype;
+    size_t vocab, dim;         /* at least 1 */
+    const void *tokens;        /* n_tokens indices */
+    int index_bytes;
+    size_t n_tokens;           /* 0: nothing is done */
+    float scale;
+    void *out;                 /* n_tokens x dim */
+    size_t out_stride;
+} rar_embedding_args;
+
+int rar_embedding(rar_handle h, const rar_embedding_args *a, void *stream);
+
+/* Gradient of rar_embedding for the table, dtables[v] = scale x sum of dout[t]
+ * over the t with tokens[t] = v: the tokens are sorted and each row's gradients
+ * added in the order of t in 32 bits.  accumulate: added to what dtables holds (rows
+ * without a token stay untouched); otherwise every row is written. */
+typedef struct {
+    const void *dout;          /* n_tokens x dim */
+    size_t dout_stride;
+    const void *tokens;
+    int index_bytes;
+    size_t n_tokens;           /* at most 2^24 */
+    void *const *dtables;      /* host array of p pieces */
+    size_t dtable_stride;
+    int p;
+    int dtype;
+    size_t vocab, dim;         /* at least 1; vocab at most 2^31 - 1 */
+    float scale;
+    int accumulate;
+    void *workspace;
+    size_t workspace_bytes;
+} rar_embedding_grad_args;
+
+size_t rar_embedding_grad_workspace(size_t n_tokens, size_t vocab, size_t dim);
+int rar_embedding_grad(rar_handle h, const rar_embedding_grad_args *a, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -115,6 +115,7 @@ def load_library():
                      "rar_allreduce_noalloc", "rar_status", "rar_send_counts", "rar_destroy", "rar_version",
                      "rar_trace"):
             getattr(lib, name).restype = i32
+        _ops.declare(lib)
         _lib = lib
         return lib
 
@@ -307,6 +308,23 @@ class Handle:
     def all_gather(self, tensors, stream=None):
         rar_all_gather(self.h, tensors, stream)
 
+    # The model operators (see the functions of the same names in _ops).
+
+    def add_rmsnorm(self, parts, weight=None, **kw):
+        return _ops.rar_add_rmsnorm(self.h, parts, weight, **kw)
+
+    def add_rmsnorm_grad(self, dout, sum, rstd, weight=None, **kw):
+        return _ops.rar_add_rmsnorm_grad(self.h, dout, sum, rstd, weight, **kw)
+
+    def vocab_xent(self, hidden, weights, targets, **kw):
+        return _ops.rar_vocab_xent(self.h, hidden, weights, targets, **kw)
+
+    def embedding(self, tables, tokens, **kw):
+        return _ops.rar_embedding(self.h, tables, tokens, **kw)
+
+    def embedding_grad(self, dout, tokens, dtables, **kw):
+        return _ops.rar_embedding_grad(self.h, dout, tokens, dtables, **kw)
+
     def status(self) -> int:
         return rar_status(self.h)
 
@@ -336,3 +354,6 @@ class Handle:
             self.close()
         except Exception:
             pass
+
+
+from . import _ops  # noqa: E402  (its functions take _check and load_library from here)

@@ -8,7 +8,7 @@
 #include <utility>
 #include <vector>
 
-#include "rar_internal.h"
+#include "rar_ctx.h"
 
 namespace {
 
@@ -40,70 +40,12 @@ constexpr size_t kLLAutoMaxBytes = (size_t)1 << 20;
 constexpr int kLLTreeAutoMinP = 16;
 constexpr size_t kLLTreeAutoMaxBytes = (size_t)64 << 10;
 
-thread_local std::string g_init_error;  // errors before a handle exists
 // step trace: {work, wait} per (rank, step)
 constexpr size_t kTraceWords = 2 * (size_t)RAR_MAX_P * RAR_TRACE_MAX_STEPS;
 
 }  // namespace
 
-struct rar_ctx {
-    int device = 0;
-    rar_options opt{};
-    std::string err;
-    int sm_count = 0;
-    // scratch owned by the handle (ring engines; table for p > kInlineP)
-    unsigned long long *flags = nullptr;
-    unsigned long long *recv_counts = nullptr;
-    RingStatus *status = nullptr;
-    unsigned *abort_word = nullptr;
-    unsigned *epoch_words = nullptr;  // [0] last finished launch's epoch, [1] finish counter
-    void **ptr_table = nullptr;
-    unsigned long long *ll_box = nullptr;  // low-latency mailbox, kLLMailboxWords
-    unsigned long long *trace = nullptr;   // step trace (rar_options.trace), kTraceWords
-    bool last_traced = false;              // the last call filled the trace
-    int last_trace_steps = 0;
-    unsigned acked_seq = 0;           // status failures already reported
-    // last call, for rar_status / rar_send_counts
-    bool have_last = false;
-    cudaStream_t last_stream = nullptr;
-    bool last_ring = false;
-    int last_p = 0;
-    // ring launches of the last call (the hierarchical schedule makes three)
-    int last_phases = 0;
-    int last_layout[3] = {0, 0, 0};
-    int last_channels[3] = {0, 0, 0};
-    int last_fwd_channels[3] = {0, 0, 0};
-    int last_group = 0;
-};
-
 namespace {
-
-int fail(rar_ctx *h, int code, const std::string &msg) {
-    if (h) h->err = msg;
-    else g_init_error = msg;
-    return code;
-}
-
-int cuda_fail(rar_ctx *h, cudaError_t e, const char *what) {
-    return fail(h, RAR_ECUDA, std::string(what) + ": " + cudaGetErrorString(e));
-}
-
-// Make `dev` current for the scope of a call and restore the caller's device.
-struct DeviceGuard {
-    int prev = -1;
-    bool changed = false;
-    cudaError_t err = cudaSuccess;
-    explicit DeviceGuard(int dev) {
-        err = cudaGetDevice(&prev);
-        if (err == cudaSuccess && prev != dev) {
-            err = cudaSetDevice(dev);
-            changed = err == cudaSuccess;
-        }
-    }
-    ~DeviceGuard() {
-        if (changed) cudaSetDevice(prev);
-    }
-};
 
 int check_options(rar_ctx *h, const rar_options &o) {
     if (o.engine < RAR_ENGINE_FUSED || o.engine > RAR_ENGINE_TREE)
@@ -159,20 +101,6 @@ int check_call(rar_ctx *h, void *const *bufs, int p, size_t n, int dtype, int op
                                                std::to_string(h->device));
         }
     }
-    return RAR_OK;
-}
-
-// Fill the pointer part of the launch arguments (table copy for large p).
-int fill_ptrs(rar_ctx *h, RankPtrs &rp, void *const *bufs, int p, cudaStream_t stream) {
-    std::memset(&rp, 0, sizeof(rp));
-    if (p <= kInlineP) {
-        for (int r = 0; r < p; r++) rp.inl[r] = bufs[r];
-        return RAR_OK;
-    }
-    // pageable source: staged by the runtime before the call returns
-    cudaError_t ce = cudaMemcpyAsync(h->ptr_table, bufs, sizeof(void *) * (size_t)p, cudaMemcpyHostToDevice, stream);
-    if (ce != cudaSuccess) return cuda_fail(h, ce, "copying the rank pointer table");
-    rp.table = h->ptr_table;
     return RAR_OK;
 }
 
@@ -625,6 +553,7 @@ int run(rar_ctx *h, void *const *bufs, int p, size_t n, int dtype, int op, int p
 }  // namespace
 
 namespace rar {
+thread_local std::string g_init_error;
 // Message returned by rar_last_error(NULL) for entry points without a handle.
 void set_handleless_error(const std::string &msg) { g_init_error = msg; }
 }  // namespace rar
