@@ -755,6 +755,8 @@ int rar_status(rar_handle h) {
                           "ring wait timed out: rank %d, step %d, slice %d, waiting on rank %d "
                           "(progress word 0x%llx, wanted 0x%llx)",
                           st.rank, st.step, st.slice, st.waited_on, st.flag_seen, st.flag_wanted);
+        else if (st.rank == -2)
+            std::snprintf(buf, sizeof(buf), "tile wait timed out: CTA %d, role %d (vocabulary cross entropy)", st.slice, st.step);
         else
             std::snprintf(buf, sizeof(buf),
                           "bulk-copy wait timed out: tile %d, step %d, waiting for rank %d's tile (fused streaming "

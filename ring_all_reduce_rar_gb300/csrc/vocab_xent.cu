@@ -11,16 +11,23 @@
 // time: the logit tiles again, G in the 16-bit type into the workspace, and
 // the two products with it.  dhidden adds up over the windows in 32 bits.
 //
+// All four products run on the tensor cores through one kernel (tc_gemm.cuh):
+// a pair of CTAs computes a 256 x 256 tile, and the epilogue of a tile overlaps the
+// next tile's product (two accumulators).  G is rounded once, to the
+// type of the products that it enters: an error of half a unit in its last place, of the
+// size that rounding dhidden and dweights has anyway.
+//
 // Bound by the tensor cores for many tokens (8 tokens x vocab x dim
 // operations against 6 if the logits were kept), by memory for few.
 #include <algorithm>
 
-#include "op_elem.cuh"
 #include "op_host.h"
+#include "tc_gemm.cuh"
 
 namespace rar {
 
-constexpr int kBlock = 256;  // vocabulary rows of a block
+constexpr int kBlock = 256;  // vocabulary rows of a block: a tile's columns
+constexpr int kTile = 256;   // rows and columns of a tile
 
 struct XentArgs {
     RankPtrs w, dw;  // pieces
@@ -38,15 +45,23 @@ struct XentArgs {
     long long nb_big, nb_small;  // blocks of a piece of base + 1 / base rows
     long long n_blocks;
     // workspace
-    float2 *stats;        // [n_blocks][tokens]: max, sum of exp(z - max)
+    float2 *stats;        // [2 n_blocks][tokens]: a half block's max, sum of exp(z - max)
     float *z_target;      // [tokens]
     float *lse_ws;        // [tokens]
     float *row_weight;    // [tokens] scaled token_weight, 0 where left out
     unsigned *w_max;      // bits of the largest finite |token_weight|
     void *hidden_used;    // [tokens][dim]: hidden, zeros where left out
     void *g;              // [tokens][window * kBlock]
-    float *dh_acc;        // [tokens][dim]
+    float *dh_part;       // [splits][tokens][dim]
     long long window;     // blocks of a window
+    int splits;           // of dhidden's sum over a window
+    bool direct;          // one split: the last window writes dhidden itself
+    TcLimits limits;
+};
+
+// Tensor maps: boxes of 64 rows x 64 elements.
+struct XentMaps {
+    CUtensorMap hidden, hidden_used, g, w[kInlineP];
 };
 
 struct BlockOf {
@@ -84,201 +99,401 @@ __device__ __forceinline__ int g_exponent(const XentArgs &a) {
     return e > 120 ? 120 : e < -120 ? -120 : e;
 }
 
-// C[64][64] of one CTA of 256 threads, 4 x 4 a thread: sum over k of
-// A(i, k) B(j, k).
-template <typename FA, typename FB>
-__device__ __forceinline__ void tile_product(float (&acc)[4][4], long long K, FA &&fa, FB &&fb) {
-    __shared__ float sa[16][65], sb[16][65];
-    const int ti = threadIdx.x / 16, tj = threadIdx.x % 16;
-    for (long long k0 = 0; k0 < K; k0 += 16) {
-        for (int x = threadIdx.x; x < 64 * 16; x += 256) {
-            const int i = x / 16, k = x % 16;
-            sa[k][i] = k0 + k < K ? fa(i, k0 + k) : 0.0f;
-            sb[k][i] = k0 + k < K ? fb(i, k0 + k) : 0.0f;
+enum XentMode { XENT_STATS, XENT_G, XENT_DHIDDEN, XENT_DWEIGHT };
+
+// One tile of a pair of CTAs: its place, and its range along K.
+struct XentItem {
+    long long row;      // first row of the tile (token, or row of the window's blocks)
+    long long col;      // first column (row of the piece, or of dim)
+    int n;              // columns that the product covers, a multiple of 32
+    long long block;    // block of the window (not XENT_DHIDDEN)
+    int split;
+    long long k0, k1;   // XENT_DHIDDEN: blocks of the window; else steps of 64
+};
+
+__device__ __forceinline__ int round32(long long n) { return n >= kTile ? kTile : (int)((n + 31) / 32 * 32); }
+
+// Tiles in an order in which those that run at one time share operands:
+// columns of 8 tiles, so that 76 pairs work on about 8 x 9 tiles.
+template <int MODE>
+__device__ __forceinline__ XentItem xent_item(const XentArgs &a, long long b0, long long nb, long long i) {
+    XentItem o;
+    const long long tb = (a.tokens + kTile - 1) / kTile, db = (a.dim + kTile - 1) / kTile;
+    const long long rows = MODE == XENT_DWEIGHT ? nb : tb;
+    const long long cols = MODE == XENT_DHIDDEN ? db * a.splits : MODE == XENT_DWEIGHT ? db : nb;
+    const long long g = i / (8 * cols), in = i - g * 8 * cols;
+    const long long width = rows - g * 8 < 8 ? rows - g * 8 : 8;
+    const long long r = g * 8 + in % width, c = in / width;
+    o.split = 0;
+    o.block = 0;
+    if (MODE == XENT_STATS || MODE == XENT_G) {
+        o.row = r * kTile;
+        o.block = c;
+        o.col = 0;
+        o.n = round32(block_of(a, b0 + c).rows);
+        o.k0 = 0;
+        o.k1 = (a.dim + 63) / 64;
+    } else if (MODE == XENT_DHIDDEN) {
+        o.row = r * kTile;
+        o.split = (int)(c / db);
+        o.col = c % db * kTile;
+        o.n = round32(a.dim - o.col);
+        o.k0 = nb * o.split / a.splits;
+        o.k1 = nb * (o.split + 1) / a.splits;
+    } else {
+        o.row = r * kTile;
+        o.block = r;
+        o.col = c * kTile;
+        o.n = round32(a.dim - o.col);
+        o.k0 = 0;
+        o.k1 = (a.tokens + 63) / 64;
+    }
+    return o;
+}
+template <int MODE>
+__host__ __device__ inline long long xent_items(const XentArgs &a, long long nb) {
+    const long long tb = (a.tokens + kTile - 1) / kTile, db = (a.dim + kTile - 1) / kTile;
+    return MODE == XENT_DHIDDEN ? tb * db * a.splits : MODE == XENT_DWEIGHT ? nb * db : tb * nb;
+}
+
+// Calls f(k) for every step of 64 along K: f(step within the block or the
+// range, block).  Stops when f returns false.
+template <int MODE, typename F>
+__device__ __forceinline__ bool xent_steps(const XentArgs &a, long long b0, const XentItem &it, F &&f) {
+    if constexpr (MODE == XENT_DHIDDEN) {
+        for (long long k = it.k0; k < it.k1; k++) {
+            const BlockOf b = block_of(a, b0 + k);
+            for (int s = 0; s * 64 < b.rows; s++)
+                if (!f(s, k, b)) return false;
         }
-        __syncthreads();
+    } else {
+        const BlockOf b = block_of(a, b0 + it.block);
+        for (long long s = it.k0; s < it.k1; s++)
+            if (!f((int)s, it.block, b)) return false;
+    }
+    return true;
+}
+
+__device__ __forceinline__ float exp_of(float x) {  // ex2.approx: 2 units in the last place
+    float r;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x * 1.4426950408889634f));
+    return r;
+}
+template <int DT>
+__device__ __forceinline__ uint32_t narrow2(float lo, float hi) {
+    if constexpr (DT == DT_BF16) {
+        __nv_bfloat162 r = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<uint32_t *>(&r);
+    } else {
+        __half2 r = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<uint32_t *>(&r);
+    }
+}
+template <int DT>
+__device__ __forceinline__ uint4 narrow8(const float *v, float scale) {
+    return make_uint4(narrow2<DT>(v[0] * scale, v[1] * scale), narrow2<DT>(v[2] * scale, v[3] * scale),
+                      narrow2<DT>(v[4] * scale, v[5] * scale), narrow2<DT>(v[6] * scale, v[7] * scale));
+}
+
+// A thread's part of a finished tile: one row, 128 columns from `half`.
+template <int MODE, int DT>
+__device__ __forceinline__ void xent_epilogue(const XentArgs &a, long long b0, long long nb, const XentItem &it, long long row,
+                                              int half, float (&v)[128]) {
+    if constexpr (MODE == XENT_STATS) {
+        const BlockOf b = block_of(a, b0 + it.block);
+        if (row >= a.tokens) return;
+        const int cols = b.rows - half;
+        float m = -INFINITY, s = 0.0f;
+        const long long y = load_index(a.targets, a.index_bytes, row) - b.first - half;
+        if (y >= 0 && y < cols && y < 128) {
+            float z = 0.0f;
 #pragma unroll
-        for (int k = 0; k < 16; k++)
+            for (int c = 0; c < 128; c++)  // (in this form v stays in registers)
+                asm("{\n\t.reg .pred P;\n\tsetp.eq.s32 P, %1, %2;\n\tselp.f32 %0, %3, %0, P;\n\t}" : "+f"(z) : "r"((int)y), "r"(c), "f"(v[c]));
+            a.z_target[row] = z;
+        }
+        if (cols < 128) {
 #pragma unroll
-            for (int i = 0; i < 4; i++)
+            for (int c = 0; c < 128; c++) v[c] = c < cols ? v[c] : -INFINITY;
+        }
 #pragma unroll
-                for (int j = 0; j < 4; j++) acc[i][j] = fmaf(sa[k][ti * 4 + i], sb[k][tj * 4 + j], acc[i][j]);
-        __syncthreads();
+        for (int c = 0; c < 128; c++) m = fmaxf(m, v[c]);
+        // nothing but -inf (or NaN, which the sum then shows)
+        const float ref = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+        for (int c = 0; c < 128; c++) s += exp_of(v[c] - ref);
+        a.stats[(2 * (b0 + it.block) + half / 128) * a.tokens + row] = make_float2(m, s);
+    } else if constexpr (MODE == XENT_G) {
+        const BlockOf b = block_of(a, b0 + it.block);
+        if (row >= a.tokens) return;
+        const int cols = b.rows - half;
+        const float w = ldexpf(a.row_weight[row], g_exponent<DT>(a)), lse = a.lse_ws[row];
+        const long long y = load_index(a.targets, a.index_bytes, row) - b.first - half;
+        uint4 *out = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.g) + (row * a.window + it.block) * kBlock + half);
+        const bool hit = y >= 0 && y < 128;
+#pragma unroll
+        for (int c = 0; c < 128; c++) {
+            const float p = exp_of(v[c] - lse) - (hit && c == (int)y ? 1.0f : 0.0f);
+            v[c] = c < cols && w != 0.0f ? p * w : 0.0f;
+        }
+#pragma unroll
+        for (int c = 0; c < 128; c += 8) out[c / 8] = narrow8<DT>(v + c, 1.0f);
+    } else if constexpr (MODE == XENT_DHIDDEN) {
+        if (row >= a.tokens) return;
+        const float undo = ldexpf(1.0f, -g_exponent<DT>(a));
+        const bool first = b0 == 0, last = b0 + nb == a.n_blocks;
+        float *part = a.dh_part + (it.split * a.tokens + row) * a.dim;
+#pragma unroll
+        for (int c = 0; c < 128; c += 8) {
+            const long long d = it.col + half + c;
+            if (d >= a.dim) continue;
+            float4 *q = reinterpret_cast<float4 *>(part + d);
+            if (!first) {
+                const float4 x = q[0], y = q[1];
+                v[c] += x.x, v[c + 1] += x.y, v[c + 2] += x.z, v[c + 3] += x.w;
+                v[c + 4] += y.x, v[c + 5] += y.y, v[c + 6] += y.z, v[c + 7] += y.w;
+            }
+            if (last && a.direct) {
+                *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.dhidden) + row * a.dhidden_stride + d) = narrow8<DT>(v + c, undo);
+            } else {
+                q[0] = make_float4(v[c], v[c + 1], v[c + 2], v[c + 3]);
+                q[1] = make_float4(v[c + 4], v[c + 5], v[c + 6], v[c + 7]);
+            }
+        }
+    } else {
+        const BlockOf b = block_of(a, b0 + it.block);
+        const long long r = row - it.row;
+        if (r >= b.rows) return;
+        const float undo = ldexpf(1.0f, -g_exponent<DT>(a));
+        uint16_t *out = reinterpret_cast<uint16_t *>(rank_ptr(a.dw, a.p, b.piece)) + (b.row + r) * a.dweight_stride;
+#pragma unroll
+        for (int c = 0; c < 128; c += 8) {
+            const long long d = it.col + half + c;
+            if (d < a.dim) *reinterpret_cast<uint4 *>(out + d) = narrow8<DT>(v + c, undo);
+        }
     }
 }
 
-// The logits of 64 tokens x 64 rows of a block; rows beyond it are -inf.
-template <int DT>
-__device__ __forceinline__ void logits_tile(const XentArgs &a, long long t0, const BlockOf &b, int j0, float (&acc)[4][4]) {
-    const char *w = rank_ptr(a.w, a.p, b.piece);
-    tile_product(
-        acc, a.dim, [&](int i, long long k) { return t0 + i < a.tokens ? load_f<DT>(a.hidden, (t0 + i) * a.hidden_stride + k) : 0.0f; },
-        [&](int j, long long k) { return j0 + j < b.rows ? load_f<DT>(w, (b.row + j0 + j) * a.weight_stride + k) : 0.0f; });
-    const int tj = threadIdx.x % 16;
-    for (int i = 0; i < 4; i++)
-        for (int j = 0; j < 4; j++)
-            if (j0 + tj * 4 + j >= b.rows) acc[i][j] = -INFINITY;
-}
-
-// Pass 1: row maxima and sums of exponentials of a block, and the target's logit.
-template <int DT>
-__global__ void __launch_bounds__(256) xent_stats_kernel(const __grid_constant__ XentArgs a) {
+// Persistent: a pair of CTAs takes tiles i, i + pairs, ...  Warps 0 to 7: epilogue,
+// 8: loads, 9 (of the pair's first CTA): products.
+template <int MODE, int DT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
+    xent_tile_kernel(const __grid_constant__ XentArgs a, const __grid_constant__ XentMaps maps, long long b0, long long nb) {
+    extern __shared__ unsigned char dyn[];
+    __shared__ TcShared sh;
+    const uint32_t stages = (smem_u32(dyn) + 1023u) & ~1023u;
+    const uint32_t rank = cluster_rank();
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    tc_begin(&sh);
     pdl_wait();
-    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *a.w_max = 0u;
-    const BlockOf b = block_of(a, blockIdx.x);
-    const int ti = threadIdx.x / 16, tj = threadIdx.x % 16;
-    for (long long t0 = (long long)blockIdx.y * 64; t0 < a.tokens; t0 += (long long)gridDim.y * 64) {
-        float m[4], s[4];
-        for (int i = 0; i < 4; i++) m[i] = -INFINITY, s[i] = 0.0f;
-        for (int j0 = 0; j0 < b.rows; j0 += 64) {
-            float acc[4][4] = {};
-            logits_tile<DT>(a, t0, b, j0, acc);
-            for (int i = 0; i < 4; i++) {
-                const long long t = t0 + ti * 4 + i;
-                if (t < a.tokens) {
-                    const long long y = load_index(a.targets, a.index_bytes, t) - b.first - j0 - tj * 4;
-                    for (int j = 0; j < 4; j++)
-                        if (y == j && j0 + tj * 4 + j < b.rows) a.z_target[t] = acc[i][j];
+    pdl_launch_dependents();
+    if (MODE == XENT_STATS && blockIdx.x == 0 && threadIdx.x == 0) *a.w_max = 0u;
+    const long long items = xent_items<MODE>(a, nb);
+    const long long pairs = gridDim.x / 2, first = blockIdx.x / 2;
+    constexpr bool a_mn = MODE == XENT_DWEIGHT, b_mn = MODE == XENT_DHIDDEN || MODE == XENT_DWEIGHT;
+
+    if (warp == kTcEpilogueWarps && lane == 0) {
+        long long step = 0;
+        for (long long i = first; i < items && !*(volatile int *)&sh.failed; i += pairs) {
+            const XentItem it = xent_item<MODE>(a, b0, nb, i);
+            const int half = (int)rank * it.n / 2;
+            xent_steps<MODE>(a, b0, it, [&](int s, long long k, const BlockOf &b) {
+                const int st = (int)(step % kTcStages);
+                if (step >= kTcStages && !tc_wait(&sh, a.limits, &sh.empty[st], (uint32_t)(step / kTcStages - 1) & 1, 0)) return false;
+                if (rank == 0) tc_expect_tx(&sh.full[st], 2 * kTcStageBytes);
+                const uint32_t bar = peer_addr(smem_u32(&sh.full[st]), 0), to = stages + st * kTcStageBytes;
+                const CUtensorMap *ma = MODE == XENT_STATS || MODE == XENT_G ? &maps.hidden : &maps.g;
+                const CUtensorMap *mb = MODE == XENT_DWEIGHT ? &maps.hidden_used : &maps.w[b.piece];
+                for (int j = 0; j < 2; j++) {
+                    const int row = (int)it.row + (int)rank * 128 + j * 64;
+                    if (MODE == XENT_DHIDDEN) tc_load_box(ma, to + j * 8192, bar, (int)k * kBlock + s * 64, row);
+                    else if (MODE == XENT_DWEIGHT) tc_load_box(ma, to + j * 8192, bar, row, s * 64);
+                    else tc_load_box(ma, to + j * 8192, bar, s * 64, row);
                 }
-                for (int j = 0; j < 4; j++) {
-                    const float z = acc[i][j], top = fmaxf(m[i], z);
-                    if (z == -INFINITY) continue;
-                    s[i] = s[i] * expf(m[i] - top) + expf(z - top);
-                    m[i] = top;
+                for (int j = 0; j < 2; j++) {
+                    const int col = (int)it.col + half + j * 64;
+                    if (MODE == XENT_DHIDDEN) tc_load_box(mb, to + 16384 + j * 8192, bar, col, (int)b.row + s * 64);
+                    else if (MODE == XENT_DWEIGHT) tc_load_box(mb, to + 16384 + j * 8192, bar, col, s * 64);
+                    else tc_load_box(mb, to + 16384 + j * 8192, bar, s * 64, (int)b.row + col);
                 }
-            }
+                step++;
+                return true;
+            });
         }
-        for (int i = 0; i < 4; i++) {
-            for (int o = 1; o < 16; o *= 2) {
-                const float om = __shfl_xor_sync(0xFFFFFFFFu, m[i], o), os = __shfl_xor_sync(0xFFFFFFFFu, s[i], o);
-                const float top = fmaxf(m[i], om);
-                s[i] = top == -INFINITY ? s[i] + os : s[i] * expf(m[i] - top) + os * expf(om - top);
-                m[i] = top;
-            }
-            const long long t = t0 + ti * 4 + i;
-            if (tj == 0 && t < a.tokens) a.stats[(long long)blockIdx.x * a.tokens + t] = make_float2(m[i], s[i]);
+        // neither CTA may leave while the pair's loads or arrivals are on their
+        // way (the loads even after a wait that ran out)
+        for (long long k = step > kTcStages ? step - kTcStages : 0; k < step; k++) {
+            const int st = (int)(k % kTcStages);
+            if (rank == 0) tc_drain(&sh.full[st], (uint32_t)(k / kTcStages) & 1);
+            tc_wait(&sh, a.limits, &sh.empty[st], (uint32_t)(k / kTcStages) & 1, 1);
+        }
+    } else if (warp == kTcEpilogueWarps + 1 && lane == 0 && rank == 0) {
+        long long step = 0, tile = 0;
+        for (long long i = first; i < items; i += pairs, tile++) {
+            const XentItem it = xent_item<MODE>(a, b0, nb, i);
+            const int acc = (int)(tile & 1);
+            if (tile >= 2 && !tc_wait(&sh, a.limits, &sh.acc_empty[acc], (uint32_t)(tile / 2 - 1) & 1, 2)) break;
+            tc_fence_after();
+            const uint32_t d = sh.tmem + acc * kTile, idesc = tc_instruction(DT == DT_BF16, a_mn, b_mn, (uint32_t)it.n);
+            bool more = false;
+            const bool ok = xent_steps<MODE>(a, b0, it, [&](int, long long, const BlockOf &) {
+                const int st = (int)(step % kTcStages);
+                if (!tc_wait(&sh, a.limits, &sh.full[st], (uint32_t)(step / kTcStages) & 1, 3)) return false;
+                tc_fence_after();
+                const uint32_t pa = stages + st * kTcStageBytes, pb = pa + 16384;
+#pragma unroll
+                for (int k = 0; k < 4; k++) {
+                    const uint64_t da = tc_operand(pa + k * (a_mn ? 2048 : 32), a_mn ? 8192 : 16, 1024);
+                    const uint64_t db = tc_operand(pb + k * (b_mn ? 2048 : 32), b_mn ? 8192 : 16, 1024);
+                    tc_mma(d, da, db, idesc, more);
+                    more = true;
+                }
+                tc_commit(&sh.empty[st]);
+                step++;
+                return true;
+            });
+            if (!ok) break;
+            tc_commit(&sh.acc_full[acc]);
+        }
+    } else if (warp < kTcEpilogueWarps) {
+        const int quarter = warp % 4, half = warp / 4 * 128;
+        long long tile = 0;
+        for (long long i = first; i < items; i += pairs, tile++) {
+            const XentItem it = xent_item<MODE>(a, b0, nb, i);
+            const int acc = (int)(tile & 1);
+            if (!tc_wait(&sh, a.limits, &sh.acc_full[acc], (uint32_t)(tile / 2) & 1, 4)) break;
+            __syncwarp();
+            tc_fence_after();
+            float v[128];
+            const uint32_t at = sh.tmem + ((uint32_t)quarter << 21) + acc * kTile + half;
+#pragma unroll
+            for (int c = 0; c < 128; c += 32) tc_read32(at + c, v + c);
+            tc_read_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) tc_arrive_cluster(peer_addr(smem_u32(&sh.acc_empty[acc]), 0));
+            xent_epilogue<MODE, DT>(a, b0, nb, it, it.row + rank * 128 + quarter * 32 + lane, half, v);
         }
     }
+    __syncwarp();
+    tc_end(&sh);
 }
 
-// Joins a token's blocks to lse and loss; with gradients also its weight and
-// its hidden state, cleared where the token is left out (0 x NaN is not 0 in
-// dweights' sum).  A CTA a token.
+// Joins the blocks of 8 tokens to lse and loss; with gradients also their
+// weights and hidden states, cleared where a token is left out (0 x NaN is not 0
+// in dweights' sum).
 template <int DT, bool GRAD>
 __global__ void __launch_bounds__(256) xent_join_kernel(const __grid_constant__ XentArgs a) {
-    __shared__ float red[8], redm[8];
+    __shared__ float sm[32][8], ss[32][8];
+    __shared__ int counts[8];
     pdl_wait();
-    const long long t = blockIdx.x;
-    float m = -INFINITY;
-    for (long long b = threadIdx.x; b < a.n_blocks; b += blockDim.x) m = fmaxf(m, a.stats[b * a.tokens + t].x);
-    m = warp_max(m);
-    if (threadIdx.x % 32 == 0) redm[threadIdx.x / 32] = m;
+    pdl_launch_dependents();
+    const int j = threadIdx.x % 8, g = threadIdx.x / 8;
+    const long long t0 = (long long)blockIdx.x * 8, t = t0 + j;
+    float m = -INFINITY, s = 0.0f;
+    auto add = [&](float om, float os) {
+        if (os == 0.0f) return;  // an empty half block
+        const float top = fmaxf(m, om);
+        // (a block of -inf or NaN alone has a sum of its own to keep)
+        s = top == -INFINITY ? s + os : s * exp_of(m - top) + os * exp_of(om - top);
+        m = top;
+    };
+    if (t < a.tokens)
+        for (long long b = g; b < 2 * a.n_blocks; b += 32) {
+            const float2 v = a.stats[b * a.tokens + t];
+            add(v.x, v.y);
+        }
+    sm[g][j] = m;
+    ss[g][j] = s;
     __syncthreads();
-    for (int w = 0; w < 8; w++) m = fmaxf(m, redm[w]);
-    float s = 0.0f;
-    for (long long b = threadIdx.x; b < a.n_blocks; b += blockDim.x) {
-        const float2 v = a.stats[b * a.tokens + t];
-        if (v.y != 0.0f) s = fmaf(v.y, expf(v.x - m), s);  // (a NaN sum of a block of NaN is kept)
-    }
-    s = block_sum(s, red);
-    const float lse = m + logf(s);
-    const long long y = load_index(a.targets, a.index_bytes, t);
-    const bool counts = y >= 0 && y < a.vocab;
-    if (threadIdx.x == 0) {
-        if (a.lse) a.lse[t] = lse;
-        if (a.loss) a.loss[t] = counts ? lse - a.z_target[t] : 0.0f;
-        if (GRAD) {
-            const float w = !counts ? 0.0f : a.token_weight ? a.token_weight[t] : 1.0f;
-            a.lse_ws[t] = lse;
-            a.row_weight[t] = w;
-            if (isfinite(w)) atomicMax(a.w_max, __float_as_uint(fabsf(w)));
-        }
-    }
-    if (GRAD)
-        for (long long j = threadIdx.x; j < a.dim; j += blockDim.x)
-            store_f<DT>(a.hidden_used, t * a.dim + j, counts ? load_f<DT>(a.hidden, t * a.hidden_stride + j) : 0.0f);
-}
-
-// Pass 2: G of a window.
-template <int DT>
-__global__ void __launch_bounds__(256) xent_g_kernel(const __grid_constant__ XentArgs a, long long b0) {
-    pdl_wait();
-    const BlockOf b = block_of(a, b0 + blockIdx.x);
-    const int ti = threadIdx.x / 16, tj = threadIdx.x % 16, ge = g_exponent<DT>(a);
-    for (long long t0 = (long long)blockIdx.y * 64; t0 < a.tokens; t0 += (long long)gridDim.y * 64)
-        for (int j0 = 0; j0 < kBlock; j0 += 64) {
-            float acc[4][4] = {};
-            logits_tile<DT>(a, t0, b, j0, acc);
-            for (int i = 0; i < 4; i++) {
-                const long long t = t0 + ti * 4 + i;
-                if (t >= a.tokens) continue;
-                const float w = ldexpf(a.row_weight[t], ge), lse = a.lse_ws[t];
-                const long long y = load_index(a.targets, a.index_bytes, t) - b.first - j0 - tj * 4;
-                for (int j = 0; j < 4; j++) {
-                    const int col = j0 + tj * 4 + j;
-                    float g = 0.0f;
-                    if (col < b.rows && w != 0.0f) g = (expf(acc[i][j] - lse) - (y == j ? 1.0f : 0.0f)) * w;
-                    store_f<DT>(a.g, (t * a.window + blockIdx.x) * kBlock + col, g);
-                }
+    if (g == 0) {
+        for (int k = 1; k < 32; k++) add(sm[k][j], ss[k][j]);
+        const float lse = m + logf(s);
+        bool ok = false;
+        if (t < a.tokens) {
+            const long long y = load_index(a.targets, a.index_bytes, t);
+            ok = y >= 0 && y < a.vocab;
+            if (a.lse) a.lse[t] = lse;
+            if (a.loss) a.loss[t] = ok ? lse - a.z_target[t] : 0.0f;
+            if (GRAD) {
+                const float w = !ok ? 0.0f : a.token_weight ? a.token_weight[t] : 1.0f;
+                a.lse_ws[t] = lse;
+                a.row_weight[t] = w;
+                if (isfinite(w)) atomicMax(a.w_max, __float_as_uint(fabsf(w)));
             }
         }
+        counts[j] = ok;
+    }
+    if (!GRAD) return;
+    __syncthreads();
+    const long long vecs = a.dim / 8;
+    for (int k = 0; k < 8 && t0 + k < a.tokens; k++) {
+        const uint4 *from = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.hidden) + (t0 + k) * a.hidden_stride);
+        uint4 *to = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.hidden_used) + (t0 + k) * a.dim);
+        for (long long i = threadIdx.x; i < vecs; i += blockDim.x) to[i] = counts[k] ? from[i] : make_uint4(0, 0, 0, 0);
+    }
 }
 
-// dhidden's sum over a window of nb blocks.
+// dhidden from the splits' sums.
 template <int DT>
-__global__ void __launch_bounds__(256) xent_dh_kernel(const __grid_constant__ XentArgs a, long long b0, long long nb) {
+__global__ void __launch_bounds__(256) xent_dhidden_join_kernel(const __grid_constant__ XentArgs a) {
     pdl_wait();
-    const long long d0 = (long long)blockIdx.x * 64;
+    pdl_launch_dependents();
     const float undo = ldexpf(1.0f, -g_exponent<DT>(a));
-    const int ti = threadIdx.x / 16, tj = threadIdx.x % 16;
-    for (long long t0 = (long long)blockIdx.y * 64; t0 < a.tokens; t0 += (long long)gridDim.y * 64) {
-        float acc[4][4] = {};
-        for (long long k = 0; k < nb; k++) {
-            const BlockOf b = block_of(a, b0 + k);
-            const char *w = rank_ptr(a.w, a.p, b.piece);
-            tile_product(
-                acc, b.rows,
-                [&](int i, long long v) { return t0 + i < a.tokens ? load_f<DT>(a.g, ((t0 + i) * a.window + k) * kBlock + v) : 0.0f; },
-                [&](int j, long long v) { return d0 + j < a.dim ? load_f<DT>(w, (b.row + v) * a.weight_stride + d0 + j) : 0.0f; });
+    const long long vecs = a.dim / 8, n = a.tokens * vecs;
+    for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (long long)gridDim.x * blockDim.x) {
+        const long long t = i / vecs, d = i % vecs * 8;
+        float v[8] = {};
+        for (int k = 0; k < a.splits; k++) {
+            const float4 *q = reinterpret_cast<const float4 *>(a.dh_part + (k * a.tokens + t) * a.dim + d);
+            const float4 x = q[0], y = q[1];
+            v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w, v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
         }
-        for (int i = 0; i < 4; i++)
-            for (int j = 0; j < 4; j++) {
-                const long long t = t0 + ti * 4 + i, d = d0 + tj * 4 + j;
-                if (t >= a.tokens || d >= a.dim) continue;
-                float v = acc[i][j] * undo + (b0 ? a.dh_acc[t * a.dim + d] : 0.0f);
-                if (b0 + nb < a.n_blocks) a.dh_acc[t * a.dim + d] = v;
-                else store_f<DT>(a.dhidden, t * a.dhidden_stride + d, v);
-            }
-    }
-}
-
-// dweights of a window: a block's 64-row quarter x 64 columns a CTA.
-template <int DT>
-__global__ void __launch_bounds__(256) xent_dw_kernel(const __grid_constant__ XentArgs a, long long b0) {
-    pdl_wait();
-    const long long k = blockIdx.x, d0 = (long long)blockIdx.y * 64;
-    const BlockOf b = block_of(a, b0 + k);
-    const float undo = ldexpf(1.0f, -g_exponent<DT>(a));
-    const int ti = threadIdx.x / 16, tj = threadIdx.x % 16;
-    for (int v0 = 0; v0 < b.rows; v0 += 64) {
-        float acc[4][4] = {};
-        tile_product(
-            acc, a.tokens,
-            [&](int i, long long t) { return load_f<DT>(a.g, (t * a.window + k) * kBlock + v0 + i); },
-            [&](int j, long long t) { return d0 + j < a.dim ? load_f<DT>(a.hidden_used, t * a.dim + d0 + j) : 0.0f; });
-        for (int i = 0; i < 4; i++)
-            for (int j = 0; j < 4; j++) {
-                const int v = v0 + ti * 4 + i;
-                const long long d = d0 + tj * 4 + j;
-                if (v < b.rows && d < a.dim)
-                    store_f<DT>(rank_ptr(a.dw, a.p, b.piece), (b.row + v) * a.dweight_stride + d, acc[i][j] * undo);
-            }
+        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.dhidden) + t * a.dhidden_stride + d) = narrow8<DT>(v, undo);
     }
 }
 
 namespace {
 
 constexpr size_t kWindowBytes = (size_t)256 << 20;  // of G
+constexpr size_t kPairs = 76;                       // pairs of SMs on a GB300: sizes the workspace, not the grid
+
+// cuTensorMapEncodeTiled, from the driver that the runtime has loaded.
+using EncodeTiled = decltype(&cuTensorMapEncodeTiled);
+EncodeTiled encode_tiled() {
+    static const EncodeTiled fn = [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+            found != cudaDriverEntryPointSuccess) {
+            cudaGetLastError();
+            p = nullptr;
+        }
+        return (EncodeTiled)p;
+    }();
+    return fn;
+}
+
+// A map of a rows x cols matrix of 16-bit elements, boxes of 64 x 64; what lies
+// beyond the matrix reads as zero.
+bool make_map(CUtensorMap *m, int dtype, const void *ptr, long long rows, long long cols, long long stride) {
+    const EncodeTiled encode = encode_tiled();
+    if (!encode) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)stride * 2};
+    const cuuint32_t box[2] = {64, 64}, steps[2] = {1, 1};
+    return encode(m, dtype == DT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
+                  const_cast<void *>(ptr), dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int MODE, int DT>
+cudaError_t launch_tiles(const rar_ctx *h, const XentArgs &k, const XentMaps &maps, long long b0, long long nb, cudaStream_t stream) {
+    auto kern = xent_tile_kernel<MODE, DT>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcSmem);
+    if (e != cudaSuccess) return e;
+    const long long pairs = std::min<long long>(xent_items<MODE>(k, nb), h->sm_count / 2);
+    return launch_pdl(kern, dim3((unsigned)(2 * pairs)), dim3(kTcThreads), kTcSmem, stream, k, maps, b0, nb);
+}
 
 void plan_blocks(size_t vocab, int p, XentArgs *k) {
     k->base = (long long)(vocab / p);
@@ -292,7 +507,7 @@ size_t plan(void *base, size_t tokens, size_t dim, size_t vocab, int p, bool gra
     WorkspacePlan w(base);
     plan_blocks(vocab, p, k);
     const size_t n_blocks = (size_t)k->n_blocks;
-    k->stats = w.take<float2>(n_blocks * tokens);
+    k->stats = w.take<float2>(2 * n_blocks * tokens);
     k->z_target = w.take<float>(tokens);
     k->w_max = w.take<unsigned>(1);
     k->window = 0;
@@ -304,7 +519,13 @@ size_t plan(void *base, size_t tokens, size_t dim, size_t vocab, int p, bool gra
         window = std::min(std::max<size_t>(window, 1), n_blocks);
         k->window = (long long)window;
         k->g = w.take<uint16_t>(tokens * window * kBlock);
-        k->dh_acc = w.take<float>(window < n_blocks ? tokens * dim : 0);
+        // few tiles: dhidden's sum over the window is split until there are
+        // about two tiles a pair of SMs
+        const size_t tiles = ((tokens + kTile - 1) / kTile) * ((dim + kTile - 1) / kTile);
+        const size_t splits = std::min(std::max<size_t>(2 * kPairs / std::max<size_t>(tiles, 1), 1), window);
+        k->splits = (int)splits;
+        k->direct = splits == 1;
+        k->dh_part = w.take<float>(window < n_blocks || splits > 1 ? splits * tokens * dim : 0);
     }
     return w.used;
 }
@@ -387,24 +608,51 @@ int vocab_xent(rar_ctx *h, const rar_vocab_xent_args *a, cudaStream_t stream) {
     k.want_dw = a->dweights != nullptr;
     note_op_call(h, a->p, stream);
 
+    k.limits = {h->status, h->opt.timeout_ns ? h->opt.timeout_ns : 2000000000ull};
+
+    XentMaps maps;
+    bool mapped = true;
+    if (k.tokens) {
+        mapped = make_map(&maps.hidden, a->dtype, k.hidden, k.tokens, k.dim, k.hidden_stride);
+        for (int r = 0; r < k.p && mapped; r++) {
+            const long long rows = k.base + (r < k.extra ? 1 : 0);
+            if (rows) mapped = make_map(&maps.w[r], a->dtype, k.w.inl[r], rows, k.dim, k.weight_stride);
+        }
+        if (grad && mapped)
+            mapped = make_map(&maps.hidden_used, a->dtype, k.hidden_used, k.tokens, k.dim, k.dim) &&
+                     make_map(&maps.g, a->dtype, k.g, k.tokens, k.window * kBlock, k.window * kBlock);
+    }
+    if (!mapped) return fail(h, RAR_ECUDA, "rar_vocab_xent: the driver refused a tensor map");
+
     auto run = [&](auto dt) {
         constexpr int DT = decltype(dt)::value;
-        const unsigned ty = (unsigned)std::min<long long>((k.tokens + 63) / 64, 4096);
-        const unsigned dx = (unsigned)((k.dim + 63) / 64);
         cudaError_t e = cudaSuccess;
-        if (k.tokens) {
-            e = launch_pdl(xent_stats_kernel<DT>, dim3((unsigned)k.n_blocks, ty), dim3(256), 0, stream, k);
-            if (e == cudaSuccess)
-                e = launch_pdl(grad ? xent_join_kernel<DT, true> : xent_join_kernel<DT, false>, dim3((unsigned)k.tokens), dim3(256), 0, stream, k);
+        if (!k.tokens) {  // no tokens: the pieces' gradients are zeros
+            for (int r = 0; r < k.p && e == cudaSuccess; r++) {
+                const size_t rows = (size_t)(k.base + (r < k.extra ? 1 : 0));
+                if (rows) e = cudaMemset2DAsync(k.dw.inl[r], (size_t)k.dweight_stride * 2, 0, (size_t)k.dim * 2, rows, stream);
+            }
+            return e;
         }
+        e = launch_tiles<XENT_STATS, DT>(h, k, maps, 0, k.n_blocks, stream);
+        if (e == cudaSuccess)
+            e = launch_pdl(grad ? xent_join_kernel<DT, true> : xent_join_kernel<DT, false>, dim3((unsigned)((k.tokens + 7) / 8)),
+                           dim3(256), 0, stream, k);
         if (!grad) return e;
         for (long long b0 = 0; b0 < k.n_blocks && e == cudaSuccess; b0 += k.window) {
             const long long nb = std::min(k.window, k.n_blocks - b0);
-            if (k.tokens) e = launch_pdl(xent_g_kernel<DT>, dim3((unsigned)nb, ty), dim3(256), 0, stream, k, b0);
-            if (e == cudaSuccess && k.dhidden && k.tokens)
-                e = launch_pdl(xent_dh_kernel<DT>, dim3(dx, ty), dim3(256), 0, stream, k, b0, nb);
-            if (e == cudaSuccess && k.want_dw)
-                e = launch_pdl(xent_dw_kernel<DT>, dim3((unsigned)nb, dx), dim3(256), 0, stream, k, b0);
+            e = launch_tiles<XENT_G, DT>(h, k, maps, b0, nb, stream);
+            if (e == cudaSuccess && k.dhidden) {
+                XentArgs kw = k;
+                kw.splits = (int)std::min<long long>(k.splits, nb);
+                e = launch_tiles<XENT_DHIDDEN, DT>(h, kw, maps, b0, nb, stream);
+            }
+            if (e == cudaSuccess && k.want_dw) e = launch_tiles<XENT_DWEIGHT, DT>(h, k, maps, b0, nb, stream);
+        }
+        if (e == cudaSuccess && k.dhidden && k.splits > 1) {
+            const long long n = k.tokens * (k.dim / 8);
+            const unsigned grid = (unsigned)std::min<long long>((n + 255) / 256, h->sm_count * 8);
+            e = launch_pdl(xent_dhidden_join_kernel<DT>, dim3(grid), dim3(256), 0, stream, k);
         }
         return e;
     };
