@@ -30,6 +30,22 @@ __device__ __forceinline__ void store_f(void *base, long long i, float f) {
     store_elem<DT>(static_cast<char *>(base), i, narrow<DT>(f));
 }
 
+// Two and eight 16-bit values, rounded to nearest even.
+template <int DT>
+__device__ __forceinline__ uint32_t narrow2(float lo, float hi) {
+    if constexpr (DT == DT_BF16) {
+        __nv_bfloat162 r = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<uint32_t *>(&r);
+    } else {
+        __half2 r = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<uint32_t *>(&r);
+    }
+}
+template <int DT>
+__device__ __forceinline__ uint4 narrow8(const float *v) {
+    return make_uint4(narrow2<DT>(v[0], v[1]), narrow2<DT>(v[2], v[3]), narrow2<DT>(v[4], v[5]), narrow2<DT>(v[6], v[7]));
+}
+
 // An index array of 32- or 64-bit signed integers.
 __device__ __forceinline__ long long load_index(const void *base, int bytes, long long i) {
     return bytes == 8 ? __ldg(static_cast<const long long *>(base) + i) : (long long)__ldg(static_cast<const int *>(base) + i);
@@ -40,29 +56,43 @@ __device__ __forceinline__ float warp_sum(float v) {
     for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
     return v;
 }
-__device__ __forceinline__ float warp_max(float v) {  // NaN is passed over
-#pragma unroll
-    for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
-    return v;
-}
-// Sum over the block in a fixed order; `red` holds a float per warp.  Every
-// thread gets the result, and may reuse `red` after its next barrier.
-__device__ __forceinline__ float block_sum(float v, float *red) {
-    v = warp_sum(v);
-    if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = v;
-    __syncthreads();
-    float t = 0.0f;
-    for (int w = 0; w < (int)blockDim.x / 32; w++) t += red[w];
-    return t;
-}
-
 // The scale of a group whose largest magnitude is amax: the e4m3 range
 // [-448, 448] spans the group; never 0, infinite or NaN.
 __device__ __forceinline__ float scale_of(float amax) {
     return fmaxf(__fdiv_rn(fminf(amax, 3.402823466e38f), 448.0f), 1.175494351e-38f);
 }
-__device__ __forceinline__ uint8_t to_e4m3(float v) {
-    return (uint8_t)__nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3);
+// Codes of values divided by a scale.  The product with the reciprocal,
+// corrected once by its remainder, is the correctly rounded quotient (Markstein
+// 1990): the scale and its reciprocal are normal numbers, and where the
+// remainder underflows the quotient is far below the smallest code (or the
+// scale is 2^-126 and the product exact).  It is inf or NaN where the value is.
+struct CodeOf {
+    float scale, inv;
+    __device__ __forceinline__ explicit CodeOf(float s) {
+        scale = s;
+        inv = __fdiv_rn(1.0f, s);
+    }
+    __device__ __forceinline__ float quotient(float v) const {
+        const float q = v * inv, r = fmaf(-q, scale, v), c = fmaf(r, inv, q);
+        return fabsf(q) <= 512.0f ? c : q;  // (the remainder of an infinity is NaN)
+    }
+    __device__ __forceinline__ uint8_t one(float v) const {
+        return (uint8_t)__nv_cvt_float_to_fp8(quotient(v), __NV_SATFINITE, __NV_E4M3);
+    }
+    __device__ __forceinline__ uint32_t four(const float *v) const {
+        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(quotient(v[0]), quotient(v[1])), __NV_SATFINITE, __NV_E4M3);
+        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(quotient(v[2]), quotient(v[3])), __NV_SATFINITE, __NV_E4M3);
+        return lo | hi << 16;
+    }
+};
+
+// The codes of 4 or 8 values, in one store.
+__device__ __forceinline__ void store_codes(uint8_t *to, const float (&v)[4], float scale) {
+    *reinterpret_cast<uint32_t *>(to) = CodeOf(scale).four(v);
+}
+__device__ __forceinline__ void store_codes(uint8_t *to, const float (&v)[8], float scale) {
+    const CodeOf c(scale);
+    *reinterpret_cast<uint2 *>(to) = make_uint2(c.four(v), c.four(v + 4));
 }
 
 // Calls f(IntC<dtype>{}) for a floating dtype.

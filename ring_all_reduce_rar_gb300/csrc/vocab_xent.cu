@@ -179,20 +179,13 @@ __device__ __forceinline__ float exp_of(float x) {  // ex2.approx: 2 units in th
     asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x * 1.4426950408889634f));
     return r;
 }
+// Eight values times a power of two, rounded.
 template <int DT>
-__device__ __forceinline__ uint32_t narrow2(float lo, float hi) {
-    if constexpr (DT == DT_BF16) {
-        __nv_bfloat162 r = __floats2bfloat162_rn(lo, hi);
-        return *reinterpret_cast<uint32_t *>(&r);
-    } else {
-        __half2 r = __floats2half2_rn(lo, hi);
-        return *reinterpret_cast<uint32_t *>(&r);
-    }
-}
-template <int DT>
-__device__ __forceinline__ uint4 narrow8(const float *v, float scale) {
-    return make_uint4(narrow2<DT>(v[0] * scale, v[1] * scale), narrow2<DT>(v[2] * scale, v[3] * scale),
-                      narrow2<DT>(v[4] * scale, v[5] * scale), narrow2<DT>(v[6] * scale, v[7] * scale));
+__device__ __forceinline__ uint4 narrow8_scaled(const float *v, float scale) {
+    float f[8];
+#pragma unroll
+    for (int e = 0; e < 8; e++) f[e] = v[e] * scale;
+    return narrow8<DT>(f);
 }
 
 // A thread's part of a finished tile: one row, 128 columns from `half`.
@@ -237,7 +230,7 @@ __device__ __forceinline__ void xent_epilogue(const XentArgs &a, long long b0, l
             v[c] = c < cols && w != 0.0f ? p * w : 0.0f;
         }
 #pragma unroll
-        for (int c = 0; c < 128; c += 8) out[c / 8] = narrow8<DT>(v + c, 1.0f);
+        for (int c = 0; c < 128; c += 8) out[c / 8] = narrow8<DT>(v + c);
     } else if constexpr (MODE == XENT_DHIDDEN) {
         if (row >= a.tokens) return;
         const float undo = ldexpf(1.0f, -g_exponent<DT>(a));
@@ -254,7 +247,7 @@ __device__ __forceinline__ void xent_epilogue(const XentArgs &a, long long b0, l
                 v[c + 4] += y.x, v[c + 5] += y.y, v[c + 6] += y.z, v[c + 7] += y.w;
             }
             if (last && a.direct) {
-                *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.dhidden) + row * a.dhidden_stride + d) = narrow8<DT>(v + c, undo);
+                *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.dhidden) + row * a.dhidden_stride + d) = narrow8_scaled<DT>(v + c, undo);
             } else {
                 q[0] = make_float4(v[c], v[c + 1], v[c + 2], v[c + 3]);
                 q[1] = make_float4(v[c + 4], v[c + 5], v[c + 6], v[c + 7]);
@@ -269,7 +262,7 @@ __device__ __forceinline__ void xent_epilogue(const XentArgs &a, long long b0, l
 #pragma unroll
         for (int c = 0; c < 128; c += 8) {
             const long long d = it.col + half + c;
-            if (d < a.dim) *reinterpret_cast<uint4 *>(out + d) = narrow8<DT>(v + c, undo);
+            if (d < a.dim) *reinterpret_cast<uint4 *>(out + d) = narrow8_scaled<DT>(v + c, undo);
         }
     }
 }
@@ -449,7 +442,7 @@ __global__ void __launch_bounds__(256) xent_dhidden_join_kernel(const __grid_con
             const float4 x = q[0], y = q[1];
             v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w, v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
         }
-        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.dhidden) + t * a.dhidden_stride + d) = narrow8<DT>(v, undo);
+        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.dhidden) + t * a.dhidden_stride + d) = narrow8_scaled<DT>(v, undo);
     }
 }
 
