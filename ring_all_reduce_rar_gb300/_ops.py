@@ -11,6 +11,8 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import functools
+import struct
+from array import array
 from typing import NamedTuple, Optional
 
 from . import _abi
@@ -74,6 +76,16 @@ class EmbeddingGradArgs(ctypes.Structure):
                 ("scale", _f32), ("accumulate", _i32), ("workspace", _vp), ("workspace_bytes", _sz)]
 
 
+def _packer(cls):
+    """struct.Struct of a ctypes structure: filling one costs a tenth of
+    setting its fields."""
+    codes = {_vp: "P", _sz: "N", _i32: "i", _f32: "f"}
+    fmt = "@" + "".join(codes[kind] for _, kind in cls._fields_)
+    packer = struct.Struct(fmt + "0P")
+    assert packer.size == ctypes.sizeof(cls)
+    return packer.pack
+
+
 class AddRmsNorm(NamedTuple):
     """Results of add_rmsnorm; those that were not asked for are None."""
     sum: torch.Tensor
@@ -91,13 +103,15 @@ class VocabXent(NamedTuple):
     dweights: Optional[list]
 
 
+_pack_norm, _pack_norm_grad, _pack_xent, _pack_embed, _pack_embed_grad = map(
+    _packer, (RmsNormArgs, RmsNormGradArgs, VocabXentArgs, EmbeddingArgs, EmbeddingGradArgs))
+
+
 def declare(lib) -> None:
-    """Argument types of the operators' C functions."""
-    for name, args in (("rar_add_rmsnorm", RmsNormArgs), ("rar_add_rmsnorm_grad", RmsNormGradArgs),
-                       ("rar_vocab_xent", VocabXentArgs), ("rar_embedding", EmbeddingArgs),
-                       ("rar_embedding_grad", EmbeddingGradArgs)):
+    """Argument types of the operators' C functions; their structs go as packed bytes or by reference."""
+    for name in ("rar_add_rmsnorm", "rar_add_rmsnorm_grad", "rar_vocab_xent", "rar_embedding", "rar_embedding_grad"):
         f = getattr(lib, name)
-        f.argtypes = [_vp, ctypes.POINTER(args), _vp]
+        f.argtypes = [_vp, _vp, _vp]
         f.restype = _i32
     for name, argtypes in (("rar_add_rmsnorm_grad_workspace", [_sz, _sz]),
                            ("rar_vocab_xent_workspace", [_sz, _sz, _sz, _i32, _i32]),
@@ -107,66 +121,90 @@ def declare(lib) -> None:
         f.restype = _sz
 
 
-def _matrix(name, t, rows=None, cols=None, like=None):
-    """(pointer, row stride) of a 2-D CUDA tensor with contiguous rows."""
-    if t.dim() != 2:
-        raise ValueError(f"{name} must have two dimensions")
-    shape = t.shape
-    if (rows is not None and shape[0] != rows) or (cols is not None and shape[1] != cols):
-        raise ValueError(f"{name} must be {rows} x {cols}, got {shape[0]} x {shape[1]}")
-    if like is not None and (t.dtype != like.dtype or t.device != like.device):
-        raise ValueError(f"{name} must share dtype and device with the other matrices")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    stride = t.stride()
-    if shape[1] > 1 and stride[1] != 1:
+def _stride(name, t):
+    """Row stride of a matrix whose rows are contiguous."""
+    if t.is_contiguous():
+        return t.shape[1]
+    st, (rows, cols) = t.stride(), t.shape
+    if cols > 1 and st[1] != 1:
         raise ValueError(f"{name} must have contiguous rows")
-    return t.data_ptr(), (stride[0] if shape[0] > 1 else shape[1])
+    return st[0] if rows > 1 else cols
+
+
+def _matrix(name, t, shape, dtype, device):
+    """(pointer, row stride) of a CUDA matrix of this shape."""
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != device:
+        raise ValueError(f"{name} must be a {tuple(shape)} {dtype} tensor on device {device}, got {tuple(t.shape)} "
+                         f"{t.dtype} on {t.device}")
+    return t.data_ptr(), _stride(name, t)
 
 
 def _vector(name, t, n, dtype, device):
-    if t.dim() != 1 or t.shape[0] != n or t.dtype != dtype or t.device != device or (n > 1 and t.stride(0) != 1):
-        raise ValueError(f"{name} must be a contiguous vector of {n} {dtype} values on {device}")
+    if t.shape != (n,) or t.dtype is not dtype or t.get_device() != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous vector of {n} {dtype} values on device {device}")
     return t.data_ptr()
 
 
-def _indices(name, t, device):
-    sizes = _index_bytes()
-    if t.dim() != 1 or t.dtype not in sizes or t.device != device or (t.shape[0] > 1 and t.stride(0) != 1):
-        raise ValueError(f"{name} must be a contiguous vector of int32 or int64 values on {device}")
-    return t.data_ptr(), sizes[t.dtype], t.shape[0]
+def _indices(name, t, n, device):
+    size = _index_bytes().get(t.dtype)
+    if size is None or t.dim() != 1 or (n is not None and t.shape[0] != n) or t.get_device() != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous vector of int32 or int64 values on device {device}"
+                         + (f", one for each of {n} rows" if n is not None else ""))
+    return t.data_ptr(), size
 
 
-def _code(t):
+def _first(name, t):
+    """(dtype, its code, device index) that a call's matrices share."""
     code = _codes().get(t.dtype)
+    device = t.get_device()
     if code is None:
         raise ValueError(f"unsupported dtype {t.dtype}")
-    return code
+    if device < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions")
+    return t.dtype, code, device
 
 
-def _pieces(name, pieces, like=None):
+def _matrices(name, tensors, dtype, device, shapes):
+    """(array of pointers, row stride) of matrices with one row stride, which
+    those of a single row do not decide."""
+    ptrs, stride = array("Q"), 0
+    for r, t in enumerate(tensors):
+        if t.shape != shapes[r] or t.dtype is not dtype or t.get_device() != device:
+            raise ValueError(f"{name} {r} must be a {tuple(shapes[r])} {dtype} tensor on device {device}, got "
+                             f"{tuple(t.shape)} {t.dtype} on {t.device}")
+        ptrs.append(t.data_ptr())
+        if t.is_contiguous():
+            st = shapes[r][1]
+        else:
+            st = _stride(f"{name} {r}", t)
+        if st != stride and shapes[r][0] > 1:
+            if stride:
+                raise ValueError(f"{name}s must share their row stride")
+            stride = st
+    return ptrs, stride
+
+
+def _pieces(name, pieces, dtype, device):
     """(pointer array, row stride, p, vocab, dim) of a matrix in pieces by
     chunk_bounds: the first vocab mod p pieces are one row longer."""
     p = len(pieces)
-    if p < 1:
-        raise ValueError(f"{name}: need at least one piece")
-    first = pieces[0]
-    like = first if like is None else like
-    if first.dim() != 2:
-        raise ValueError(f"a piece of {name} must have two dimensions")
-    dim = first.shape[1]
-    vocab = sum(t.shape[0] for t in pieces)
+    dim = pieces[0].shape[-1]
+    vocab = 0
+    for t in pieces:
+        vocab += t.shape[0]
     base, extra = divmod(vocab, p)
-    ptrs, stride = (_vp * p)(), 0
-    for r, t in enumerate(pieces):
-        rows = base + (r < extra)
-        ptr, st = _matrix(f"piece {r} of {name}", t, rows, dim, like)
-        ptrs[r] = ptr
-        if rows > 1:
-            if stride and st != stride:
-                raise ValueError(f"the pieces of {name} must share their row stride")
-            stride = st
+    ptrs, stride = _matrices(name, pieces, dtype, device, [(base + 1, dim)] * extra + [(base, dim)] * (p - extra))
     return ptrs, stride, p, vocab, dim
+
+
+@functools.lru_cache(maxsize=None)
+def _current_stream():
+    """Raw handle of a device's current stream."""
+    torch = _torch()
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw or (lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
 @contextlib.contextmanager
@@ -180,14 +218,14 @@ def _external(stream, device):
 def _on_stream(stream, device, body):
     """body(raw stream), with results allocated on that stream."""
     if stream is None:
-        return body(_torch().cuda.current_stream(device).cuda_stream)
+        return body(_current_stream()(device))
     with _external(stream, device) as raw:
         return body(raw)
 
 
-def _workspace(nbytes, device):
-    torch = _torch()
-    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+def _check(handle, rc):
+    if rc:
+        _abi._check(handle, rc)
 
 
 def rar_add_rmsnorm(handle, parts, weight=None, residual=None, eps=1e-6, quant_group=None, keep_out=None,
@@ -201,41 +239,32 @@ def rar_add_rmsnorm(handle, parts, weight=None, residual=None, eps=1e-6, quant_g
     if len(parts) < 1:
         raise ValueError("need at least one part")
     x = parts[0]
-    if x.dim() != 2:
-        raise ValueError("a part must have two dimensions")
-    rows, dim = x.shape
+    dtype, code, device = _first("a part", x)
+    shape = x.shape
+    rows, dim = shape
     p = len(parts)
-    a = RmsNormArgs()
-    a.p, a.dtype, a.rows, a.dim, a.eps = p, _code(x), rows, dim, eps
-    ptrs = (_vp * p)()
-    stride = 0
-    for r, t in enumerate(parts):
-        ptrs[r], st = _matrix(f"part {r}", t, rows, dim, x)
-        if r and st != stride:
-            raise ValueError("the parts must share their row stride")
-        stride = st
-    a.parts, a.part_stride = ctypes.addressof(ptrs), stride
-    device = x.device
-    if residual is not None:
-        a.residual, a.residual_stride = _matrix("residual", residual, rows, dim, x)
-    if weight is not None:
-        a.weight = _vector("weight", weight, dim, x.dtype, device)
-    want_out = quant_group is None or bool(keep_out)
+    ptrs, stride = _matrices("part", parts, dtype, device, [shape] * p)
+    res, res_stride = _matrix("residual", residual, shape, dtype, device) if residual is not None else (0, 0)
+    w = _vector("weight", weight, dim, dtype, device) if weight is not None else 0
+    group = quant_group or 0
+    if group < 0:
+        raise ValueError("quant_group must be None, 0 or positive")
 
     def body(raw):
-        s = torch.empty((rows, dim), dtype=x.dtype, device=device)
-        rstd = torch.empty(rows, dtype=torch.float32, device=device)
-        a.sum, a.rstd = s.data_ptr(), rstd.data_ptr()
+        s = torch.empty(shape, dtype=dtype, device=x.device)
+        rstd = torch.empty(rows, dtype=torch.float32, device=x.device)
         out = out8 = scales = None
-        if want_out:
-            out = torch.empty((rows, dim), dtype=x.dtype, device=device)
-            a.out = out.data_ptr()
+        out_p = out8_p = scales_p = 0
+        if quant_group is None or keep_out:
+            out = torch.empty_like(s)
+            out_p = out.data_ptr()
         if quant_group is not None:
-            groups = -(-dim // quant_group) if quant_group else 1
-            out8 = torch.empty((rows, dim), dtype=torch.float8_e4m3fn, device=device)
-            scales = torch.empty((rows, groups), dtype=torch.float32, device=device)
-            a.out8, a.scales, a.group = out8.data_ptr(), scales.data_ptr(), quant_group
-        _abi._check(handle, _abi.load_library().rar_add_rmsnorm(handle, ctypes.byref(a), raw))
+            out8 = torch.empty_like(s, dtype=torch.float8_e4m3fn)
+            scales = torch.empty((rows, -(-dim // group) if group else 1), dtype=torch.float32, device=x.device)
+            out8_p, scales_p = out8.data_ptr(), scales.data_ptr()
+        args = _pack_norm(ptrs.buffer_info()[0], p, code, rows, dim, stride, res, res_stride, w, eps, s.data_ptr(), 0,
+                          out_p, 0, rstd.data_ptr(), out8_p, 0, scales_p, group)
+        _check(handle, _abi.load_library().rar_add_rmsnorm(handle, args, raw))
         return AddRmsNorm(s, rstd, out, out8, scales)
 
     return _on_stream(stream, device, body)
@@ -246,30 +275,24 @@ def rar_add_rmsnorm_grad(handle, dout, sum, rstd, weight=None, dsum=None, stream
     and of every part alike.  sum and rstd are its results; dsum is the
     gradient of its sum, if that is used elsewhere."""
     torch = _torch()
-    if dout.dim() != 2:
-        raise ValueError("dout must have two dimensions")
-    rows, dim = dout.shape
-    device = dout.device
-    a = RmsNormGradArgs()
-    a.dtype, a.rows, a.dim = _code(dout), rows, dim
-    a.dout, a.dout_stride = _matrix("dout", dout)
-    a.sum, a.sum_stride = _matrix("sum", sum, rows, dim, dout)
-    a.rstd = _vector("rstd", rstd, rows, torch.float32, device)
-    if dsum is not None:
-        a.dsum, a.dsum_stride = _matrix("dsum", dsum, rows, dim, dout)
-    if weight is not None:
-        a.weight = _vector("weight", weight, dim, dout.dtype, device)
+    dtype, code, device = _first("dout", dout)
+    shape = dout.shape
+    rows, dim = shape
+    x, x_stride = _matrix("sum", sum, shape, dtype, device)
+    r = _vector("rstd", rstd, rows, torch.float32, device)
+    ds, ds_stride = _matrix("dsum", dsum, shape, dtype, device) if dsum is not None else (0, 0)
+    w = _vector("weight", weight, dim, dtype, device) if weight is not None else 0
+    dout_stride = _stride("dout", dout)
     lib = _abi.load_library()
     need = lib.rar_add_rmsnorm_grad_workspace(rows, dim)
 
     def body(raw):
-        dx = torch.empty((rows, dim), dtype=dout.dtype, device=device)
-        dweight = torch.empty(dim, dtype=dout.dtype, device=device)
-        ws = _workspace(need, device)
-        a.dx, a.dweight = dx.data_ptr(), dweight.data_ptr()
-        if ws is not None:
-            a.workspace, a.workspace_bytes = ws.data_ptr(), need
-        _abi._check(handle, lib.rar_add_rmsnorm_grad(handle, ctypes.byref(a), raw))
+        dx = torch.empty(shape, dtype=dtype, device=dout.device)
+        dweight = torch.empty(dim, dtype=dtype, device=dout.device)
+        ws = torch.empty(need, dtype=torch.uint8, device=dout.device)
+        args = _pack_norm_grad(code, rows, dim, dout.data_ptr(), dout_stride, ds, ds_stride, x, x_stride, r, w,
+                               dx.data_ptr(), 0, dweight.data_ptr(), ws.data_ptr(), need)
+        _check(handle, lib.rar_add_rmsnorm_grad(handle, args, raw))
         return dx, dweight
 
     return _on_stream(stream, device, body)
@@ -282,36 +305,32 @@ def rar_vocab_xent(handle, hidden, weights, targets, token_weight=None, grad=Fal
     token out.  grad=True also returns the gradients of
     sum(token_weight * loss) for hidden and for every piece."""
     torch = _torch()
-    ptrs, wstride, p, vocab, dim = _pieces("weights", weights, hidden)
-    device = hidden.device
-    a = VocabXentArgs()
-    a.hidden, a.hidden_stride = _matrix("hidden", hidden, None, dim)
+    if len(weights) < 1:
+        raise ValueError("need at least one piece")
+    dtype, code, device = _first("hidden", hidden)
+    ptrs, wstride, p, vocab, dim = _pieces("weight piece", weights, dtype, device)
     tokens = hidden.shape[0]
-    a.weights, a.weight_stride, a.p, a.dtype = ctypes.addressof(ptrs), wstride, p, _code(hidden)
-    a.tokens, a.dim, a.vocab = tokens, dim, vocab
-    a.targets, a.index_bytes, n = _indices("targets", targets, device)
-    if n != tokens:
-        raise ValueError("targets must hold one index per token")
-    if token_weight is not None:
-        a.token_weight = _vector("token_weight", token_weight, tokens, torch.float32, device)
+    hid, hid_stride = _matrix("hidden", hidden, (tokens, dim), dtype, device)
+    tgt, index_bytes = _indices("targets", targets, tokens, device)
+    tw = _vector("token_weight", token_weight, tokens, torch.float32, device) if token_weight is not None else 0
     lib = _abi.load_library()
     need = lib.rar_vocab_xent_workspace(tokens, dim, vocab, p, 1 if grad else 0)
 
     def body(raw):
-        stats = torch.empty((2, tokens), dtype=torch.float32, device=device)
-        loss, lse = stats.unbind(0)
-        a.loss, a.lse = loss.data_ptr(), lse.data_ptr()
+        loss = torch.empty(tokens, dtype=torch.float32, device=hidden.device)
+        lse = torch.empty_like(loss)
+        ws = torch.empty(need, dtype=torch.uint8, device=hidden.device)
         dhidden = dweights = None
+        dh_p = dw_p = 0
         if grad:
-            dhidden = torch.empty((tokens, dim), dtype=hidden.dtype, device=device)
-            whole = torch.empty((vocab, dim), dtype=hidden.dtype, device=device)
+            dhidden = torch.empty((tokens, dim), dtype=dtype, device=hidden.device)
+            whole = torch.empty((vocab, dim), dtype=dtype, device=hidden.device)
             dweights = list(whole.split([t.shape[0] for t in weights]))
-            dptrs = (_vp * p)(*[t.data_ptr() for t in dweights])
-            a.dhidden, a.dweights = dhidden.data_ptr(), ctypes.addressof(dptrs)
-        ws = _workspace(need, device)
-        if ws is not None:
-            a.workspace, a.workspace_bytes = ws.data_ptr(), need
-        _abi._check(handle, lib.rar_vocab_xent(handle, ctypes.byref(a), raw))
+            dptrs = array("Q", [t.data_ptr() for t in dweights])
+            dh_p, dw_p = dhidden.data_ptr(), dptrs.buffer_info()[0]
+        args = _pack_xent(hid, hid_stride, ptrs.buffer_info()[0], wstride, p, code, tokens, dim, vocab, tgt, index_bytes,
+                          tw, loss.data_ptr(), lse.data_ptr(), dh_p, 0, dw_p, 0, ws.data_ptr(), need)
+        _check(handle, lib.rar_vocab_xent(handle, args, raw))
         return VocabXent(loss, lse, dhidden, dweights)
 
     return _on_stream(stream, device, body)
@@ -321,18 +340,18 @@ def rar_embedding(handle, tables, tokens, scale=1.0, stream=None):
     """scale x rows of a table in p pieces, one for each token; zeros for a
     token outside the vocabulary (see rar_embedding in rar.h)."""
     torch = _torch()
-    ptrs, stride, p, vocab, dim = _pieces("tables", tables)
+    if len(tables) < 1:
+        raise ValueError("need at least one piece")
     first = tables[0]
-    device = first.device
-    a = EmbeddingArgs()
-    a.tables, a.table_stride, a.p, a.dtype = ctypes.addressof(ptrs), stride, p, _code(first)
-    a.vocab, a.dim, a.scale = vocab, dim, scale
-    a.tokens, a.index_bytes, a.n_tokens = _indices("tokens", tokens, device)
+    dtype, code, device = _first("a table piece", first)
+    ptrs, stride, p, vocab, dim = _pieces("table piece", tables, dtype, device)
+    tok, index_bytes = _indices("tokens", tokens, None, device)
+    n = tokens.shape[0]
 
     def body(raw):
-        out = torch.empty((tokens.shape[0], dim), dtype=first.dtype, device=device)
-        a.out = out.data_ptr()
-        _abi._check(handle, _abi.load_library().rar_embedding(handle, ctypes.byref(a), raw))
+        out = torch.empty((n, dim), dtype=dtype, device=first.device)
+        args = _pack_embed(ptrs.buffer_info()[0], stride, p, code, vocab, dim, tok, index_bytes, n, scale, out.data_ptr(), 0)
+        _check(handle, _abi.load_library().rar_embedding(handle, args, raw))
         return out
 
     return _on_stream(stream, device, body)
@@ -341,23 +360,22 @@ def rar_embedding(handle, tables, tokens, scale=1.0, stream=None):
 def rar_embedding_grad(handle, dout, tokens, dtables, scale=1.0, accumulate=False, stream=None):
     """Gradient of rar_embedding for its table, into the p pieces `dtables`:
     added to them with accumulate=True, else written whole.  Returns dtables."""
-    ptrs, stride, p, vocab, dim = _pieces("dtables", dtables, dout)
-    device = dout.device
-    a = EmbeddingGradArgs()
-    a.dout, a.dout_stride = _matrix("dout", dout, None, dim)
-    a.tokens, a.index_bytes, a.n_tokens = _indices("tokens", tokens, device)
-    if dout.shape[0] != tokens.shape[0]:
-        raise ValueError("dout must have one row per token")
-    a.dtables, a.dtable_stride, a.p, a.dtype = ctypes.addressof(ptrs), stride, p, _code(dout)
-    a.vocab, a.dim, a.scale, a.accumulate = vocab, dim, scale, 1 if accumulate else 0
+    torch = _torch()
+    if len(dtables) < 1:
+        raise ValueError("need at least one piece")
+    dtype, code, device = _first("dout", dout)
+    ptrs, stride, p, vocab, dim = _pieces("gradient piece", dtables, dtype, device)
+    n = dout.shape[0]
+    do, do_stride = _matrix("dout", dout, (n, dim), dtype, device)
+    tok, index_bytes = _indices("tokens", tokens, n, device)
     lib = _abi.load_library()
-    need = lib.rar_embedding_grad_workspace(tokens.shape[0], vocab, dim)
+    need = lib.rar_embedding_grad_workspace(n, vocab, dim)
 
     def body(raw):
-        ws = _workspace(need, device)
-        if ws is not None:
-            a.workspace, a.workspace_bytes = ws.data_ptr(), need
-        _abi._check(handle, lib.rar_embedding_grad(handle, ctypes.byref(a), raw))
+        ws = torch.empty(need, dtype=torch.uint8, device=dout.device)
+        args = _pack_embed_grad(do, do_stride, tok, index_bytes, n, ptrs.buffer_info()[0], stride, p, code, vocab, dim,
+                                scale, 1 if accumulate else 0, ws.data_ptr(), need)
+        _check(handle, lib.rar_embedding_grad(handle, args, raw))
         return dtables
 
     return _on_stream(stream, device, body)
