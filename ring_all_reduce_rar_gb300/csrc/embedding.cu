@@ -6,6 +6,9 @@
 //                of dout[t]   (+ what dtables[v] held, with accumulate)
 //
 // Bound by memory: a read and a write an element.
+#include <algorithm>
+#include <utility>
+
 #include "op_elem.cuh"
 #include "op_host.h"
 
@@ -24,53 +27,375 @@ struct EmbedArgs {
     int accumulate;
 };
 
-// Row v of a table in pieces (chunk_bounds over the vocabulary).
-__device__ __forceinline__ char *table_row(const EmbedArgs &a, long long v, int elem_size) {
-    const long long base = a.vocab / a.p, extra = a.vocab % a.p;
-    const int r = chunk_of(v, base, extra);
-    return rank_ptr(a.pieces, a.p, r) + (v - chunk_start(r, base, extra)) * a.table_stride * elem_size;
+// Row v of a table in pieces.
+__device__ __forceinline__ char *table_row(const EmbedArgs &a, const Chunks &c, long long v, int elem_size) {
+    const int r = c.of(v);
+    return rank_ptr(a.pieces, a.p, r) + (v - chunk_start(r, c.base, c.extra)) * a.table_stride * elem_size;
 }
 
-template <int DT>
+// The lookup: the out matrix as one run of 16-byte vectors (VEC) or single elements,
+// U of them a thread with their loads in flight together.
+template <int DT, bool VEC, int U>
 __global__ void __launch_bounds__(256) embedding_kernel(const __grid_constant__ EmbedArgs a) {
+    constexpr int VE = VEC ? RowBits<DT>::VE : 1, EB = ElemInfo<DT>::bytes;
     pdl_wait();
-    for (long long t = blockIdx.x; t < a.n_tokens; t += gridDim.x) {
-        const long long v = load_index(a.tokens, a.index_bytes, t);
-        const bool valid = v >= 0 && v < a.vocab;
-        const char *row = valid ? table_row(a, v, ElemInfo<DT>::bytes) : nullptr;
-        for (long long j = threadIdx.x; j < a.dim; j += blockDim.x)
-            store_f<DT>(a.out, t * a.row_stride + j, valid ? load_f<DT>(row, j) * a.scale : 0.0f);
+    pdl_launch_dependents();
+    const Chunks chunks(a.vocab, a.p);
+    const long long per_row = a.dim / VE, total = a.n_tokens * per_row;
+    const long long i0 = (long long)blockIdx.x * (256 * U) + threadIdx.x;
+    const char *from[U];
+    long long t[U];
+    int j[U];
+    bool has[U];
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+        const long long i = i0 + u * 256;
+        has[u] = i < total;
+        t[u] = total < 0x7FFFFFFF ? (long long)((uint32_t)i / (uint32_t)per_row) : i / per_row;
+        j[u] = (int)(i - t[u] * per_row);
+        const long long v = has[u] ? load_index(a.tokens, a.index_bytes, t[u]) : -1;
+        from[u] = v >= 0 && v < a.vocab ? table_row(a, chunks, v, EB) : nullptr;
+    }
+    if constexpr (VEC) {
+        RowBits<DT> w[U];
+#pragma unroll
+        for (int u = 0; u < U; u++) w[u].load(from[u], j[u], from[u] != nullptr);
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+            float f[VE];
+#pragma unroll
+            for (int e = 0; e < VE; e++) f[e] = w[u].get(e) * a.scale;
+            if (!from[u])  // (0 x an infinite scale)
+#pragma unroll
+                for (int e = 0; e < VE; e++) f[e] = 0.0f;
+            if (has[u]) store_vec<DT>(static_cast<char *>(a.out) + t[u] * a.row_stride * EB, j[u], f);
+        }
+    } else {
+        uint32_t w[U];
+#pragma unroll
+        for (int u = 0; u < U; u++) w[u] = from[u] ? load_elem<DT>(from[u], j[u]) : 0u;
+#pragma unroll
+        for (int u = 0; u < U; u++)
+            if (has[u]) store_f<DT>(a.out, t[u] * a.row_stride + j[u], from[u] ? widen<DT>(w[u]) * a.scale : 0.0f);
     }
 }
 
-// A CTA per row of the table looks through all tokens.
-template <int DT>
-__global__ void __launch_bounds__(256) embedding_grad_kernel(const __grid_constant__ EmbedArgs a) {
-    pdl_wait();
-    for (long long v = blockIdx.x; v < a.vocab; v += gridDim.x) {
-        char *row = table_row(a, v, ElemInfo<DT>::bytes);
-        for (long long j0 = 0; j0 < a.dim; j0 += blockDim.x) {
-            const long long j = j0 + threadIdx.x;
-            float sum = 0.0f;
-            bool any = false;
-            for (long long t0 = 0; t0 < a.n_tokens; t0 += blockDim.x) {
-                __shared__ unsigned hits[8];
-                const long long t = t0 + threadIdx.x;
-                const unsigned hit =
-                    __ballot_sync(0xFFFFFFFFu, t < a.n_tokens && load_index(a.tokens, a.index_bytes, t) == v);
-                __syncthreads();
-                if (threadIdx.x % 32 == 0) hits[threadIdx.x / 32] = hit;
-                __syncthreads();
-                for (int w = 0; w < 8; w++)
-                    for (unsigned m = hits[w]; m; m &= m - 1) {
-                        any = true;
-                        if (j < a.dim) sum += load_f<DT>(a.dout, (t0 + w * 32 + __ffs(m) - 1) * a.row_stride + j);
-                    }
+// ---- gradient
+//
+// 1. The tokens are sorted by index, equal ones in the order of their places
+//    (radix sort by one cluster); meanwhile the other CTAs clear the table.
+// 2. The sorted places are cut into chunks.  A CTA adds up the runs of its chunk in
+//    order; a run inside the chunk is written to the table, one that goes
+//    on beyond it into the workspace.
+// 3. Runs over several chunks are joined, chunk by chunk.
+// So a frequent token costs no more than others, and no sum depends on timing.
+
+struct SortArgs {
+    EmbedArgs e;
+    uint2 *items[2];    // (index, place), from one pass to the next
+    int bits, passes;   // of an index; of the sort
+    int chunk, n_chunks;
+    float *part;        // [n_chunks][2][dim]: sums of runs that began before the chunk, that go on after it
+};
+
+constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32;
+constexpr int kSortMaxBits = 9;       // of a pass
+constexpr int kSortCluster = 8;       // CTAs that sort, for more than kSortOneCta tokens
+constexpr int kSortOneCta = 8192;
+constexpr int kSortPitch = kSortWarps + 1;  // counts of a digit, one a warp (odd: no bank conflicts)
+constexpr int kSortSmem = (kSortPitch + 2) * (1 << kSortMaxBits) * (int)sizeof(unsigned);
+
+__device__ __forceinline__ uint32_t dsmem_load(const void *p, int rank) {
+    uint32_t addr = (uint32_t)__cvta_generic_to_shared(p), v;
+    asm volatile("mapa.shared::cluster.u32 %0, %0, %1;" : "+r"(addr) : "r"(rank));
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ void sort_cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Least significant digit first.  A warp owns a run of places, so that equal
+// digits keep their order; it counts its digits, the counts of all warps and
+// CTAs are summed up in (digit, CTA, warp) order, and the warp moves its
+// items there.
+__device__ __forceinline__ void sort_tokens(const SortArgs &s, unsigned *smem, int cta, int ctas) {
+    const EmbedArgs &a = s.e;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const unsigned n = (unsigned)a.n_tokens, warps = (unsigned)(ctas * kSortWarps);
+    const unsigned run = ((n + warps - 1) / warps + 31) / 32 * 32;
+    const unsigned lo = min(n, run * (unsigned)(cta * kSortWarps + warp)), hi = min(n, lo + run);
+    const int width = (s.bits + s.passes - 1) / s.passes;
+    const unsigned bins = 1u << width;
+    unsigned *count = smem;                       // [bins][kSortPitch]
+    unsigned *total = smem + bins * kSortPitch;   // [bins] of this CTA
+    unsigned *start = total + bins;               // [bins] of this CTA's items
+    __shared__ unsigned warp_sums[kSortWarps];
+    for (int pass = 0; pass < s.passes; pass++) {
+        const uint2 *in = s.items[pass & 1];
+        uint2 *out = s.items[(pass & 1) ^ 1];
+        auto item = [&](unsigned i) {
+            if (pass) return __ldcg(in + i);
+            const long long v = load_index(a.tokens, a.index_bytes, i);
+            return make_uint2(v >= 0 && v < a.vocab ? (unsigned)v : (unsigned)a.vocab, i);
+        };
+        for (unsigned i = threadIdx.x; i < bins * kSortPitch; i += kSortThreads) count[i] = 0u;
+        __syncthreads();
+        for (unsigned i0 = lo; i0 < hi; i0 += 32) {
+            const bool has = i0 + lane < hi;
+            const unsigned d = has ? item(i0 + lane).x >> (pass * width) & (bins - 1) : bins;
+            const unsigned peers = __match_any_sync(0xFFFFFFFFu, d);
+            if (has && lane == __ffs(peers) - 1) count[d * kSortPitch + warp] += __popc(peers);
+            __syncwarp();
+        }
+        __syncthreads();
+        // a digit's warps: a warp a digit, lane = warp
+        for (unsigned d = warp; d < bins; d += kSortWarps) {
+            const unsigned c = count[d * kSortPitch + lane];
+            unsigned x = c;
+#pragma unroll
+            for (int o = 1; o < 32; o *= 2) {
+                const unsigned y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+                if (lane >= o) x += y;
             }
-            if (j < a.dim && (any || !a.accumulate))
-                store_f<DT>(row, j, a.accumulate ? fmaf(sum, a.scale, load_f<DT>(row, j)) : sum * a.scale);
+            count[d * kSortPitch + lane] = x - c;
+            if (lane == 31) total[d] = x;
+        }
+        __syncthreads();
+        if (ctas > 1) sort_cluster_sync();
+        // where the digit's items begin, and this CTA's among them
+        unsigned all = 0, before = 0;
+        if (threadIdx.x < bins) {
+            if (ctas == 1) all = total[threadIdx.x];
+            else
+                for (int c = 0; c < ctas; c++) {
+                    const unsigned x = dsmem_load(total + threadIdx.x, c);
+                    all += x;
+                    if (c < cta) before += x;
+                }
+        }
+        unsigned x = all;
+#pragma unroll
+        for (int o = 1; o < 32; o *= 2) {
+            const unsigned y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+            if (lane >= o) x += y;
+        }
+        if (lane == 31) warp_sums[warp] = x;
+        __syncthreads();
+        unsigned base = 0;
+        for (int w = 0; w < warp; w++) base += warp_sums[w];
+        if (threadIdx.x < bins) start[threadIdx.x] = base + x - all + before;
+        __syncthreads();
+        for (unsigned i0 = lo; i0 < hi; i0 += 32) {
+            const bool has = i0 + lane < hi;
+            const uint2 it = has ? item(i0 + lane) : make_uint2(0, 0);
+            const unsigned d = has ? it.x >> (pass * width) & (bins - 1) : bins;
+            const unsigned peers = __match_any_sync(0xFFFFFFFFu, d);
+            const unsigned ahead = __popc(peers & ((1u << lane) - 1));
+            unsigned at = 0;
+            if (has) at = count[d * kSortPitch + warp];
+            __syncwarp();
+            if (has) {
+                out[start[d] + at + ahead] = it;
+                if (ahead == 0) count[d * kSortPitch + warp] = at + __popc(peers);
+            }
+            __syncwarp();
+        }
+        // the items, and every CTA's reads of the totals, before the next pass
+        if (ctas > 1) {
+            __threadfence();
+            sort_cluster_sync();
+        } else {
+            __syncthreads();
         }
     }
+}
+
+// CTAs 0 .. gridDim.y - 1 (one cluster) sort; the others clear the table.
+template <int DT, bool VEC>
+__global__ void __launch_bounds__(kSortThreads) embedding_sort_kernel(const __grid_constant__ SortArgs s, int sorters) {
+    extern __shared__ unsigned sort_smem[];
+    const EmbedArgs &a = s.e;
+    pdl_wait();
+    pdl_launch_dependents();
+    if ((int)blockIdx.x < sorters) {
+        sort_tokens(s, sort_smem, blockIdx.x, sorters);
+        return;
+    }
+    const Chunks chunks(a.vocab, a.p);
+    for (long long v = blockIdx.x - sorters; v < a.vocab; v += gridDim.x - sorters) {
+        char *row = table_row(a, chunks, v, ElemInfo<DT>::bytes);
+        if constexpr (VEC) {
+            for (int j = threadIdx.x; j < (int)(a.dim / RowBits<DT>::VE); j += kSortThreads)
+                reinterpret_cast<uint4 *>(row)[j] = make_uint4(0, 0, 0, 0);
+        } else {
+            for (long long j = threadIdx.x; j < a.dim; j += kSortThreads) store_f<DT>(row, j, 0.0f);
+        }
+    }
+}
+
+constexpr int kReduceThreads = 256;
+constexpr int kReduceAhead = 8;  // rows whose loads are in flight together
+constexpr int kMinChunk = 16;
+
+// Columns of a thread: a 16-byte vector, or 4 single elements 256 apart.
+template <int DT, bool VEC>
+struct GradCols {
+    static constexpr int N = VEC ? RowBits<DT>::VE : 4, kTile = kReduceThreads * N;
+    long long dim, first;
+    __device__ __forceinline__ long long at(int e) const {
+        return VEC ? first + (long long)threadIdx.x * N + e : first + threadIdx.x + e * kReduceThreads;
+    }
+    __device__ __forceinline__ bool has(int e) const { return at(VEC ? 0 : e) < dim; }
+    __device__ __forceinline__ void load(const void *row, float (&f)[N]) const {
+        if constexpr (VEC) {
+            RowBits<DT> w;
+            w.load(row, (int)(at(0) / N), has(0));
+#pragma unroll
+            for (int e = 0; e < N; e++) f[e] = w.get(e);
+        } else {
+#pragma unroll
+            for (int e = 0; e < N; e++) f[e] = has(e) ? load_f<DT>(row, at(e)) : 0.0f;
+        }
+    }
+    // a row of the workspace's sums
+    __device__ __forceinline__ void load_part(const float *part, float (&f)[N]) const {
+        if constexpr (VEC) {
+#pragma unroll
+            for (int e = 0; e < N; e += 4) {
+                const float4 q = has(0) ? *reinterpret_cast<const float4 *>(part + at(e)) : make_float4(0, 0, 0, 0);
+                f[e] = q.x, f[e + 1] = q.y, f[e + 2] = q.z, f[e + 3] = q.w;
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < N; e++) f[e] = has(e) ? part[at(e)] : 0.0f;
+        }
+    }
+    __device__ __forceinline__ void store_part(float *part, const float (&f)[N]) const {
+        if constexpr (VEC) {
+            if (has(0))
+#pragma unroll
+                for (int e = 0; e < N; e += 4) *reinterpret_cast<float4 *>(part + at(e)) = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < N; e++)
+                if (has(e)) part[at(e)] = f[e];
+        }
+    }
+    // dtables' row: scaled, added to what it holds if asked for, rounded once
+    __device__ __forceinline__ void finish(const EmbedArgs &a, char *row, const float (&sum)[N]) const {
+        float f[N] = {};
+        if (a.accumulate) {
+            if constexpr (VEC) {
+                if (has(0)) {
+                    const uint4 q = *reinterpret_cast<const uint4 *>(row + at(0) * ElemInfo<DT>::bytes);
+                    RowBits<DT> w;
+                    w.w[0] = q.x, w.w[1] = q.y, w.w[2] = q.z, w.w[3] = q.w;
+#pragma unroll
+                    for (int e = 0; e < N; e++) f[e] = w.get(e);
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < N; e++) f[e] = has(e) ? load_f<DT>(row, at(e)) : 0.0f;
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < N; e++) f[e] = a.accumulate ? fmaf(sum[e], a.scale, f[e]) : sum[e] * a.scale;
+        if constexpr (VEC) {
+            if (has(0)) store_vec<DT>(row, (int)(at(0) / N), f);
+        } else {
+#pragma unroll
+            for (int e = 0; e < N; e++)
+                if (has(e)) store_f<DT>(row, at(e), f[e]);
+        }
+    }
+};
+
+template <int DT, bool VEC>
+__global__ void __launch_bounds__(kReduceThreads) embedding_runs_kernel(const __grid_constant__ SortArgs s) {
+    using Cols = GradCols<DT, VEC>;
+    constexpr int N = Cols::N, EB = ElemInfo<DT>::bytes;
+    const EmbedArgs &a = s.e;
+    pdl_wait();
+    pdl_launch_dependents();
+    const Chunks chunks(a.vocab, a.p);
+    const uint2 *items = s.items[s.passes & 1];
+    const Cols cols{a.dim, (long long)blockIdx.y * Cols::kTile};
+    const int lo = blockIdx.x * s.chunk, hi = min((long long)lo + s.chunk, a.n_tokens);
+    const unsigned none = (unsigned)a.vocab;  // left out: sorted last
+    const unsigned prev = lo ? items[lo - 1].x : none + 1, next = hi < a.n_tokens ? items[hi].x : none + 1;
+    float sum[N] = {};
+    unsigned key = items[lo].x;
+    bool began = key != prev;  // the run begins in this chunk
+    auto close = [&](bool ends) {
+        if (began && ends) {
+            cols.finish(a, table_row(a, chunks, key, EB), sum);
+        } else {
+            cols.store_part(s.part + ((long long)blockIdx.x * 2 + (began ? 1 : 0)) * a.dim, sum);
+        }
+    };
+    for (int i0 = lo; i0 < hi && key != none; i0 += kReduceAhead) {
+        uint2 it[kReduceAhead];
+        float f[kReduceAhead][N];
+#pragma unroll
+        for (int u = 0; u < kReduceAhead; u++) it[u] = i0 + u < hi ? items[i0 + u] : make_uint2(none, 0);
+#pragma unroll
+        for (int u = 0; u < kReduceAhead; u++)
+            if (it[u].x != none) cols.load(static_cast<const char *>(a.dout) + it[u].y * a.row_stride * EB, f[u]);
+#pragma unroll
+        for (int u = 0; u < kReduceAhead; u++) {
+            if (i0 + u >= hi || key == none) continue;
+            if (it[u].x != key) {
+                close(true);
+                key = it[u].x;
+                began = true;
+#pragma unroll
+                for (int e = 0; e < N; e++) sum[e] = 0.0f;
+                if (key == none) continue;
+            }
+#pragma unroll
+            for (int e = 0; e < N; e++) sum[e] += f[u][e];
+        }
+    }
+    if (key != none) close(key != next);
+}
+
+// A run that begins in chunk blockIdx.x and goes on beyond it.
+template <int DT, bool VEC>
+__global__ void __launch_bounds__(kReduceThreads) embedding_join_kernel(const __grid_constant__ SortArgs s) {
+    using Cols = GradCols<DT, VEC>;
+    constexpr int N = Cols::N;
+    const EmbedArgs &a = s.e;
+    pdl_wait();
+    pdl_launch_dependents();
+    const uint2 *items = s.items[s.passes & 1];
+    auto end_of = [&](int c) { return min((long long)(c + 1) * s.chunk, a.n_tokens); };
+    const int c0 = blockIdx.x;
+    const long long hi = end_of(c0);
+    const unsigned key = items[hi - 1].x;
+    if (hi == a.n_tokens || key == (unsigned)a.vocab || items[hi].x != key) return;
+    const long long lo = (long long)c0 * s.chunk;
+    if (lo && items[lo - 1].x == key) return;  // it began earlier (the chunk's last run reaches back to it)
+    // the chunk that it ends in: the chunks after c0 that begin with its key
+    int last = c0;
+    for (int c = c0 + 1;; c += kReduceThreads) {
+        const int mine = c + (int)threadIdx.x;
+        const int more = __syncthreads_count(mine < s.n_chunks && items[(long long)mine * s.chunk].x == key);
+        last += more;
+        if (more < kReduceThreads) break;
+    }
+    const Cols cols{a.dim, (long long)blockIdx.y * Cols::kTile};
+    float sum[N];
+    cols.load_part(s.part + ((long long)c0 * 2 + 1) * a.dim, sum);
+#pragma unroll 4
+    for (int c = c0 + 1; c <= last; c++) {
+        float f[N];
+        cols.load_part(s.part + (long long)c * 2 * a.dim, f);
+#pragma unroll
+        for (int e = 0; e < N; e++) sum[e] += f[e];
+    }
+    const Chunks chunks(a.vocab, a.p);
+    cols.finish(a, table_row(a, chunks, key, ElemInfo<DT>::bytes), sum);
 }
 
 namespace {
@@ -126,15 +451,59 @@ int embedding(rar_ctx *h, const rar_embedding_args *a, cudaStream_t stream) {
     k.scale = a->scale;
     k.out = a->out;
     note_op_call(h, a->p, stream);
-    const size_t most = (size_t)h->sm_count * 8;
-    const dim3 grid((unsigned)(a->n_tokens < most ? a->n_tokens : most));
+    const size_t ve = 16 / e;
+    bool vec = a->dim % ve == 0 && vec16(a->out, a->n_tokens, k.row_stride, e);
+    for (int r = 0; r < a->p && vec; r++) vec = vec16(a->tables[r], a->vocab / a->p + 1, k.table_stride, e);
+    // 4 loads in flight a thread where that still leaves 4 CTAs an SM, else one
+    const size_t count = vec ? a->n_tokens * (a->dim / ve) : a->n_tokens * a->dim;
+    const bool many = count >= (size_t)h->sm_count * 4 * 1024;
+    const size_t ctas = many ? (count + 1023) / 1024 : (count + 255) / 256;
+    if (ctas > 0x7FFFFFFFu) return c.bad("the lookup is too large");
     cudaError_t ce = dispatch_float(a->dtype, [&](auto dt) {
-        return launch_pdl(embedding_kernel<decltype(dt)::value>, grid, dim3(256), 0, stream, k);
+        constexpr int DT = decltype(dt)::value;
+        return launch_pdl(vec ? (many ? embedding_kernel<DT, true, 4> : embedding_kernel<DT, true, 1>)
+                              : (many ? embedding_kernel<DT, false, 4> : embedding_kernel<DT, false, 1>),
+                          dim3((unsigned)ctas), dim3(256), 0, stream, k);
     });
     return ce == cudaSuccess ? RAR_OK : cuda_fail(h, ce, "launching the lookup");
 }
 
-size_t grad_workspace(size_t, size_t, size_t) { return 0; }
+size_t grad_plan(void *base, size_t n_tokens, size_t vocab, size_t dim, SortArgs *s) {
+    WorkspacePlan w(base);
+    // at most 4096 chunks, so that their sums stay small against dout
+    const size_t chunk = std::max<size_t>(kMinChunk, (n_tokens + 4095) / 4096), n = (n_tokens + chunk - 1) / chunk;
+    s->chunk = (int)chunk;
+    s->n_chunks = (int)n;
+    s->items[0] = w.take<uint2>(n_tokens);
+    s->items[1] = w.take<uint2>(n_tokens);
+    s->part = w.take<float>(n > 1 ? n * 2 * dim : 0);
+    s->bits = 1;
+    while (((size_t)1 << s->bits) <= vocab) s->bits++;  // 0 .. vocab, which stands for left out
+    s->passes = (s->bits + kSortMaxBits - 1) / kSortMaxBits;
+    return w.used;
+}
+
+// The launch of the sorting cluster and the clearing CTAs.
+template <typename... Params, typename... Args>
+cudaError_t launch_clusters(void (*kern)(Params...), unsigned grid, unsigned cluster, cudaStream_t stream, Args &&...args) {
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSortSmem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kSortThreads);
+    cfg.dynamicSmemBytes = kSortSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
+}
 
 int embedding_grad(rar_ctx *h, const rar_embedding_grad_args *a, cudaStream_t stream) {
     OpCheck c(h, "rar_embedding_grad");
@@ -145,6 +514,7 @@ int embedding_grad(rar_ctx *h, const rar_embedding_grad_args *a, cudaStream_t st
     if (a->vocab < 1 || a->dim < 1) return c.bad("vocab and dim must be at least 1");
     if (a->vocab > 0x7FFFFFFFu) return c.bad("vocab must be at most 2^31 - 1");
     if (a->n_tokens > (size_t)1 << 24) return c.bad("n_tokens must be at most 2^24");
+    if (a->dim > (size_t)1 << 24) return c.bad("dim must be at most 2^24");
     if (a->index_bytes != 4 && a->index_bytes != 8) return c.bad("index_bytes must be 4 or 8");
     const size_t e = (size_t)elem_bytes(a->dtype);
     MatrixSpan s;
@@ -156,7 +526,8 @@ int embedding_grad(rar_ctx *h, const rar_embedding_grad_args *a, cudaStream_t st
     c.input(s);
     if ((rc = c.matrix("dout", a->dout, a->n_tokens, a->dim, a->dout_stride, e, e, &s)) != RAR_OK) return rc;
     c.input(s);
-    rc = c.workspace(a->workspace, a->workspace_bytes, grad_workspace(a->n_tokens, a->vocab, a->dim));
+    SortArgs sort{};
+    rc = c.workspace(a->workspace, a->workspace_bytes, grad_plan(nullptr, a->n_tokens, a->vocab, a->dim, &sort));
     if (rc != RAR_OK) return rc;
     if ((rc = c.overlaps([](const MatrixSpan &, const MatrixSpan &) { return false; })) != RAR_OK) return rc;
 
@@ -177,10 +548,30 @@ int embedding_grad(rar_ctx *h, const rar_embedding_grad_args *a, cudaStream_t st
     k.dout = a->dout;
     k.accumulate = a->accumulate;
     note_op_call(h, a->p, stream);
-    const size_t most = (size_t)h->sm_count * 8;
-    const dim3 grid((unsigned)(a->vocab < most ? a->vocab : most));
+    grad_plan(a->workspace, a->n_tokens, a->vocab, a->dim, &sort);
+    sort.e = k;
+    const size_t ve = 16 / e;
+    bool vec = a->dim % ve == 0 && vec16(a->dout, a->n_tokens, k.row_stride, e);
+    for (int r = 0; r < a->p && vec; r++) vec = vec16(a->dtables[r], a->vocab / a->p + 1, k.table_stride, e);
+    const unsigned sorters = a->n_tokens == 0 ? 0 : a->n_tokens <= (size_t)kSortOneCta ? 1 : kSortCluster;
+    const unsigned cluster = std::max(sorters, 1u);
+    // the clearing CTAs: as many as are resident (2 an SM), in whole clusters
+    unsigned clear = 0;
+    if (!a->accumulate) clear = (unsigned)std::min<size_t>(a->vocab, (size_t)h->sm_count * 2 - cluster) / cluster * cluster;
+    if (!a->accumulate && clear == 0) clear = cluster;
     cudaError_t ce = dispatch_float(a->dtype, [&](auto dt) {
-        return launch_pdl(embedding_grad_kernel<decltype(dt)::value>, grid, dim3(256), 0, stream, k);
+        constexpr int DT = decltype(dt)::value;
+        auto steps = [&](auto vv) {
+            constexpr bool VEC = decltype(vv)::value != 0;
+            cudaError_t e1 = launch_clusters(embedding_sort_kernel<DT, VEC>, sorters + clear, cluster, stream, sort, (int)sorters);
+            if (e1 != cudaSuccess || sorters == 0) return e1;
+            const dim3 grid((unsigned)sort.n_chunks, (unsigned)((a->dim + GradCols<DT, VEC>::kTile - 1) / GradCols<DT, VEC>::kTile));
+            e1 = launch_pdl(embedding_runs_kernel<DT, VEC>, grid, dim3(kReduceThreads), 0, stream, sort);
+            if (e1 == cudaSuccess && sort.n_chunks > 1)
+                e1 = launch_pdl(embedding_join_kernel<DT, VEC>, grid, dim3(kReduceThreads), 0, stream, sort);
+            return e1;
+        };
+        return vec ? steps(IntC<1>{}) : steps(IntC<0>{});
     });
     return ce == cudaSuccess ? RAR_OK : cuda_fail(h, ce, "launching the lookup's gradient");
 }
@@ -198,7 +589,9 @@ int rar_embedding(rar_handle h, const rar_embedding_args *a, void *stream) {
 }
 
 size_t rar_embedding_grad_workspace(size_t n_tokens, size_t vocab, size_t dim) {
-    return rar::grad_workspace(n_tokens, vocab, dim);
+    if (vocab < 1 || vocab > 0x7FFFFFFFu || dim < 1 || n_tokens > (size_t)1 << 24) return 0;
+    rar::SortArgs s{};
+    return rar::grad_plan(nullptr, n_tokens, vocab, dim, &s);
 }
 
 int rar_embedding_grad(rar_handle h, const rar_embedding_grad_args *a, void *stream) {

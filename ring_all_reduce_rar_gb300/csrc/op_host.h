@@ -119,6 +119,11 @@ inline void note_op_call(rar_ctx *h, int p, cudaStream_t stream) {
     h->last_phases = 0;
 }
 
+// Whether 16-byte accesses reach every row of a matrix.
+inline bool vec16(const void *ptr, size_t rows, long long stride, size_t e) {
+    return (uintptr_t)ptr % 16 == 0 && (rows <= 1 || (size_t)stride * e % 16 == 0);
+}
+
 // Runs an entry point's body: no C++ exception leaves the library.
 template <typename F>
 int guarded(rar_ctx *h, F &&body) {

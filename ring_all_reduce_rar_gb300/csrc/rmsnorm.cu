@@ -32,30 +32,6 @@ struct NormArgs {
     int warps;       // warps a row
 };
 
-// A 16-byte vector of a row as it was read: VE elements, widened where they
-// are used, so that a load in flight takes 4 registers.
-template <int DT>
-struct RowBits {
-    static constexpr int VE = 16 / ElemInfo<DT>::bytes;
-    uint32_t w[4];
-    __device__ __forceinline__ void load(const void *row, int vec, bool has) {
-        uint4 q = make_uint4(0, 0, 0, 0);
-        if (has) q = __ldg(static_cast<const uint4 *>(row) + vec);
-        w[0] = q.x, w[1] = q.y, w[2] = q.z, w[3] = q.w;
-    }
-    __device__ __forceinline__ float get(int e) const {
-        if constexpr (DT == DT_F32) return __uint_as_float(w[e]);
-        else if constexpr (DT == DT_BF16) return __uint_as_float(e % 2 ? w[e / 2] & 0xFFFF0000u : w[e / 2] << 16);
-        else return widen<DT>(e % 2 ? w[e / 2] >> 16 : w[e / 2] & 0xFFFFu);
-    }
-};
-template <int DT>
-__device__ __forceinline__ void store_vec(void *row, int vec, const float *f) {
-    uint4 q;
-    if constexpr (DT == DT_F32) q = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
-    else q = narrow8<DT>(f);
-    static_cast<uint4 *>(row)[vec] = q;
-}
 template <int DT>
 __device__ __forceinline__ const char *row_of(const void *base, long long t, long long stride) {
     return static_cast<const char *>(base) + t * stride * ElemInfo<DT>::bytes;
@@ -78,21 +54,6 @@ __device__ __forceinline__ float row_sum(float v, float *red, int warps) {
     float t = threadIdx.x % 32 < warps ? red[w0 + threadIdx.x % 32] : 0.0f;
     return warp_sum(t);
 }
-
-// chunk_of with 32-bit divisions where the buffer allows them.
-struct Chunks {
-    long long base, extra;
-    bool small;
-    __device__ __forceinline__ Chunks(long long n, int p) : small(n < 0x7FFFFFFF) {
-        if (small) base = (uint32_t)n / (uint32_t)p, extra = (uint32_t)n % (uint32_t)p;
-        else base = n / p, extra = n % p;
-    }
-    __device__ __forceinline__ int of(long long i) const {
-        if (!small) return chunk_of(i, base, extra);
-        const uint32_t b = (uint32_t)base, x = (uint32_t)extra, big = x * (b + 1), k = (uint32_t)i;
-        return (int)(k < big ? k / (b + 1) : x + (k - big) / b);
-    }
-};
 
 constexpr int kNormMaxThreads = 512;
 constexpr int kNormRanks = 8;  // ranks whose loads are in flight together
@@ -451,11 +412,6 @@ cudaError_t launch_any(void (*kern)(Args), dim3 grid, int threads, size_t smem, 
 }
 // Threads of a CTA that takes a row of `dim` single elements: about 4 each.
 int any_threads(size_t dim) { return (int)std::min<size_t>(std::max<size_t>((dim / 4 + 31) / 32 * 32, 32), kNormMaxThreads); }
-// Whether 16-byte accesses reach every row of a matrix.
-bool vec16(const void *ptr, size_t rows, long long stride, size_t e) {
-    return (uintptr_t)ptr % 16 == 0 && (rows <= 1 || (size_t)stride * e % 16 == 0);
-}
-
 int add_rmsnorm(rar_ctx *h, const rar_rmsnorm_args *a, cudaStream_t stream) {
     OpCheck c(h, "rar_add_rmsnorm");
     if (!a) return c.bad("args is NULL");
