@@ -508,7 +508,7 @@ typedef struct {
     size_t dtable_stride;
     int p;
     int dtype;
-    size_t vocab, dim;         /* at least 1; vocab at most 2^31 - 1 */
+    size_t vocab, dim;         /* at least 1; vocab at most 2^31 - 1, dim at most 2^22 */
     float scale;
     int accumulate;
     void *workspace;

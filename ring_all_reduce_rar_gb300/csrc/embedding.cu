@@ -101,7 +101,8 @@ struct SortArgs {
 constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32;
 constexpr int kSortMaxBits = 9;       // of a pass
 constexpr int kSortCluster = 8;       // CTAs that sort, for more than kSortOneCta tokens
-constexpr int kSortOneCta = 8192;
+constexpr int kSortHeld = 8;          // items a thread in flight
+constexpr int kSortOneCta = kSortThreads * kSortHeld;
 constexpr int kSortPitch = kSortWarps + 1;  // counts of a digit, one a warp (odd: no bank conflicts)
 constexpr int kSortSmem = (kSortPitch + 2) * (1 << kSortMaxBits) * (int)sizeof(unsigned);
 
@@ -131,22 +132,39 @@ __device__ __forceinline__ void sort_tokens(const SortArgs &s, unsigned *smem, i
     unsigned *total = smem + bins * kSortPitch;   // [bins] of this CTA
     unsigned *start = total + bins;               // [bins] of this CTA's items
     __shared__ unsigned warp_sums[kSortWarps];
+    const bool held = run <= 32 * kSortHeld;      // the run's items stay in registers
     for (int pass = 0; pass < s.passes; pass++) {
         const uint2 *in = s.items[pass & 1];
         uint2 *out = s.items[(pass & 1) ^ 1];
-        auto item = [&](unsigned i) {
-            if (pass) return __ldcg(in + i);
-            const long long v = load_index(a.tokens, a.index_bytes, i);
-            return make_uint2(v >= 0 && v < a.vocab ? (unsigned)v : (unsigned)a.vocab, i);
+        uint2 it[kSortHeld];
+        // the items of kSortHeld rounds of 32 from place i0, loads in flight together
+        auto load = [&](unsigned i0) {
+#pragma unroll
+            for (int k = 0; k < kSortHeld; k++) {
+                const unsigned i = i0 + 32 * k + lane;
+                it[k] = make_uint2(0, 0);
+                if (i >= hi) continue;
+                if (pass) {
+                    it[k] = __ldcg(in + i);
+                } else {
+                    const long long v = load_index(a.tokens, a.index_bytes, i);
+                    it[k] = make_uint2(v >= 0 && v < a.vocab ? (unsigned)v : (unsigned)a.vocab, i);
+                }
+            }
         };
+        auto digit = [&](int k, unsigned i0) { return i0 + 32 * k + lane < hi ? it[k].x >> (pass * width) & (bins - 1) : bins; };
+        load(lo);
         for (unsigned i = threadIdx.x; i < bins * kSortPitch; i += kSortThreads) count[i] = 0u;
         __syncthreads();
-        for (unsigned i0 = lo; i0 < hi; i0 += 32) {
-            const bool has = i0 + lane < hi;
-            const unsigned d = has ? item(i0 + lane).x >> (pass * width) & (bins - 1) : bins;
-            const unsigned peers = __match_any_sync(0xFFFFFFFFu, d);
-            if (has && lane == __ffs(peers) - 1) count[d * kSortPitch + warp] += __popc(peers);
-            __syncwarp();
+        for (unsigned i0 = lo; i0 < hi; i0 += 32 * kSortHeld) {
+            if (i0 != lo) load(i0);
+#pragma unroll
+            for (int k = 0; k < kSortHeld; k++) {
+                if (i0 + 32 * k >= hi) break;
+                const unsigned d = digit(k, i0), peers = __match_any_sync(0xFFFFFFFFu, d);
+                if (d < bins && lane == __ffs(peers) - 1) count[d * kSortPitch + warp] += __popc(peers);
+                __syncwarp();
+            }
         }
         __syncthreads();
         // a digit's warps: a warp a digit, lane = warp
@@ -186,20 +204,21 @@ __device__ __forceinline__ void sort_tokens(const SortArgs &s, unsigned *smem, i
         for (int w = 0; w < warp; w++) base += warp_sums[w];
         if (threadIdx.x < bins) start[threadIdx.x] = base + x - all + before;
         __syncthreads();
-        for (unsigned i0 = lo; i0 < hi; i0 += 32) {
-            const bool has = i0 + lane < hi;
-            const uint2 it = has ? item(i0 + lane) : make_uint2(0, 0);
-            const unsigned d = has ? it.x >> (pass * width) & (bins - 1) : bins;
-            const unsigned peers = __match_any_sync(0xFFFFFFFFu, d);
-            const unsigned ahead = __popc(peers & ((1u << lane) - 1));
-            unsigned at = 0;
-            if (has) at = count[d * kSortPitch + warp];
-            __syncwarp();
-            if (has) {
-                out[start[d] + at + ahead] = it;
-                if (ahead == 0) count[d * kSortPitch + warp] = at + __popc(peers);
+        for (unsigned i0 = lo; i0 < hi; i0 += 32 * kSortHeld) {
+            if (!held) load(i0);
+#pragma unroll
+            for (int k = 0; k < kSortHeld; k++) {
+                if (i0 + 32 * k >= hi) break;
+                const unsigned d = digit(k, i0), peers = __match_any_sync(0xFFFFFFFFu, d);
+                const unsigned ahead = __popc(peers & ((1u << lane) - 1));
+                const unsigned at = d < bins ? count[d * kSortPitch + warp] : 0u;
+                __syncwarp();
+                if (d < bins) {
+                    out[start[d] + at + ahead] = it[k];
+                    if (ahead == 0) count[d * kSortPitch + warp] = at + __popc(peers);
+                }
+                __syncwarp();
             }
-            __syncwarp();
         }
         // the items, and every CTA's reads of the totals, before the next pass
         if (ctas > 1) {
@@ -211,24 +230,46 @@ __device__ __forceinline__ void sort_tokens(const SortArgs &s, unsigned *smem, i
     }
 }
 
-// CTAs 0 .. gridDim.y - 1 (one cluster) sort; the others clear the table.
+constexpr int kClearBytes = 16384;  // zeros in shared memory, the source of the bulk stores
+
+// CTAs 0 .. sorters - 1 (one cluster) sort; the others clear the table.
 template <int DT, bool VEC>
 __global__ void __launch_bounds__(kSortThreads) embedding_sort_kernel(const __grid_constant__ SortArgs s, int sorters) {
-    extern __shared__ unsigned sort_smem[];
+    extern __shared__ __align__(128) unsigned sort_smem[];
     const EmbedArgs &a = s.e;
-    pdl_wait();
-    pdl_launch_dependents();
     if ((int)blockIdx.x < sorters) {
+        pdl_wait();
+        pdl_launch_dependents();
         sort_tokens(s, sort_smem, blockIdx.x, sorters);
         return;
     }
     const Chunks chunks(a.vocab, a.p);
-    for (long long v = blockIdx.x - sorters; v < a.vocab; v += gridDim.x - sorters) {
-        char *row = table_row(a, chunks, v, ElemInfo<DT>::bytes);
-        if constexpr (VEC) {
-            for (int j = threadIdx.x; j < (int)(a.dim / RowBits<DT>::VE); j += kSortThreads)
-                reinterpret_cast<uint4 *>(row)[j] = make_uint4(0, 0, 0, 0);
-        } else {
+    const int clearers = gridDim.x - sorters, me = blockIdx.x - sorters;
+    if constexpr (VEC) {
+        // every warp's lane 0 has one bulk store a row in flight after the other
+        for (int i = threadIdx.x; i < kClearBytes / 16; i += kSortThreads) reinterpret_cast<uint4 *>(sort_smem)[i] = make_uint4(0, 0, 0, 0);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncthreads();
+        pdl_wait();
+        pdl_launch_dependents();
+        if (threadIdx.x % 32 == 0) {
+            const uint32_t zeros = (uint32_t)__cvta_generic_to_shared(sort_smem);
+            const long long bytes = a.dim * ElemInfo<DT>::bytes;
+            for (long long v = (long long)me * kSortWarps + threadIdx.x / 32; v < a.vocab; v += (long long)clearers * kSortWarps) {
+                char *row = table_row(a, chunks, v, ElemInfo<DT>::bytes);
+                for (long long at = 0; at < bytes; at += kClearBytes)
+                    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(row + at), "r"(zeros),
+                                 "r"((uint32_t)(bytes - at < kClearBytes ? bytes - at : kClearBytes))
+                                 : "memory");
+                asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+            }
+            asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        }
+    } else {
+        pdl_wait();
+        pdl_launch_dependents();
+        for (long long v = me; v < a.vocab; v += clearers) {
+            char *row = table_row(a, chunks, v, ElemInfo<DT>::bytes);
             for (long long j = threadIdx.x; j < a.dim; j += kSortThreads) store_f<DT>(row, j, 0.0f);
         }
     }
@@ -238,25 +279,29 @@ constexpr int kReduceThreads = 256;
 constexpr int kReduceAhead = 8;  // rows whose loads are in flight together
 constexpr int kMinChunk = 16;
 
-// Columns of a thread: a 16-byte vector, or 4 single elements 256 apart.
+// Columns of a thread of `n` threads: a 16-byte vector, or 4 single elements n apart.
+// Rows are held as they were read.
 template <int DT, bool VEC>
 struct GradCols {
-    static constexpr int N = VEC ? RowBits<DT>::VE : 4, kTile = kReduceThreads * N;
+    static constexpr int N = VEC ? RowBits<DT>::VE : 4;
     long long dim, first;
-    __device__ __forceinline__ long long at(int e) const {
-        return VEC ? first + (long long)threadIdx.x * N + e : first + threadIdx.x + e * kReduceThreads;
-    }
+    int tid, n;
+    struct Bits {
+        RowBits<DT> v;
+        __device__ __forceinline__ float get(int e) const { return VEC ? v.get(e) : widen<DT>(v.w[e]); }
+    };
+    __device__ __forceinline__ long long at(int e) const { return VEC ? first + (long long)tid * N + e : first + tid + (long long)e * n; }
     __device__ __forceinline__ bool has(int e) const { return at(VEC ? 0 : e) < dim; }
-    __device__ __forceinline__ void load(const void *row, float (&f)[N]) const {
+    __device__ __forceinline__ Bits load(const char *row, bool wanted) const {  // (coherent: a row of the table is written later)
+        Bits b;
         if constexpr (VEC) {
-            RowBits<DT> w;
-            w.load(row, (int)(at(0) / N), has(0));
-#pragma unroll
-            for (int e = 0; e < N; e++) f[e] = w.get(e);
+            const uint4 q = wanted && has(0) ? *reinterpret_cast<const uint4 *>(row + at(0) * ElemInfo<DT>::bytes) : make_uint4(0, 0, 0, 0);
+            b.v.w[0] = q.x, b.v.w[1] = q.y, b.v.w[2] = q.z, b.v.w[3] = q.w;
         } else {
 #pragma unroll
-            for (int e = 0; e < N; e++) f[e] = has(e) ? load_f<DT>(row, at(e)) : 0.0f;
+            for (int e = 0; e < N; e++) b.v.w[e] = wanted && has(e) ? load_elem<DT>(row, at(e)) : 0u;
         }
+        return b;
     }
     // a row of the workspace's sums
     __device__ __forceinline__ void load_part(const float *part, float (&f)[N]) const {
@@ -282,25 +327,11 @@ struct GradCols {
                 if (has(e)) part[at(e)] = f[e];
         }
     }
-    // dtables' row: scaled, added to what it holds if asked for, rounded once
-    __device__ __forceinline__ void finish(const EmbedArgs &a, char *row, const float (&sum)[N]) const {
-        float f[N] = {};
-        if (a.accumulate) {
-            if constexpr (VEC) {
-                if (has(0)) {
-                    const uint4 q = *reinterpret_cast<const uint4 *>(row + at(0) * ElemInfo<DT>::bytes);
-                    RowBits<DT> w;
-                    w.w[0] = q.x, w.w[1] = q.y, w.w[2] = q.z, w.w[3] = q.w;
+    // a row of the table: the sum, scaled, added to what the row held, rounded once
+    __device__ __forceinline__ void finish(char *row, const float (&sum)[N], float scale, bool add, const Bits &old) const {
+        float f[N];
 #pragma unroll
-                    for (int e = 0; e < N; e++) f[e] = w.get(e);
-                }
-            } else {
-#pragma unroll
-                for (int e = 0; e < N; e++) f[e] = has(e) ? load_f<DT>(row, at(e)) : 0.0f;
-            }
-        }
-#pragma unroll
-        for (int e = 0; e < N; e++) f[e] = a.accumulate ? fmaf(sum[e], a.scale, f[e]) : sum[e] * a.scale;
+        for (int e = 0; e < N; e++) f[e] = add ? fmaf(sum[e], scale, old.get(e)) : sum[e] * scale;
         if constexpr (VEC) {
             if (has(0)) store_vec<DT>(row, (int)(at(0) / N), f);
         } else {
@@ -311,8 +342,10 @@ struct GradCols {
     }
 };
 
-template <int DT, bool VEC>
-__global__ void __launch_bounds__(kReduceThreads) embedding_runs_kernel(const __grid_constant__ SortArgs s) {
+// ADD: accumulate.  The row that a run is added to is read together with the
+// run's last row of dout.
+template <int DT, bool VEC, bool ADD>
+__global__ void __launch_bounds__(kReduceThreads, ADD ? 2 : 3) embedding_runs_kernel(const __grid_constant__ SortArgs s) {
     using Cols = GradCols<DT, VEC>;
     constexpr int N = Cols::N, EB = ElemInfo<DT>::bytes;
     const EmbedArgs &a = s.e;
@@ -320,62 +353,61 @@ __global__ void __launch_bounds__(kReduceThreads) embedding_runs_kernel(const __
     pdl_launch_dependents();
     const Chunks chunks(a.vocab, a.p);
     const uint2 *items = s.items[s.passes & 1];
-    const Cols cols{a.dim, (long long)blockIdx.y * Cols::kTile};
-    const int lo = blockIdx.x * s.chunk, hi = min((long long)lo + s.chunk, a.n_tokens);
+    const Cols cols{a.dim, (long long)blockIdx.y * kReduceThreads * N, (int)threadIdx.x, kReduceThreads};
+    const int lo = blockIdx.x * s.chunk, hi = (int)min((long long)lo + s.chunk, a.n_tokens);
     const unsigned none = (unsigned)a.vocab;  // left out: sorted last
-    const unsigned prev = lo ? items[lo - 1].x : none + 1, next = hi < a.n_tokens ? items[hi].x : none + 1;
     float sum[N] = {};
-    unsigned key = items[lo].x;
-    bool began = key != prev;  // the run begins in this chunk
-    auto close = [&](bool ends) {
-        if (began && ends) {
-            cols.finish(a, table_row(a, chunks, key, EB), sum);
-        } else {
-            cols.store_part(s.part + ((long long)blockIdx.x * 2 + (began ? 1 : 0)) * a.dim, sum);
-        }
-    };
-    for (int i0 = lo; i0 < hi && key != none; i0 += kReduceAhead) {
+    bool began = lo == 0 || items[lo - 1].x != items[lo].x;  // the run begins in this chunk
+    for (int i0 = lo; i0 < hi; i0 += kReduceAhead) {
         uint2 it[kReduceAhead];
-        float f[kReduceAhead][N];
-#pragma unroll
-        for (int u = 0; u < kReduceAhead; u++) it[u] = i0 + u < hi ? items[i0 + u] : make_uint2(none, 0);
-#pragma unroll
-        for (int u = 0; u < kReduceAhead; u++)
-            if (it[u].x != none) cols.load(static_cast<const char *>(a.dout) + it[u].y * a.row_stride * EB, f[u]);
+        unsigned after[kReduceAhead];  // the next item's index
 #pragma unroll
         for (int u = 0; u < kReduceAhead; u++) {
-            if (i0 + u >= hi || key == none) continue;
-            if (it[u].x != key) {
-                close(true);
-                key = it[u].x;
-                began = true;
+            it[u] = i0 + u < hi ? items[i0 + u] : make_uint2(none, 0);
+            after[u] = i0 + u + 1 < a.n_tokens ? items[i0 + u + 1].x : none + 1;
+        }
+        typename Cols::Bits f[kReduceAhead], old[ADD ? kReduceAhead : 1];
 #pragma unroll
-                for (int e = 0; e < N; e++) sum[e] = 0.0f;
-                if (key == none) continue;
+        for (int u = 0; u < kReduceAhead; u++) {
+            f[u] = cols.load(static_cast<const char *>(a.dout) + it[u].y * a.row_stride * EB, it[u].x != none);
+            if (ADD) {
+                const bool ends = it[u].x != none && it[u].x != after[u];
+                old[u] = cols.load(ends ? table_row(a, chunks, it[u].x, EB) : nullptr, ends);
             }
+        }
 #pragma unroll
-            for (int e = 0; e < N; e++) sum[e] += f[u][e];
+        for (int u = 0; u < kReduceAhead; u++) {
+            if (it[u].x == none) continue;
+#pragma unroll
+            for (int e = 0; e < N; e++) sum[e] += f[u].get(e);
+            const bool ends = it[u].x != after[u];
+            if (!ends && i0 + u + 1 < hi) continue;
+            if (began && ends) cols.finish(table_row(a, chunks, it[u].x, EB), sum, a.scale, ADD, old[ADD ? u : 0]);
+            else cols.store_part(s.part + ((long long)blockIdx.x * 2 + (began ? 1 : 0)) * a.dim, sum);
+            began = true;
+#pragma unroll
+            for (int e = 0; e < N; e++) sum[e] = 0.0f;
         }
     }
-    if (key != none) close(key != next);
 }
 
-// A run that begins in chunk blockIdx.x and goes on beyond it.
-template <int DT, bool VEC>
+// A run that begins in chunk blockIdx.x and goes on beyond it: 8 warps take every
+// eighth chunk, and their sums are added in order.
+template <int DT, bool VEC, bool ADD>
 __global__ void __launch_bounds__(kReduceThreads) embedding_join_kernel(const __grid_constant__ SortArgs s) {
     using Cols = GradCols<DT, VEC>;
-    constexpr int N = Cols::N;
+    constexpr int N = Cols::N, kWarps = kReduceThreads / 32;
+    __shared__ float sums[kWarps][N][32];
     const EmbedArgs &a = s.e;
     pdl_wait();
     pdl_launch_dependents();
     const uint2 *items = s.items[s.passes & 1];
-    auto end_of = [&](int c) { return min((long long)(c + 1) * s.chunk, a.n_tokens); };
-    const int c0 = blockIdx.x;
-    const long long hi = end_of(c0);
-    const unsigned key = items[hi - 1].x;
-    if (hi == a.n_tokens || key == (unsigned)a.vocab || items[hi].x != key) return;
-    const long long lo = (long long)c0 * s.chunk;
-    if (lo && items[lo - 1].x == key) return;  // it began earlier (the chunk's last run reaches back to it)
+    const int c0 = blockIdx.x, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const long long lo = (long long)c0 * s.chunk, hi = min(lo + s.chunk, a.n_tokens);
+    if (hi == a.n_tokens) return;
+    const unsigned key = items[hi - 1].x, next = items[hi].x, before = lo ? items[lo - 1].x : (unsigned)a.vocab;
+    // (one that reaches back before the chunk is the business of an earlier CTA)
+    if (key == (unsigned)a.vocab || next != key || before == key) return;
     // the chunk that it ends in: the chunks after c0 that begin with its key
     int last = c0;
     for (int c = c0 + 1;; c += kReduceThreads) {
@@ -384,18 +416,26 @@ __global__ void __launch_bounds__(kReduceThreads) embedding_join_kernel(const __
         last += more;
         if (more < kReduceThreads) break;
     }
-    const Cols cols{a.dim, (long long)blockIdx.y * Cols::kTile};
-    float sum[N];
-    cols.load_part(s.part + ((long long)c0 * 2 + 1) * a.dim, sum);
+    const Cols cols{a.dim, (long long)blockIdx.y * 32 * N, lane, 32};
+    char *row = table_row(a, Chunks(a.vocab, a.p), key, ElemInfo<DT>::bytes);
+    const typename Cols::Bits old = cols.load(row, ADD && warp == 0);
+    float sum[N] = {};
+    if (warp == 0) cols.load_part(s.part + ((long long)c0 * 2 + 1) * a.dim, sum);
 #pragma unroll 4
-    for (int c = c0 + 1; c <= last; c++) {
+    for (int c = c0 + 1 + warp; c <= last; c += kWarps) {
         float f[N];
         cols.load_part(s.part + (long long)c * 2 * a.dim, f);
 #pragma unroll
         for (int e = 0; e < N; e++) sum[e] += f[e];
     }
-    const Chunks chunks(a.vocab, a.p);
-    cols.finish(a, table_row(a, chunks, key, ElemInfo<DT>::bytes), sum);
+#pragma unroll
+    for (int e = 0; e < N; e++) sums[warp][e][lane] = sum[e];
+    __syncthreads();
+    if (warp) return;
+    for (int w = 1; w < kWarps; w++)
+#pragma unroll
+        for (int e = 0; e < N; e++) sum[e] += sums[w][e][lane];
+    cols.finish(row, sum, a.scale, ADD, old);
 }
 
 namespace {
@@ -514,7 +554,7 @@ int embedding_grad(rar_ctx *h, const rar_embedding_grad_args *a, cudaStream_t st
     if (a->vocab < 1 || a->dim < 1) return c.bad("vocab and dim must be at least 1");
     if (a->vocab > 0x7FFFFFFFu) return c.bad("vocab must be at most 2^31 - 1");
     if (a->n_tokens > (size_t)1 << 24) return c.bad("n_tokens must be at most 2^24");
-    if (a->dim > (size_t)1 << 24) return c.bad("dim must be at most 2^24");
+    if (a->dim > (size_t)1 << 22) return c.bad("dim must be at most 2^22");
     if (a->index_bytes != 4 && a->index_bytes != 8) return c.bad("index_bytes must be 4 or 8");
     const size_t e = (size_t)elem_bytes(a->dtype);
     MatrixSpan s;
@@ -565,10 +605,13 @@ int embedding_grad(rar_ctx *h, const rar_embedding_grad_args *a, cudaStream_t st
             constexpr bool VEC = decltype(vv)::value != 0;
             cudaError_t e1 = launch_clusters(embedding_sort_kernel<DT, VEC>, sorters + clear, cluster, stream, sort, (int)sorters);
             if (e1 != cudaSuccess || sorters == 0) return e1;
-            const dim3 grid((unsigned)sort.n_chunks, (unsigned)((a->dim + GradCols<DT, VEC>::kTile - 1) / GradCols<DT, VEC>::kTile));
-            e1 = launch_pdl(embedding_runs_kernel<DT, VEC>, grid, dim3(kReduceThreads), 0, stream, sort);
+            constexpr int N = GradCols<DT, VEC>::N;
+            auto grid = [&](int threads) { return dim3((unsigned)sort.n_chunks, (unsigned)((a->dim + threads * N - 1) / (threads * N))); };
+            e1 = launch_pdl(a->accumulate ? embedding_runs_kernel<DT, VEC, true> : embedding_runs_kernel<DT, VEC, false>, grid(kReduceThreads),
+                            dim3(kReduceThreads), 0, stream, sort);
             if (e1 == cudaSuccess && sort.n_chunks > 1)
-                e1 = launch_pdl(embedding_join_kernel<DT, VEC>, grid, dim3(kReduceThreads), 0, stream, sort);
+                e1 = launch_pdl(a->accumulate ? embedding_join_kernel<DT, VEC, true> : embedding_join_kernel<DT, VEC, false>, grid(32),
+                                dim3(kReduceThreads), 0, stream, sort);
             return e1;
         };
         return vec ? steps(IntC<1>{}) : steps(IntC<0>{});

@@ -293,11 +293,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
             xent_steps<MODE>(a, b0, it, [&](int s, long long k, const BlockOf &b) {
                 const int st = (int)(step % kTcStages);
                 if (step >= kTcStages && !tc_wait(&sh, a.limits, &sh.empty[st], (uint32_t)(step / kTcStages - 1) & 1, 0)) return false;
-                if (rank == 0) tc_expect_tx(&sh.full[st], 2 * kTcStageBytes);
+                // boxes of tokens past the last are not loaded: their rows of the
+                // accumulator are never read (few tokens: half of the loads)
+                auto row_box = [&](int box) { return MODE == XENT_DWEIGHT || it.row + box * 64 < a.tokens; };
+                if (rank == 0)
+                    tc_expect_tx(&sh.full[st], kTcStageBytes + 8192u * (row_box(0) + row_box(1) + row_box(2) + row_box(3)));
                 const uint32_t bar = peer_addr(smem_u32(&sh.full[st]), 0), to = stages + st * kTcStageBytes;
                 const CUtensorMap *ma = MODE == XENT_STATS || MODE == XENT_G ? &maps.hidden : &maps.g;
                 const CUtensorMap *mb = MODE == XENT_DWEIGHT ? &maps.hidden_used : &maps.w[b.piece];
                 for (int j = 0; j < 2; j++) {
+                    if (!row_box((int)rank * 2 + j)) continue;
                     const int row = (int)it.row + (int)rank * 128 + j * 64;
                     if (MODE == XENT_DHIDDEN) tc_load_box(ma, to + j * 8192, bar, (int)k * kBlock + s * 64, row);
                     else if (MODE == XENT_DWEIGHT) tc_load_box(ma, to + j * 8192, bar, row, s * 64);
@@ -391,11 +396,14 @@ __global__ void __launch_bounds__(256) xent_join_kernel(const __grid_constant__ 
         s = top == -INFINITY ? s + os : s * exp_of(m - top) + os * exp_of(om - top);
         m = top;
     };
-    if (t < a.tokens)
-        for (long long b = g; b < 2 * a.n_blocks; b += 32) {
-            const float2 v = a.stats[b * a.tokens + t];
-            add(v.x, v.y);
-        }
+    for (long long b0 = g; b0 < 2 * a.n_blocks && t < a.tokens; b0 += 32 * 8) {
+        float2 v[8];  // loads in flight together
+#pragma unroll
+        for (int k = 0; k < 8; k++)
+            v[k] = b0 + 32 * k < 2 * a.n_blocks ? __ldcg(a.stats + (b0 + 32 * k) * a.tokens + t) : make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int k = 0; k < 8; k++) add(v[k].x, v[k].y);
+    }
     sm[g][j] = m;
     ss[g][j] = s;
     __syncthreads();
@@ -437,10 +445,19 @@ __global__ void __launch_bounds__(256) xent_dhidden_join_kernel(const __grid_con
     for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (long long)gridDim.x * blockDim.x) {
         const long long t = i / vecs, d = i % vecs * 8;
         float v[8] = {};
-        for (int k = 0; k < a.splits; k++) {
-            const float4 *q = reinterpret_cast<const float4 *>(a.dh_part + (k * a.tokens + t) * a.dim + d);
-            const float4 x = q[0], y = q[1];
-            v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w, v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
+        for (int k0 = 0; k0 < a.splits; k0 += 8) {
+            float4 x[8], y[8];  // loads in flight together
+#pragma unroll
+            for (int k = 0; k < 8; k++) {
+                const float4 *q = reinterpret_cast<const float4 *>(a.dh_part + ((k0 + k) * a.tokens + t) * a.dim + d);
+                x[k] = k0 + k < a.splits ? q[0] : make_float4(0, 0, 0, 0);
+                y[k] = k0 + k < a.splits ? q[1] : make_float4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (int k = 0; k < 8; k++) {
+                v[0] += x[k].x, v[1] += x[k].y, v[2] += x[k].z, v[3] += x[k].w;
+                v[4] += y[k].x, v[5] += y[k].y, v[6] += y[k].z, v[7] += y[k].w;
+            }
         }
         *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.dhidden) + t * a.dhidden_stride + d) = narrow8_scaled<DT>(v, undo);
     }
