@@ -1,12 +1,15 @@
-"""Build the CUDA library (librar.so) in-tree with nvcc for sm_103a.
+"""Build the CUDA library (librar.so) in-tree with nvcc for sm_103a, and the
+module that calls its model operators on torch tensors (_torch_ops.so) with g++.
 
-Each translation unit compiles in its own nvcc process, in parallel, then one
+Each translation unit compiles in its own process, in parallel, then one
 link step makes the shared library.  IEEE behaviour is kept (no fast-math,
 no FMA contraction, no flush-to-zero)."""
 from __future__ import annotations
 
+import importlib.util
 import os
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -15,6 +18,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(BUILD_DIR, "librar.so")
+TORCH_OPS_PATH = os.path.join(BUILD_DIR, "_torch_ops.so")
 
 SOURCES = ["rar_api.cu", "fused.cu", "fused_stream.cu", "ring.cu", "ll.cu", "tree.cu", "noalloc.cu",
            "rmsnorm.cu", "vocab_xent.cu", "embedding.cu"]
@@ -37,10 +41,39 @@ def _inputs():
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH):
+    outputs = [LIB_PATH] + ([TORCH_OPS_PATH] if _torch_dir() else [])
+    if not all(os.path.exists(f) for f in outputs):
         return False
-    t = os.path.getmtime(LIB_PATH)
+    t = min(os.path.getmtime(f) for f in outputs)
     return all(os.path.getmtime(f) <= t for f in _inputs())
+
+
+def _torch_dir() -> str | None:
+    """Where torch is installed (it is not imported)."""
+    spec = importlib.util.find_spec("torch")
+    return os.path.dirname(spec.origin) if spec and spec.origin else None
+
+
+def _compile_torch_ops(obj: str) -> None:
+    torch_dir = _torch_dir()
+    cuda = os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-c", "-I", INCLUDE, "-I", sysconfig.get_paths()["include"],
+           "-isystem", os.path.join(torch_dir, "include"), "-isystem",
+           os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"), "-isystem", cuda,
+           os.path.join(CSRC, "torch_ops.cpp"), "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on torch_ops.cpp:\n{r.stdout}\n{r.stderr}")
+
+
+def _link_torch_ops(obj: str) -> None:
+    tmp = TORCH_OPS_PATH + f".tmp{os.getpid()}"
+    cmd = ["g++", "-shared", "-o", tmp, obj, "-L", os.path.join(_torch_dir(), "lib"), "-ltorch_python", "-ltorch_cpu",
+           "-lc10", "-lc10_cuda", "-L", BUILD_DIR, "-lrar", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"linking _torch_ops.so failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, TORCH_OPS_PATH)
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | None = None) -> str:
@@ -60,14 +93,20 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
             print(r.stdout + r.stderr)
         return obj
 
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    torch_obj = os.path.join(BUILD_DIR, "torch_ops.o")
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        torch_ops = ex.submit(_compile_torch_ops, torch_obj) if _torch_dir() else None
         objs = list(ex.map(compile_one, SOURCES))
+        if torch_ops:
+            torch_ops.result()
     tmp = LIB_PATH + f".tmp{os.getpid()}"
     cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB_PATH)
+    if torch_ops:
+        _link_torch_ops(torch_obj)
     return LIB_PATH
 
 
