@@ -24,15 +24,15 @@
 
 namespace rar {
 
-constexpr int kTcStages = 6;
-constexpr int kTcStageBytes = 32768;       // a CTA's share of A (128 x 64) and of B (128 x 64)
+constexpr int kTcMaxStages = 8;
+constexpr int kTcRingBytes = 196608;       // stages of 32 KB (128 rows of A and of B a CTA) or less
 constexpr int kTcEpilogueWarps = 8;        // two per quarter of the accumulator's lanes
 constexpr int kTcThreads = 32 * (kTcEpilogueWarps + 2);
-constexpr int kTcSmem = kTcStages * kTcStageBytes + 1024;  // + alignment to the swizzle's 1024 bytes
+constexpr int kTcSmem = kTcRingBytes + 1024;  // + alignment to the swizzle's 1024 bytes
 
 struct TcShared {
-    uint64_t full[kTcStages];   // leader: both CTAs' loads of a stage have landed
-    uint64_t empty[kTcStages];  // each CTA: the products that read a stage are done
+    uint64_t full[kTcMaxStages];   // leader: both CTAs' loads of a stage have landed
+    uint64_t empty[kTcMaxStages];  // each CTA: the products that read a stage are done
     uint64_t acc_full[2];       // each CTA: an accumulator is complete
     uint64_t acc_empty[2];      // leader: both CTAs' epilogues have read it
     uint32_t tmem;
@@ -171,12 +171,25 @@ __device__ __forceinline__ void tc_read32(uint32_t addr, float *v) {
 }
 __device__ __forceinline__ void tc_read_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
+// 32-byte accesses: a whole sector a thread.
+__device__ __forceinline__ void store_32b(void *p, const uint32_t *r) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]),
+                 "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+__device__ __forceinline__ void load_32b(const void *p, uint32_t *r) {
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "l"(p)
+                 : "memory");
+}
+
 // Barriers and tensor memory of the pair; every thread of both CTAs calls
 // these two, first and last.
 __device__ __forceinline__ void tc_begin(TcShared *sh) {
     if (threadIdx.x == 0) {
         sh->failed = 0;
-        for (int s = 0; s < kTcStages; s++) {
+        for (int s = 0; s < kTcMaxStages; s++) {
             tc_mbar_init(&sh->full[s], 1);
             tc_mbar_init(&sh->empty[s], 1);
         }

@@ -41,9 +41,9 @@ struct XentArgs {
     void *dhidden;
     bool want_dw;
     // blocks
-    long long base, extra;     // chunk_bounds(vocab, p)
-    long long nb_big, nb_small;  // blocks of a piece of base + 1 / base rows
-    long long n_blocks;
+    int base, extra;       // chunk_bounds(vocab, p)
+    int nb_big, nb_small;  // blocks of a piece of base + 1 / base rows
+    int n_blocks;
     // workspace
     float2 *stats;        // [2 n_blocks][tokens]: a half block's max, sum of exp(z - max)
     float *z_target;      // [tokens]
@@ -53,7 +53,7 @@ struct XentArgs {
     void *hidden_used;    // [tokens][dim]: hidden, zeros where left out
     void *g;              // [tokens][window * kBlock]
     float *dh_part;       // [splits][tokens][dim]
-    long long window;     // blocks of a window
+    int window;           // blocks of a window
     int splits;           // of dhidden's sum over a window
     bool direct;          // one split: the last window writes dhidden itself
     TcLimits limits;
@@ -66,25 +66,24 @@ struct XentMaps {
 
 struct BlockOf {
     int piece;
-    long long row;   // first row in the piece
-    int rows;        // 1 .. kBlock
-    long long first;  // its index in the vocabulary
+    int row;    // first row in the piece
+    int rows;   // 1 .. kBlock
+    int first;  // its index in the vocabulary
 };
-__device__ __forceinline__ BlockOf block_of(const XentArgs &a, long long b) {
+__device__ __forceinline__ BlockOf block_of(const XentArgs &a, int b) {
     BlockOf o;
-    const long long big = a.extra * a.nb_big;
-    long long k;
-    if (b < big) {
-        o.piece = (int)(b / a.nb_big);
-        k = b % a.nb_big;
+    const unsigned big = (unsigned)(a.extra * a.nb_big), u = (unsigned)b;
+    unsigned k;
+    if (u < big) {
+        o.piece = (int)(u / (unsigned)a.nb_big);
+        k = u % (unsigned)a.nb_big;
     } else {
-        o.piece = (int)(a.extra + (b - big) / a.nb_small);
-        k = (b - big) % a.nb_small;
+        o.piece = a.extra + (int)((u - big) / (unsigned)a.nb_small);
+        k = (u - big) % (unsigned)a.nb_small;
     }
-    o.row = k * kBlock;
-    const long long piece_rows = a.base + (o.piece < a.extra ? 1 : 0);
-    o.rows = (int)(piece_rows - o.row < kBlock ? piece_rows - o.row : kBlock);
-    o.first = chunk_start(o.piece, a.base, a.extra) + o.row;
+    o.row = (int)k * kBlock;
+    o.rows = min(a.base + (o.piece < a.extra ? 1 : 0) - o.row, kBlock);
+    o.first = o.piece * a.base + min(o.piece, a.extra) + o.row;
     return o;
 }
 
@@ -99,77 +98,95 @@ __device__ __forceinline__ int g_exponent(const XentArgs &a) {
     return e > 120 ? 120 : e < -120 ? -120 : e;
 }
 
-enum XentMode { XENT_STATS, XENT_G, XENT_DHIDDEN, XENT_DWEIGHT };
+// XENT_STATS, XENT_G: rows of a tile are tokens, columns a block of the
+// vocabulary.  The FEW forms turn the tile round (up to kFewTokens tokens): rows
+// are the block, columns the tokens, so that the product is no wider than
+// they are and most of the loads are of W.
+enum XentMode { XENT_STATS, XENT_G, XENT_DHIDDEN, XENT_DWEIGHT, XENT_STATS_FEW, XENT_G_FEW };
+constexpr int kFewTokens = 128;
+template <int MODE>
+struct Mode {
+    static constexpr bool few = MODE == XENT_STATS_FEW || MODE == XENT_G_FEW;
+    static constexpr bool stats = MODE == XENT_STATS || MODE == XENT_STATS_FEW, logits = stats || MODE == XENT_G || MODE == XENT_G_FEW;
+    static constexpr int stage_bytes = few ? 24576 : 32768, stages = kTcRingBytes / stage_bytes;
+    static_assert(stages <= kTcMaxStages, "barriers of a stage");
+};
 
 // One tile of a pair of CTAs: its place, and its range along K.
 struct XentItem {
-    long long row;      // first row of the tile (token, or row of the window's blocks)
-    long long col;      // first column (row of the piece, or of dim)
-    int n;              // columns that the product covers, a multiple of 32
-    long long block;    // block of the window (not XENT_DHIDDEN)
+    int row;     // first row of the tile (token, row of the window's blocks, or 0)
+    int col;     // first column (of dim, or 0)
+    int n;       // columns that the product covers, a multiple of 32
+    int block;   // block of the window (not XENT_DHIDDEN)
     int split;
-    long long k0, k1;   // XENT_DHIDDEN: blocks of the window; else steps of 64
+    int k0, k1;  // XENT_DHIDDEN: blocks of the window; else steps of 64
 };
 
-__device__ __forceinline__ int round32(long long n) { return n >= kTile ? kTile : (int)((n + 31) / 32 * 32); }
+__host__ __device__ inline int tiles_of(long long n) { return (int)((n + kTile - 1) / kTile); }
+__device__ __forceinline__ int round32(int n) { return n >= kTile ? kTile : (n + 31) / 32 * 32; }
 
 // Tiles in an order in which those that run at one time share operands:
 // columns of 8 tiles, so that 76 pairs work on about 8 x 9 tiles.
 template <int MODE>
-__device__ __forceinline__ XentItem xent_item(const XentArgs &a, long long b0, long long nb, long long i) {
+__device__ __forceinline__ XentItem xent_item(const XentArgs &a, int b0, int nb, int i) {
     XentItem o;
-    const long long tb = (a.tokens + kTile - 1) / kTile, db = (a.dim + kTile - 1) / kTile;
-    const long long rows = MODE == XENT_DWEIGHT ? nb : tb;
-    const long long cols = MODE == XENT_DHIDDEN ? db * a.splits : MODE == XENT_DWEIGHT ? db : nb;
-    const long long g = i / (8 * cols), in = i - g * 8 * cols;
-    const long long width = rows - g * 8 < 8 ? rows - g * 8 : 8;
-    const long long r = g * 8 + in % width, c = in / width;
     o.split = 0;
     o.block = 0;
+    o.col = 0;
+    o.k0 = 0;
+    if (Mode<MODE>::few) {
+        o.row = 0;
+        o.block = i;
+        o.n = round32((int)a.tokens);
+        o.k1 = (int)((a.dim + 63) / 64);
+        return o;
+    }
+    const unsigned tb = (unsigned)tiles_of(a.tokens), db = (unsigned)tiles_of(a.dim);
+    const unsigned rows = MODE == XENT_DWEIGHT ? (unsigned)nb : tb;
+    const unsigned cols = MODE == XENT_DHIDDEN ? db * (unsigned)a.splits : MODE == XENT_DWEIGHT ? db : (unsigned)nb;
+    const unsigned g = (unsigned)i / (8 * cols), in = (unsigned)i - g * 8 * cols;
+    const unsigned width = min(rows - g * 8, 8u), c = in / width;
+    const int r = (int)(g * 8 + in - c * width);
+    o.row = r * kTile;
     if (MODE == XENT_STATS || MODE == XENT_G) {
-        o.row = r * kTile;
-        o.block = c;
-        o.col = 0;
-        o.n = round32(block_of(a, b0 + c).rows);
-        o.k0 = 0;
-        o.k1 = (a.dim + 63) / 64;
+        o.block = (int)c;
+        o.n = round32(block_of(a, b0 + (int)c).rows);
+        o.k1 = (int)((a.dim + 63) / 64);
     } else if (MODE == XENT_DHIDDEN) {
-        o.row = r * kTile;
         o.split = (int)(c / db);
-        o.col = c % db * kTile;
-        o.n = round32(a.dim - o.col);
-        o.k0 = nb * o.split / a.splits;
-        o.k1 = nb * (o.split + 1) / a.splits;
+        o.col = (int)(c % db) * kTile;
+        o.n = round32((int)a.dim - o.col);
+        o.k0 = (int)((long long)nb * o.split / a.splits);
+        o.k1 = (int)((long long)nb * (o.split + 1) / a.splits);
     } else {
-        o.row = r * kTile;
         o.block = r;
-        o.col = c * kTile;
-        o.n = round32(a.dim - o.col);
-        o.k0 = 0;
-        o.k1 = (a.tokens + 63) / 64;
+        o.col = (int)c * kTile;
+        o.n = round32((int)a.dim - o.col);
+        o.k1 = (int)((a.tokens + 63) / 64);
     }
     return o;
 }
 template <int MODE>
-__host__ __device__ inline long long xent_items(const XentArgs &a, long long nb) {
-    const long long tb = (a.tokens + kTile - 1) / kTile, db = (a.dim + kTile - 1) / kTile;
+__host__ __device__ inline int xent_items(const XentArgs &a, int nb) {
+    if (Mode<MODE>::few) return nb;
+    const int tb = tiles_of(a.tokens), db = tiles_of(a.dim);
     return MODE == XENT_DHIDDEN ? tb * db * a.splits : MODE == XENT_DWEIGHT ? nb * db : tb * nb;
 }
 
-// Calls f(k) for every step of 64 along K: f(step within the block or the
-// range, block).  Stops when f returns false.
+// Calls f for every step of 64 along K: f(step within the block or the
+// range, block of the window, the block).  Stops when f returns false.
 template <int MODE, typename F>
-__device__ __forceinline__ bool xent_steps(const XentArgs &a, long long b0, const XentItem &it, F &&f) {
+__device__ __forceinline__ bool xent_steps(const XentArgs &a, int b0, const XentItem &it, F &&f) {
     if constexpr (MODE == XENT_DHIDDEN) {
-        for (long long k = it.k0; k < it.k1; k++) {
+        for (int k = it.k0; k < it.k1; k++) {
             const BlockOf b = block_of(a, b0 + k);
             for (int s = 0; s * 64 < b.rows; s++)
                 if (!f(s, k, b)) return false;
         }
     } else {
         const BlockOf b = block_of(a, b0 + it.block);
-        for (long long s = it.k0; s < it.k1; s++)
-            if (!f((int)s, it.block, b)) return false;
+        for (int s = it.k0; s < it.k1; s++)
+            if (!f(s, it.block, b)) return false;
     }
     return true;
 }
@@ -188,131 +205,214 @@ __device__ __forceinline__ uint4 narrow8_scaled(const float *v, float scale) {
     return narrow8<DT>(f);
 }
 
-// A thread's part of a finished tile: one row, 128 columns from `half`.
+// What an epilogue thread keeps of a tile: one row of it.
+struct XentRow {
+    int row;          // of tokens (or of the block, XENT_DWEIGHT)
+    bool live;        // the row exists
+    int cols;         // columns of its half that exist
+    int target;       // column of its target in its half, or one out of range
+    float w, lse;     // XENT_G
+    float max, sum;   // XENT_STATS
+    char *out;        // where the row's half begins
+    float *part;      // XENT_DHIDDEN: the sums so far
+};
+
 template <int MODE, int DT>
-__device__ __forceinline__ void xent_epilogue(const XentArgs &a, long long b0, long long nb, const XentItem &it, long long row,
-                                              int half, float (&v)[128]) {
-    if constexpr (MODE == XENT_STATS) {
+__device__ __forceinline__ XentRow xent_row(const XentArgs &a, int b0, const XentItem &it, int row, int half) {
+    XentRow r;
+    r.row = row;
+    r.out = nullptr;
+    r.part = nullptr;
+    if constexpr (MODE == XENT_DHIDDEN) {
+        r.live = row < a.tokens;
+        r.cols = (int)a.dim - it.col - half;
+        r.out = static_cast<char *>(a.dhidden) + (row * a.dhidden_stride + it.col + half) * 2;
+        r.part = a.dh_part + ((long long)it.split * a.tokens + row) * a.dim + it.col + half;
+    } else if constexpr (MODE == XENT_DWEIGHT) {
         const BlockOf b = block_of(a, b0 + it.block);
-        if (row >= a.tokens) return;
-        const int cols = b.rows - half;
-        float m = -INFINITY, s = 0.0f;
-        const long long y = load_index(a.targets, a.index_bytes, row) - b.first - half;
-        if (y >= 0 && y < cols && y < 128) {
+        r.row = row - it.row;
+        r.live = r.row < b.rows;
+        r.cols = (int)a.dim - it.col - half;
+        r.out = rank_ptr(a.dw, a.p, b.piece) + ((long long)(b.row + r.row) * a.dweight_stride + it.col + half) * 2;
+    } else {
+        const BlockOf b = block_of(a, b0 + it.block);
+        r.live = row < a.tokens;
+        r.cols = b.rows - half;
+        const long long y = r.live ? load_index(a.targets, a.index_bytes, row) - b.first - half : -1;
+        r.target = y >= 0 && y < r.cols ? (int)y : -1;
+        r.max = -INFINITY;
+        r.sum = 0.0f;
+        if constexpr (MODE == XENT_G) {
+            r.w = r.live ? ldexpf(a.row_weight[row], g_exponent<DT>(a)) : 0.0f;
+            r.lse = r.live ? a.lse_ws[row] : 0.0f;
+            r.out = static_cast<char *>(a.g) + (((long long)row * a.window + it.block) * kBlock + half) * 2;
+        }
+    }
+    return r;
+}
+
+// Columns c0 .. c0 + 31 of the row's half.
+template <int MODE, int DT>
+__device__ __forceinline__ void xent_columns(const XentArgs &a, XentRow &r, int c0, float undo, bool first, bool direct, float (&v)[32]) {
+    if (!r.live) return;
+    const int cols = r.cols - c0;
+    if constexpr (MODE == XENT_STATS) {
+        if (cols <= 0) return;
+        if (cols < 32) {
+#pragma unroll
+            for (int c = 0; c < 32; c++) v[c] = c < cols ? v[c] : -INFINITY;
+        }
+        const int y = r.target - c0;
+        if (y >= 0 && y < 32) {
             float z = 0.0f;
 #pragma unroll
-            for (int c = 0; c < 128; c++)  // (in this form v stays in registers)
-                asm("{\n\t.reg .pred P;\n\tsetp.eq.s32 P, %1, %2;\n\tselp.f32 %0, %3, %0, P;\n\t}" : "+f"(z) : "r"((int)y), "r"(c), "f"(v[c]));
-            a.z_target[row] = z;
+            for (int c = 0; c < 32; c++)  // (in this form v stays in registers)
+                asm("{\n\t.reg .pred P;\n\tsetp.eq.s32 P, %1, %2;\n\tselp.f32 %0, %3, %0, P;\n\t}" : "+f"(z) : "r"(y), "r"(c), "f"(v[c]));
+            a.z_target[r.row] = z;
         }
-        if (cols < 128) {
+        float m = r.max;
 #pragma unroll
-            for (int c = 0; c < 128; c++) v[c] = c < cols ? v[c] : -INFINITY;
-        }
-#pragma unroll
-        for (int c = 0; c < 128; c++) m = fmaxf(m, v[c]);
+        for (int c = 0; c < 32; c++) m = fmaxf(m, v[c]);
         // nothing but -inf (or NaN, which the sum then shows)
         const float ref = m == -INFINITY ? 0.0f : m;
+        float s = r.sum * exp_of(r.max - ref);
 #pragma unroll
-        for (int c = 0; c < 128; c++) s += exp_of(v[c] - ref);
-        a.stats[(2 * (b0 + it.block) + half / 128) * a.tokens + row] = make_float2(m, s);
+        for (int c = 0; c < 32; c++) s += exp_of(v[c] - ref);
+        r.max = m;
+        r.sum = s;
     } else if constexpr (MODE == XENT_G) {
-        const BlockOf b = block_of(a, b0 + it.block);
-        if (row >= a.tokens) return;
-        const int cols = b.rows - half;
-        const float w = ldexpf(a.row_weight[row], g_exponent<DT>(a)), lse = a.lse_ws[row];
-        const long long y = load_index(a.targets, a.index_bytes, row) - b.first - half;
-        uint4 *out = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.g) + (row * a.window + it.block) * kBlock + half);
-        const bool hit = y >= 0 && y < 128;
+        const int y = r.target - c0;
 #pragma unroll
-        for (int c = 0; c < 128; c++) {
-            const float p = exp_of(v[c] - lse) - (hit && c == (int)y ? 1.0f : 0.0f);
-            v[c] = c < cols && w != 0.0f ? p * w : 0.0f;
+        for (int c = 0; c < 32; c++) {
+            const float p = exp_of(v[c] - r.lse) - (c == y ? 1.0f : 0.0f);
+            v[c] = c < cols && r.w != 0.0f ? p * r.w : 0.0f;
         }
 #pragma unroll
-        for (int c = 0; c < 128; c += 8) out[c / 8] = narrow8<DT>(v + c);
+        for (int c = 0; c < 32; c += 16) {
+            const uint4 x = narrow8<DT>(v + c), y4 = narrow8<DT>(v + c + 8);
+            const uint32_t q[8] = {x.x, x.y, x.z, x.w, y4.x, y4.y, y4.z, y4.w};
+            store_32b(r.out + (c0 + c) * 2, q);
+        }
     } else if constexpr (MODE == XENT_DHIDDEN) {
-        if (row >= a.tokens) return;
-        const float undo = ldexpf(1.0f, -g_exponent<DT>(a));
-        const bool first = b0 == 0, last = b0 + nb == a.n_blocks;
-        float *part = a.dh_part + (it.split * a.tokens + row) * a.dim;
 #pragma unroll
-        for (int c = 0; c < 128; c += 8) {
-            const long long d = it.col + half + c;
-            if (d >= a.dim) continue;
-            float4 *q = reinterpret_cast<float4 *>(part + d);
+        for (int c = 0; c < 32; c += 8) {
+            if (c >= cols) continue;
+            float *part = r.part + c0 + c;
             if (!first) {
-                const float4 x = q[0], y = q[1];
-                v[c] += x.x, v[c + 1] += x.y, v[c + 2] += x.z, v[c + 3] += x.w;
-                v[c + 4] += y.x, v[c + 5] += y.y, v[c + 6] += y.z, v[c + 7] += y.w;
+                uint32_t q[8];
+                load_32b(part, q);
+#pragma unroll
+                for (int e = 0; e < 8; e++) v[c + e] += __uint_as_float(q[e]);
             }
-            if (last && a.direct) {
-                *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.dhidden) + row * a.dhidden_stride + d) = narrow8_scaled<DT>(v + c, undo);
+            if (direct) {
+                *reinterpret_cast<uint4 *>(r.out + (c0 + c) * 2) = narrow8_scaled<DT>(v + c, undo);
             } else {
-                q[0] = make_float4(v[c], v[c + 1], v[c + 2], v[c + 3]);
-                q[1] = make_float4(v[c + 4], v[c + 5], v[c + 6], v[c + 7]);
+                uint32_t q[8];
+#pragma unroll
+                for (int e = 0; e < 8; e++) q[e] = __float_as_uint(v[c + e]);
+                store_32b(part, q);
             }
         }
     } else {
-        const BlockOf b = block_of(a, b0 + it.block);
-        const long long r = row - it.row;
-        if (r >= b.rows) return;
-        const float undo = ldexpf(1.0f, -g_exponent<DT>(a));
-        uint16_t *out = reinterpret_cast<uint16_t *>(rank_ptr(a.dw, a.p, b.piece)) + (b.row + r) * a.dweight_stride;
 #pragma unroll
-        for (int c = 0; c < 128; c += 8) {
-            const long long d = it.col + half + c;
-            if (d < a.dim) *reinterpret_cast<uint4 *>(out + d) = narrow8_scaled<DT>(v + c, undo);
+        for (int c = 0; c < 32; c += 8)
+            if (c < cols) *reinterpret_cast<uint4 *>(r.out + (c0 + c) * 2) = narrow8_scaled<DT>(v + c, undo);
+    }
+}
+
+struct XentFew {
+    float2 part[2][4][kFewTokens];  // by tile parity and quarter of the rows: max and sum of a token
+    int target[kFewTokens];         // index in the vocabulary, or -1
+    float w[kFewTokens], lse[kFewTokens];
+};
+// Barrier 1: the epilogue warps only.
+__device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kTcEpilogueWarps) : "memory"); }
+
+// The epilogue of the FEW forms: lanes are rows of the block, so a token's
+// statistics are reduced over the lanes.  A warp's columns (tokens) are
+// [half, half + count).
+template <int MODE, int DT>
+__device__ __forceinline__ void few_columns(const XentArgs &a, const BlockOf &b, int block, int parity, XentFew &few, int row, int quarter,
+                                            int t0, int count, float (&v)[32]) {
+    const bool live = row < b.rows;
+    const int index = b.first + row;
+#pragma unroll
+    for (int c = 0; c < 32; c++) {
+        const int t = t0 + c;
+        if (c >= count) break;
+        if constexpr (MODE == XENT_STATS_FEW) {
+            const float z = live ? v[c] : -INFINITY;
+            if (live && few.target[t] == index) a.z_target[t] = z;
+            float m = z;
+#pragma unroll
+            for (int o = 16; o; o /= 2) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+            const float s = warp_sum(exp_of(z - (m == -INFINITY ? 0.0f : m)));
+            if (threadIdx.x % 32 == 0) few.part[parity][quarter][t] = make_float2(m, s);
+        } else {
+            const float w = few.w[t], p = exp_of(v[c] - few.lse[t]) - (few.target[t] == index ? 1.0f : 0.0f);
+            store_f<DT>(a.g, ((long long)t * a.window + block) * kBlock + row, live && w != 0.0f ? p * w : 0.0f);
         }
     }
 }
 
+// Adds sums of exponentials, each relative to its maximum.
+__device__ __forceinline__ void add_exp(float &m, float &s, float om, float os) {
+    if (os == 0.0f) return;  // nothing there
+    const float top = fmaxf(m, om);
+    // (a block of -inf or NaN alone has a sum of its own to keep)
+    s = top == -INFINITY ? s + os : s * exp_of(m - top) + os * exp_of(om - top);
+    m = top;
+}
+
 // Persistent: a pair of CTAs takes tiles i, i + pairs, ...  Warps 0 to 7: epilogue,
-// 8: loads, 9 (of the pair's first CTA): products.
+// 8: loads, 9 (of the pair's first CTA): products.  The epilogue reads its half
+// row 32 columns at a time: the code of all 128 at once is four times as long, and
+// its instruction fetches showed in calls of a few tiles.
 template <int MODE, int DT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
-    xent_tile_kernel(const __grid_constant__ XentArgs a, const __grid_constant__ XentMaps maps, long long b0, long long nb) {
+    xent_tile_kernel(const __grid_constant__ XentArgs a, const __grid_constant__ XentMaps maps, int b0, int nb) {
     extern __shared__ unsigned char dyn[];
     __shared__ TcShared sh;
+    constexpr bool kFew = Mode<MODE>::few;
+    constexpr int kStages = Mode<MODE>::stages, kStageBytes = Mode<MODE>::stage_bytes;
     const uint32_t stages = (smem_u32(dyn) + 1023u) & ~1023u;
     const uint32_t rank = cluster_rank();
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     tc_begin(&sh);
     pdl_wait();
     pdl_launch_dependents();
-    if (MODE == XENT_STATS && blockIdx.x == 0 && threadIdx.x == 0) *a.w_max = 0u;
-    const long long items = xent_items<MODE>(a, nb);
-    const long long pairs = gridDim.x / 2, first = blockIdx.x / 2;
+    if (Mode<MODE>::stats && blockIdx.x == 0 && threadIdx.x == 0) *a.w_max = 0u;
+    const int items = xent_items<MODE>(a, nb), pairs = gridDim.x / 2, first = blockIdx.x / 2;
     constexpr bool a_mn = MODE == XENT_DWEIGHT, b_mn = MODE == XENT_DHIDDEN || MODE == XENT_DWEIGHT;
 
     if (warp == kTcEpilogueWarps && lane == 0) {
-        long long step = 0;
-        for (long long i = first; i < items && !*(volatile int *)&sh.failed; i += pairs) {
+        unsigned step = 0;
+        for (int i = first; i < items && !*(volatile int *)&sh.failed; i += pairs) {
             const XentItem it = xent_item<MODE>(a, b0, nb, i);
             const int half = (int)rank * it.n / 2;
-            xent_steps<MODE>(a, b0, it, [&](int s, long long k, const BlockOf &b) {
-                const int st = (int)(step % kTcStages);
-                if (step >= kTcStages && !tc_wait(&sh, a.limits, &sh.empty[st], (uint32_t)(step / kTcStages - 1) & 1, 0)) return false;
-                // boxes of tokens past the last are not loaded: their rows of the
-                // accumulator are never read (few tokens: half of the loads)
-                auto row_box = [&](int box) { return MODE == XENT_DWEIGHT || it.row + box * 64 < a.tokens; };
+            xent_steps<MODE>(a, b0, it, [&](int s, int k, const BlockOf &b) {
+                const int st = (int)(step % kStages);
+                if (step >= kStages && !tc_wait(&sh, a.limits, &sh.empty[st], (step / kStages - 1) & 1, 0)) return false;
+                // boxes past the last row are not loaded: their rows of the accumulator
+                // are never read (few tokens: half of the loads)
+                auto row_box = [&](int box) { return MODE == XENT_DWEIGHT || (kFew ? box * 64 < b.rows : it.row + box * 64 < a.tokens); };
                 if (rank == 0)
-                    tc_expect_tx(&sh.full[st], kTcStageBytes + 8192u * (row_box(0) + row_box(1) + row_box(2) + row_box(3)));
-                const uint32_t bar = peer_addr(smem_u32(&sh.full[st]), 0), to = stages + st * kTcStageBytes;
-                const CUtensorMap *ma = MODE == XENT_STATS || MODE == XENT_G ? &maps.hidden : &maps.g;
-                const CUtensorMap *mb = MODE == XENT_DWEIGHT ? &maps.hidden_used : &maps.w[b.piece];
+                    tc_expect_tx(&sh.full[st], (kFew ? 16384u : 32768u) + 8192u * (row_box(0) + row_box(1) + row_box(2) + row_box(3)));
+                const uint32_t bar = peer_addr(smem_u32(&sh.full[st]), 0), to = stages + st * kStageBytes;
+                const CUtensorMap *ma = kFew ? &maps.w[b.piece] : Mode<MODE>::logits ? &maps.hidden : &maps.g;
+                const CUtensorMap *mb = kFew ? &maps.hidden : MODE == XENT_DWEIGHT ? &maps.hidden_used : &maps.w[b.piece];
                 for (int j = 0; j < 2; j++) {
                     if (!row_box((int)rank * 2 + j)) continue;
-                    const int row = (int)it.row + (int)rank * 128 + j * 64;
-                    if (MODE == XENT_DHIDDEN) tc_load_box(ma, to + j * 8192, bar, (int)k * kBlock + s * 64, row);
+                    const int row = (kFew ? b.row : it.row) + (int)rank * 128 + j * 64;
+                    if (MODE == XENT_DHIDDEN) tc_load_box(ma, to + j * 8192, bar, k * kBlock + s * 64, row);
                     else if (MODE == XENT_DWEIGHT) tc_load_box(ma, to + j * 8192, bar, row, s * 64);
                     else tc_load_box(ma, to + j * 8192, bar, s * 64, row);
                 }
-                for (int j = 0; j < 2; j++) {
-                    const int col = (int)it.col + half + j * 64;
-                    if (MODE == XENT_DHIDDEN) tc_load_box(mb, to + 16384 + j * 8192, bar, col, (int)b.row + s * 64);
+                for (int j = 0; j < (kFew ? 1 : 2); j++) {
+                    const int col = it.col + half + j * 64;
+                    if (MODE == XENT_DHIDDEN) tc_load_box(mb, to + 16384 + j * 8192, bar, col, b.row + s * 64);
                     else if (MODE == XENT_DWEIGHT) tc_load_box(mb, to + 16384 + j * 8192, bar, col, s * 64);
-                    else tc_load_box(mb, to + 16384 + j * 8192, bar, s * 64, (int)b.row + col);
+                    else tc_load_box(mb, to + 16384 + j * 8192, bar, s * 64, kFew ? col : b.row + col);
                 }
                 step++;
                 return true;
@@ -320,25 +420,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
         }
         // neither CTA may leave while the pair's loads or arrivals are on their
         // way (the loads even after a wait that ran out)
-        for (long long k = step > kTcStages ? step - kTcStages : 0; k < step; k++) {
-            const int st = (int)(k % kTcStages);
-            if (rank == 0) tc_drain(&sh.full[st], (uint32_t)(k / kTcStages) & 1);
-            tc_wait(&sh, a.limits, &sh.empty[st], (uint32_t)(k / kTcStages) & 1, 1);
+        for (unsigned k = step > kStages ? step - kStages : 0; k < step; k++) {
+            const int st = (int)(k % kStages);
+            if (rank == 0) tc_drain(&sh.full[st], (k / kStages) & 1);
+            tc_wait(&sh, a.limits, &sh.empty[st], (k / kStages) & 1, 1);
         }
     } else if (warp == kTcEpilogueWarps + 1 && lane == 0 && rank == 0) {
-        long long step = 0, tile = 0;
-        for (long long i = first; i < items; i += pairs, tile++) {
+        unsigned step = 0, tile = 0;
+        for (int i = first; i < items; i += pairs, tile++) {
             const XentItem it = xent_item<MODE>(a, b0, nb, i);
             const int acc = (int)(tile & 1);
-            if (tile >= 2 && !tc_wait(&sh, a.limits, &sh.acc_empty[acc], (uint32_t)(tile / 2 - 1) & 1, 2)) break;
+            if (tile >= 2 && !tc_wait(&sh, a.limits, &sh.acc_empty[acc], (tile / 2 - 1) & 1, 2)) break;
             tc_fence_after();
             const uint32_t d = sh.tmem + acc * kTile, idesc = tc_instruction(DT == DT_BF16, a_mn, b_mn, (uint32_t)it.n);
             bool more = false;
-            const bool ok = xent_steps<MODE>(a, b0, it, [&](int, long long, const BlockOf &) {
-                const int st = (int)(step % kTcStages);
-                if (!tc_wait(&sh, a.limits, &sh.full[st], (uint32_t)(step / kTcStages) & 1, 3)) return false;
+            const bool ok = xent_steps<MODE>(a, b0, it, [&](int, int, const BlockOf &) {
+                const int st = (int)(step % kStages);
+                if (!tc_wait(&sh, a.limits, &sh.full[st], (step / kStages) & 1, 3)) return false;
                 tc_fence_after();
-                const uint32_t pa = stages + st * kTcStageBytes, pb = pa + 16384;
+                const uint32_t pa = stages + st * kStageBytes, pb = pa + 16384;
 #pragma unroll
                 for (int k = 0; k < 4; k++) {
                     const uint64_t da = tc_operand(pa + k * (a_mn ? 2048 : 32), a_mn ? 8192 : 16, 1024);
@@ -354,23 +454,59 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
             tc_commit(&sh.acc_full[acc]);
         }
     } else if (warp < kTcEpilogueWarps) {
-        const int quarter = warp % 4, half = warp / 4 * 128;
-        long long tile = 0;
-        for (long long i = first; i < items; i += pairs, tile++) {
+        const int quarter = warp % 4;
+        const float undo = MODE == XENT_DHIDDEN || MODE == XENT_DWEIGHT ? ldexpf(1.0f, -g_exponent<DT>(a)) : 1.0f;
+        const bool first_window = b0 == 0, direct = a.direct && b0 + nb == a.n_blocks;
+        __shared__ XentFew few;
+        if (kFew) {
+            const int t = threadIdx.x;
+            if (t < kFewTokens && t < a.tokens) {
+                const long long y = load_index(a.targets, a.index_bytes, t);
+                few.target[t] = y >= 0 && y < a.vocab ? (int)y : -1;
+                if (MODE == XENT_G_FEW) {
+                    few.w[t] = ldexpf(a.row_weight[t], g_exponent<DT>(a));
+                    few.lse[t] = a.lse_ws[t];
+                }
+            }
+            epilogue_sync();
+        }
+        unsigned tile = 0;
+        for (int i = first; i < items; i += pairs, tile++) {
             const XentItem it = xent_item<MODE>(a, b0, nb, i);
-            const int acc = (int)(tile & 1);
-            if (!tc_wait(&sh, a.limits, &sh.acc_full[acc], (uint32_t)(tile / 2) & 1, 4)) break;
+            const int acc = (int)(tile & 1), half = kFew ? warp / 4 * (it.n / 2) : warp / 4 * 128;
+            const int count = kFew ? min(it.n / 2, (int)a.tokens - half) : 128;  // columns of the half
+            const int row = (kFew ? 0 : it.row) + (int)rank * 128 + quarter * 32 + lane;
+            XentRow r;
+            BlockOf b;
+            if constexpr (kFew) b = block_of(a, b0 + it.block);
+            else r = xent_row<MODE, DT>(a, b0, it, row, half);
+            const bool ok = tc_wait(&sh, a.limits, &sh.acc_full[acc], (tile / 2) & 1, 4);
+            if (!ok && !kFew) break;  // (FEW: the warps still meet at their barriers)
             __syncwarp();
             tc_fence_after();
-            float v[128];
             const uint32_t at = sh.tmem + ((uint32_t)quarter << 21) + acc * kTile + half;
-#pragma unroll
-            for (int c = 0; c < 128; c += 32) tc_read32(at + c, v + c);
-            tc_read_wait();
+#pragma unroll 1
+            for (int c0 = 0; c0 < count; c0 += 32) {
+                float v[32];
+                tc_read32(at + c0, v);
+                tc_read_wait();
+                if constexpr (kFew) few_columns<MODE, DT>(a, b, it.block, acc, few, row, quarter, half + c0, count - c0, v);
+                else xent_columns<MODE, DT>(a, r, c0, undo, first_window, direct, v);
+            }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) tc_arrive_cluster(peer_addr(smem_u32(&sh.acc_empty[acc]), 0));
-            xent_epilogue<MODE, DT>(a, b0, nb, it, it.row + rank * 128 + quarter * 32 + lane, half, v);
+            if constexpr (MODE == XENT_STATS)
+                if (r.live) a.stats[(2ll * (b0 + it.block) + half / 128) * a.tokens + row] = make_float2(r.max, r.sum);
+            if constexpr (MODE == XENT_STATS_FEW) {  // the four warps of a token
+                epilogue_sync();
+                const int t = threadIdx.x;
+                if (t < a.tokens) {
+                    float m = -INFINITY, s = 0.0f;
+                    for (int q = 0; q < 4; q++) add_exp(m, s, few.part[acc][q][t].x, few.part[acc][q][t].y);
+                    a.stats[(2ll * (b0 + it.block) + rank) * a.tokens + t] = make_float2(m, s);
+                }
+            }
         }
     }
     __syncwarp();
@@ -389,20 +525,15 @@ __global__ void __launch_bounds__(256) xent_join_kernel(const __grid_constant__ 
     const int j = threadIdx.x % 8, g = threadIdx.x / 8;
     const long long t0 = (long long)blockIdx.x * 8, t = t0 + j;
     float m = -INFINITY, s = 0.0f;
-    auto add = [&](float om, float os) {
-        if (os == 0.0f) return;  // an empty half block
-        const float top = fmaxf(m, om);
-        // (a block of -inf or NaN alone has a sum of its own to keep)
-        s = top == -INFINITY ? s + os : s * exp_of(m - top) + os * exp_of(om - top);
-        m = top;
-    };
-    for (long long b0 = g; b0 < 2 * a.n_blocks && t < a.tokens; b0 += 32 * 8) {
+    auto add = [&](float om, float os) { add_exp(m, s, om, os); };
+    const int n = 2 * a.n_blocks;
+    for (int b0 = g; b0 < n && t < a.tokens; b0 += 32 * 8) {
         float2 v[8];  // loads in flight together
 #pragma unroll
-        for (int k = 0; k < 8; k++)
-            v[k] = b0 + 32 * k < 2 * a.n_blocks ? __ldcg(a.stats + (b0 + 32 * k) * a.tokens + t) : make_float2(0.0f, 0.0f);
+        for (int k = 0; k < 8; k++) v[k] = __ldcg(a.stats + (long long)min(b0 + 32 * k, n - 1) * a.tokens + t);
 #pragma unroll
-        for (int k = 0; k < 8; k++) add(v[k].x, v[k].y);
+        for (int k = 0; k < 8; k++)
+            if (b0 + 32 * k < n) add(v[k].x, v[k].y);
     }
     sm[g][j] = m;
     ss[g][j] = s;
@@ -427,11 +558,21 @@ __global__ void __launch_bounds__(256) xent_join_kernel(const __grid_constant__ 
     }
     if (!GRAD) return;
     __syncthreads();
-    const long long vecs = a.dim / 8;
-    for (int k = 0; k < 8 && t0 + k < a.tokens; k++) {
-        const uint4 *from = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.hidden) + (t0 + k) * a.hidden_stride);
-        uint4 *to = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.hidden_used) + (t0 + k) * a.dim);
-        for (long long i = threadIdx.x; i < vecs; i += blockDim.x) to[i] = counts[k] ? from[i] : make_uint4(0, 0, 0, 0);
+    const int vecs = (int)(a.dim / 8), total = vecs * (int)(a.tokens - t0 < 8 ? a.tokens - t0 : 8);
+    for (int i0 = threadIdx.x; i0 < total; i0 += 4 * 256) {
+        uint4 q[4];  // loads in flight together
+#pragma unroll
+        for (int u = 0; u < 4; u++) {
+            const int i = min(i0 + u * 256, total - 1), k = i / vecs;
+            q[u] = *(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.hidden) + (t0 + k) * a.hidden_stride) + (i - k * vecs));
+        }
+#pragma unroll
+        for (int u = 0; u < 4; u++) {
+            const int i = i0 + u * 256, k = i / vecs;
+            if (i < total)
+                *(reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.hidden_used) + (t0 + k) * a.dim) + (i - k * vecs)) =
+                    counts[k] ? q[u] : make_uint4(0, 0, 0, 0);
+        }
     }
 }
 
@@ -443,21 +584,19 @@ __global__ void __launch_bounds__(256) xent_dhidden_join_kernel(const __grid_con
     const float undo = ldexpf(1.0f, -g_exponent<DT>(a));
     const long long vecs = a.dim / 8, n = a.tokens * vecs;
     for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (long long)gridDim.x * blockDim.x) {
-        const long long t = i / vecs, d = i % vecs * 8;
+        const long long t = n < 0x7FFFFFFF ? (long long)((uint32_t)i / (uint32_t)vecs) : i / vecs, d = (i - t * vecs) * 8;
+        const float *part = a.dh_part + t * a.dim + d;
+        const long long pitch = a.tokens * a.dim;
         float v[8] = {};
-        for (int k0 = 0; k0 < a.splits; k0 += 8) {
-            float4 x[8], y[8];  // loads in flight together
+        for (int k0 = 0; k0 < a.splits; k0 += 4) {
+            uint32_t q[4][8];  // loads in flight together
 #pragma unroll
-            for (int k = 0; k < 8; k++) {
-                const float4 *q = reinterpret_cast<const float4 *>(a.dh_part + ((k0 + k) * a.tokens + t) * a.dim + d);
-                x[k] = k0 + k < a.splits ? q[0] : make_float4(0, 0, 0, 0);
-                y[k] = k0 + k < a.splits ? q[1] : make_float4(0, 0, 0, 0);
-            }
+            for (int k = 0; k < 4; k++) load_32b(part + min(k0 + k, a.splits - 1) * pitch, q[k]);
 #pragma unroll
-            for (int k = 0; k < 8; k++) {
-                v[0] += x[k].x, v[1] += x[k].y, v[2] += x[k].z, v[3] += x[k].w;
-                v[4] += y[k].x, v[5] += y[k].y, v[6] += y[k].z, v[7] += y[k].w;
-            }
+            for (int k = 0; k < 4; k++)
+                if (k0 + k < a.splits)
+#pragma unroll
+                    for (int e = 0; e < 8; e++) v[e] += __uint_as_float(q[k][e]);
         }
         *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.dhidden) + t * a.dhidden_stride + d) = narrow8_scaled<DT>(v, undo);
     }
@@ -497,17 +636,17 @@ bool make_map(CUtensorMap *m, int dtype, const void *ptr, long long rows, long l
 }
 
 template <int MODE, int DT>
-cudaError_t launch_tiles(const rar_ctx *h, const XentArgs &k, const XentMaps &maps, long long b0, long long nb, cudaStream_t stream) {
+cudaError_t launch_tiles(const rar_ctx *h, const XentArgs &k, const XentMaps &maps, int b0, int nb, cudaStream_t stream) {
     auto kern = xent_tile_kernel<MODE, DT>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcSmem);
     if (e != cudaSuccess) return e;
-    const long long pairs = std::min<long long>(xent_items<MODE>(k, nb), h->sm_count / 2);
+    const int pairs = std::min(xent_items<MODE>(k, nb), h->sm_count / 2);
     return launch_pdl(kern, dim3((unsigned)(2 * pairs)), dim3(kTcThreads), kTcSmem, stream, k, maps, b0, nb);
 }
 
 void plan_blocks(size_t vocab, int p, XentArgs *k) {
-    k->base = (long long)(vocab / p);
-    k->extra = (long long)(vocab % p);
+    k->base = (int)(vocab / p);
+    k->extra = (int)(vocab % p);
     k->nb_big = (k->base + 1 + kBlock - 1) / kBlock;
     k->nb_small = (k->base + kBlock - 1) / kBlock;
     k->n_blocks = k->extra * k->nb_big + (p - k->extra) * k->nb_small;
@@ -527,7 +666,7 @@ size_t plan(void *base, size_t tokens, size_t dim, size_t vocab, int p, bool gra
         k->hidden_used = w.take<uint16_t>(tokens * dim);
         size_t window = kWindowBytes / (sizeof(uint16_t) * kBlock * std::max<size_t>(tokens, 1));
         window = std::min(std::max<size_t>(window, 1), n_blocks);
-        k->window = (long long)window;
+        k->window = (int)window;
         k->g = w.take<uint16_t>(tokens * window * kBlock);
         // few tiles: dhidden's sum over the window is split until there are
         // about two tiles a pair of SMs
@@ -541,9 +680,11 @@ size_t plan(void *base, size_t tokens, size_t dim, size_t vocab, int p, bool gra
 }
 
 bool sizes_ok(size_t tokens, size_t dim, size_t vocab, int p) {
-    const size_t most = (size_t)1 << 40;
-    return p >= 1 && p <= kInlineP && dim >= 1 && vocab >= 1 && tokens <= most && dim <= most / 1024 && vocab <= 0x7FFFFFFFu &&
-           tokens <= (((size_t)1 << 58) / std::max(dim, vocab)) && dim % 8 == 0;
+    return p >= 1 && p <= kInlineP && dim >= 1 && vocab >= 1 && vocab <= 0x7FFFFF00u &&
+           dim % 8 == 0 && dim <= 0x7FFFFF00u && tokens <= 0x7FFFFF00u &&
+           // tiles and steps are counted in 32 bits
+           (tokens / kTile + 1) * (vocab / kBlock + p + 1) < 0x7FFFFFFFu && (dim / kTile + 1) * (vocab / kBlock + p + 1) < 0x7FFFFFFFu &&
+           (tokens / kTile + 1) * (dim / kTile + 1) < 0x3FFFFFFFu;
 }
 
 int vocab_xent(rar_ctx *h, const rar_vocab_xent_args *a, cudaStream_t stream) {
@@ -644,17 +785,18 @@ int vocab_xent(rar_ctx *h, const rar_vocab_xent_args *a, cudaStream_t stream) {
             }
             return e;
         }
-        e = launch_tiles<XENT_STATS, DT>(h, k, maps, 0, k.n_blocks, stream);
+        const bool few = k.tokens <= kFewTokens;
+        e = few ? launch_tiles<XENT_STATS_FEW, DT>(h, k, maps, 0, k.n_blocks, stream) : launch_tiles<XENT_STATS, DT>(h, k, maps, 0, k.n_blocks, stream);
         if (e == cudaSuccess)
             e = launch_pdl(grad ? xent_join_kernel<DT, true> : xent_join_kernel<DT, false>, dim3((unsigned)((k.tokens + 7) / 8)),
                            dim3(256), 0, stream, k);
         if (!grad) return e;
-        for (long long b0 = 0; b0 < k.n_blocks && e == cudaSuccess; b0 += k.window) {
-            const long long nb = std::min(k.window, k.n_blocks - b0);
-            e = launch_tiles<XENT_G, DT>(h, k, maps, b0, nb, stream);
+        for (int b0 = 0; b0 < k.n_blocks && e == cudaSuccess; b0 += k.window) {
+            const int nb = std::min(k.window, k.n_blocks - b0);
+            e = few ? launch_tiles<XENT_G_FEW, DT>(h, k, maps, b0, nb, stream) : launch_tiles<XENT_G, DT>(h, k, maps, b0, nb, stream);
             if (e == cudaSuccess && k.dhidden) {
                 XentArgs kw = k;
-                kw.splits = (int)std::min<long long>(k.splits, nb);
+                kw.splits = std::min(k.splits, nb);
                 e = launch_tiles<XENT_DHIDDEN, DT>(h, kw, maps, b0, nb, stream);
             }
             if (e == cudaSuccess && k.want_dw) e = launch_tiles<XENT_DWEIGHT, DT>(h, k, maps, b0, nb, stream);
