@@ -25,10 +25,9 @@
 namespace rar {
 
 constexpr int kTcMaxStages = 8;
-constexpr int kTcRingBytes = 196608;       // stages of 32 KB (128 rows of A and of B a CTA) or less
+constexpr int kTcRingBytes = 229376;       // stages of 32 KB (128 rows of A and of B a CTA) or less
 constexpr int kTcEpilogueWarps = 8;        // two per quarter of the accumulator's lanes
 constexpr int kTcThreads = 32 * (kTcEpilogueWarps + 2);
-constexpr int kTcSmem = kTcRingBytes + 1024;  // + alignment to the swizzle's 1024 bytes
 
 struct TcShared {
     uint64_t full[kTcMaxStages];   // leader: both CTAs' loads of a stage have landed

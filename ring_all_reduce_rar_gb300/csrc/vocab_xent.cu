@@ -108,7 +108,7 @@ template <int MODE>
 struct Mode {
     static constexpr bool few = MODE == XENT_STATS_FEW || MODE == XENT_G_FEW;
     static constexpr bool stats = MODE == XENT_STATS || MODE == XENT_STATS_FEW, logits = stats || MODE == XENT_G || MODE == XENT_G_FEW;
-    static constexpr int stage_bytes = few ? 24576 : 32768, stages = kTcRingBytes / stage_bytes;
+    static constexpr int stage_bytes = few ? 24576 : 32768, stages = few ? 8 : kTcRingBytes / stage_bytes;
     static_assert(stages <= kTcMaxStages, "barriers of a stage");
 };
 
@@ -385,42 +385,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
     const int items = xent_items<MODE>(a, nb), pairs = gridDim.x / 2, first = blockIdx.x / 2;
     constexpr bool a_mn = MODE == XENT_DWEIGHT, b_mn = MODE == XENT_DHIDDEN || MODE == XENT_DWEIGHT;
 
-    if (warp == kTcEpilogueWarps && lane == 0) {
+    if (warp == kTcEpilogueWarps && lane < 4) {
+        // four lanes, a box each: 0 and 1 of A, 2 and 3 of B
+        constexpr unsigned kLanes = 0xFu;
+        const int j = lane & 1;
+        const bool is_a = lane < 2;
         unsigned step = 0;
-        for (int i = first; i < items && !*(volatile int *)&sh.failed; i += pairs) {
+        for (int i = first; i < items && !__any_sync(kLanes, *(volatile int *)&sh.failed); i += pairs) {
             const XentItem it = xent_item<MODE>(a, b0, nb, i);
             const int half = (int)rank * it.n / 2;
             xent_steps<MODE>(a, b0, it, [&](int s, int k, const BlockOf &b) {
                 const int st = (int)(step % kStages);
-                if (step >= kStages && !tc_wait(&sh, a.limits, &sh.empty[st], (step / kStages - 1) & 1, 0)) return false;
+                const bool ok = step < kStages || tc_wait(&sh, a.limits, &sh.empty[st], (step / kStages - 1) & 1, 0);
+                if (!__all_sync(kLanes, ok)) return false;
                 // boxes past the last row are not loaded: their rows of the accumulator
                 // are never read (few tokens: half of the loads)
                 auto row_box = [&](int box) { return MODE == XENT_DWEIGHT || (kFew ? box * 64 < b.rows : it.row + box * 64 < a.tokens); };
-                if (rank == 0)
+                if (rank == 0 && lane == 0)
                     tc_expect_tx(&sh.full[st], (kFew ? 16384u : 32768u) + 8192u * (row_box(0) + row_box(1) + row_box(2) + row_box(3)));
-                const uint32_t bar = peer_addr(smem_u32(&sh.full[st]), 0), to = stages + st * kStageBytes;
-                const CUtensorMap *ma = kFew ? &maps.w[b.piece] : Mode<MODE>::logits ? &maps.hidden : &maps.g;
-                const CUtensorMap *mb = kFew ? &maps.hidden : MODE == XENT_DWEIGHT ? &maps.hidden_used : &maps.w[b.piece];
-                for (int j = 0; j < 2; j++) {
-                    if (!row_box((int)rank * 2 + j)) continue;
-                    const int row = (kFew ? b.row : it.row) + (int)rank * 128 + j * 64;
-                    if (MODE == XENT_DHIDDEN) tc_load_box(ma, to + j * 8192, bar, k * kBlock + s * 64, row);
-                    else if (MODE == XENT_DWEIGHT) tc_load_box(ma, to + j * 8192, bar, row, s * 64);
-                    else tc_load_box(ma, to + j * 8192, bar, s * 64, row);
-                }
-                for (int j = 0; j < (kFew ? 1 : 2); j++) {
-                    const int col = it.col + half + j * 64;
-                    if (MODE == XENT_DHIDDEN) tc_load_box(mb, to + 16384 + j * 8192, bar, col, b.row + s * 64);
-                    else if (MODE == XENT_DWEIGHT) tc_load_box(mb, to + 16384 + j * 8192, bar, col, s * 64);
-                    else tc_load_box(mb, to + 16384 + j * 8192, bar, s * 64, kFew ? col : b.row + col);
-                }
+                const uint32_t bar = peer_addr(smem_u32(&sh.full[st]), 0), to = stages + st * kStageBytes + lane * 8192;
+                const CUtensorMap *map = is_a ? (kFew ? &maps.w[b.piece] : Mode<MODE>::logits ? &maps.hidden : &maps.g)
+                                              : (kFew ? &maps.hidden : MODE == XENT_DWEIGHT ? &maps.hidden_used : &maps.w[b.piece]);
+                const int row = (kFew ? b.row : it.row) + (int)rank * 128 + j * 64, col = it.col + half + j * 64;
+                int x, y;
+                if (MODE == XENT_DHIDDEN) x = is_a ? k * kBlock + s * 64 : col, y = is_a ? row : b.row + s * 64;
+                else if (MODE == XENT_DWEIGHT) x = is_a ? row : col, y = s * 64;
+                else x = s * 64, y = is_a ? row : kFew ? col : b.row + col;
+                if (is_a ? row_box((int)rank * 2 + j) : !kFew || j == 0) tc_load_box(map, to, bar, x, y);
                 step++;
                 return true;
             });
         }
         // neither CTA may leave while the pair's loads or arrivals are on their
         // way (the loads even after a wait that ran out)
-        for (unsigned k = step > kStages ? step - kStages : 0; k < step; k++) {
+        for (unsigned k = step > kStages ? step - kStages : 0; k < step && lane == 0; k++) {
             const int st = (int)(k % kStages);
             if (rank == 0) tc_drain(&sh.full[st], (k / kStages) & 1);
             tc_wait(&sh, a.limits, &sh.empty[st], (k / kStages) & 1, 1);
@@ -638,10 +636,11 @@ bool make_map(CUtensorMap *m, int dtype, const void *ptr, long long rows, long l
 template <int MODE, int DT>
 cudaError_t launch_tiles(const rar_ctx *h, const XentArgs &k, const XentMaps &maps, int b0, int nb, cudaStream_t stream) {
     auto kern = xent_tile_kernel<MODE, DT>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcSmem);
+    constexpr int smem = Mode<MODE>::stages * Mode<MODE>::stage_bytes + 1024;  // + alignment to the swizzle's 1024 bytes
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const int pairs = std::min(xent_items<MODE>(k, nb), h->sm_count / 2);
-    return launch_pdl(kern, dim3((unsigned)(2 * pairs)), dim3(kTcThreads), kTcSmem, stream, k, maps, b0, nb);
+    return launch_pdl(kern, dim3((unsigned)(2 * pairs)), dim3(kTcThreads), smem, stream, k, maps, b0, nb);
 }
 
 void plan_blocks(size_t vocab, int p, XentArgs *k) {
