@@ -1,18 +1,17 @@
 // tc_gemm.cuh -- building blocks of a matrix product on the tensor cores by
-// pairs of CTAs (a cluster of two): TMA loads of 64 x 64 tiles into
+// pairs of CTAs (a cluster of two): TMA loads into
 // 128-byte-swizzled shared memory, tcgen05.mma of 256 x 256 x 16 steps issued by
 // one thread of the pair, accumulators in tensor memory.
 //
-// Every operand tile is a box of 64 rows of 64 16-bit elements (8 KB), whatever
-// the operand's role:
+// Operands come in boxes of 64 16-bit elements (128 bytes) of 64 or 128 rows,
+// whatever the operand's role:
 //   rows = M or N, columns = K   "K-major": the rows of 8 x 128 bytes that the
 //       swizzle works on follow each other every 1024 bytes; a step of 16 along
 //       K is 32 bytes further in the row;
 //   rows = K, columns = M or N   "MN-major": groups of 8 K rows are 1024 bytes
 //       apart, the next 64 columns are the next box; a step of 16 along K is 2048
 //       bytes further.
-// So one tensor map per matrix serves both, and no operand is transposed in
-// memory.
+// So no operand is transposed in memory.
 //
 // Every wait has a limit.  A wait that runs out raises the CTA's flag, which the other
 // waits of the CTA poll, and records it for rar_status.

@@ -59,9 +59,11 @@ struct XentArgs {
     TcLimits limits;
 };
 
-// Tensor maps: boxes of 64 rows x 64 elements.
+// Tensor maps of a launch: `one` is the operand that is one matrix (hidden or G),
+// `w` the pieces of W, or hidden as XENT_DWEIGHT's second operand.  Boxes are 64
+// elements of 128 rows where K runs along the rows, else (and for few tokens) of 64.
 struct XentMaps {
-    CUtensorMap hidden, hidden_used, g, w[kInlineP];
+    CUtensorMap one, w[kInlineP];
 };
 
 struct BlockOf {
@@ -109,6 +111,10 @@ struct Mode {
     static constexpr bool few = MODE == XENT_STATS_FEW || MODE == XENT_G_FEW;
     static constexpr bool stats = MODE == XENT_STATS || MODE == XENT_STATS_FEW, logits = stats || MODE == XENT_G || MODE == XENT_G_FEW;
     static constexpr int stage_bytes = few ? 24576 : 32768, stages = few ? 8 : kTcRingBytes / stage_bytes;
+    // whether a row of the operand is a row of K (MN-major); rows of a box; boxes of a stage
+    static constexpr bool a_mn = MODE == XENT_DWEIGHT, b_mn = MODE == XENT_DHIDDEN || MODE == XENT_DWEIGHT;
+    static constexpr int a_box = a_mn ? 64 : 128, b_box = b_mn || few ? 64 : 128;
+    static constexpr int a_boxes = 128 / a_box, b_boxes = few ? 1 : 128 / b_box;
     static_assert(stages <= kTcMaxStages, "barriers of a stage");
 };
 
@@ -383,35 +389,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
     pdl_launch_dependents();
     if (Mode<MODE>::stats && blockIdx.x == 0 && threadIdx.x == 0) *a.w_max = 0u;
     const int items = xent_items<MODE>(a, nb), pairs = gridDim.x / 2, first = blockIdx.x / 2;
-    constexpr bool a_mn = MODE == XENT_DWEIGHT, b_mn = MODE == XENT_DHIDDEN || MODE == XENT_DWEIGHT;
-
-    if (warp == kTcEpilogueWarps && lane < 4) {
-        // four lanes, a box each: 0 and 1 of A, 2 and 3 of B
-        constexpr unsigned kLanes = 0xFu;
-        const int j = lane & 1;
-        const bool is_a = lane < 2;
+    constexpr bool a_mn = Mode<MODE>::a_mn, b_mn = Mode<MODE>::b_mn;
+    constexpr int kABoxes = Mode<MODE>::a_boxes, kLoaders = kABoxes + Mode<MODE>::b_boxes;
+    if (warp == kTcEpilogueWarps && lane < kLoaders) {
+        // a lane a box, first those of A
+        constexpr unsigned kLanes = (1u << kLoaders) - 1;
+        const bool is_a = lane < kABoxes;
+        const int part = is_a ? lane * Mode<MODE>::a_box : (lane - kABoxes) * Mode<MODE>::b_box;  // rows (columns) into the operand
         unsigned step = 0;
         for (int i = first; i < items && !__any_sync(kLanes, *(volatile int *)&sh.failed); i += pairs) {
             const XentItem it = xent_item<MODE>(a, b0, nb, i);
-            const int half = (int)rank * it.n / 2;
             xent_steps<MODE>(a, b0, it, [&](int s, int k, const BlockOf &b) {
                 const int st = (int)(step % kStages);
                 const bool ok = step < kStages || tc_wait(&sh, a.limits, &sh.empty[st], (step / kStages - 1) & 1, 0);
                 if (!__all_sync(kLanes, ok)) return false;
-                // boxes past the last row are not loaded: their rows of the accumulator
-                // are never read (few tokens: half of the loads)
-                auto row_box = [&](int box) { return MODE == XENT_DWEIGHT || (kFew ? box * 64 < b.rows : it.row + box * 64 < a.tokens); };
+                // a CTA whose rows of A all lie past the last loads none of them: its
+                // rows of the accumulator are never read
+                auto a_rows = [&](int r) { return MODE == XENT_DWEIGHT || (kFew ? r * 128 < b.rows : it.row + r * 128 < a.tokens); };
                 if (rank == 0 && lane == 0)
-                    tc_expect_tx(&sh.full[st], (kFew ? 16384u : 32768u) + 8192u * (row_box(0) + row_box(1) + row_box(2) + row_box(3)));
-                const uint32_t bar = peer_addr(smem_u32(&sh.full[st]), 0), to = stages + st * kStageBytes + lane * 8192;
-                const CUtensorMap *map = is_a ? (kFew ? &maps.w[b.piece] : Mode<MODE>::logits ? &maps.hidden : &maps.g)
-                                              : (kFew ? &maps.hidden : MODE == XENT_DWEIGHT ? &maps.hidden_used : &maps.w[b.piece]);
-                const int row = (kFew ? b.row : it.row) + (int)rank * 128 + j * 64, col = it.col + half + j * 64;
+                    tc_expect_tx(&sh.full[st], (kFew ? 16384u : 32768u) + 16384u * (1u + a_rows(1)));
+                const uint32_t bar = peer_addr(smem_u32(&sh.full[st]), 0);
+                const uint32_t to = stages + st * kStageBytes + (is_a ? 0 : 16384) + part * 128;
+                const CUtensorMap *map = (is_a != kFew) && (MODE != XENT_DWEIGHT || is_a) ? &maps.one : &maps.w[MODE == XENT_DWEIGHT ? 0 : b.piece];
+                const int row = (kFew ? b.row : it.row) + (int)rank * 128 + part, col = it.col + (int)rank * it.n / 2 + part;
                 int x, y;
                 if (MODE == XENT_DHIDDEN) x = is_a ? k * kBlock + s * 64 : col, y = is_a ? row : b.row + s * 64;
                 else if (MODE == XENT_DWEIGHT) x = is_a ? row : col, y = s * 64;
                 else x = s * 64, y = is_a ? row : kFew ? col : b.row + col;
-                if (is_a ? row_box((int)rank * 2 + j) : !kFew || j == 0) tc_load_box(map, to, bar, x, y);
+                if (!is_a || a_rows((int)rank)) tc_load_box(map, to, bar, x, y);
                 step++;
                 return true;
             });
@@ -424,6 +429,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
             tc_wait(&sh, a.limits, &sh.empty[st], (k / kStages) & 1, 1);
         }
     } else if (warp == kTcEpilogueWarps + 1 && lane == 0 && rank == 0) {
+        const uint64_t operand_a = tc_operand(stages, a_mn ? 8192 : 16, 1024), operand_b = tc_operand(stages + 16384, b_mn ? 8192 : 16, 1024);
         unsigned step = 0, tile = 0;
         for (int i = first; i < items; i += pairs, tile++) {
             const XentItem it = xent_item<MODE>(a, b0, nb, i);
@@ -436,12 +442,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
                 const int st = (int)(step % kStages);
                 if (!tc_wait(&sh, a.limits, &sh.full[st], (step / kStages) & 1, 3)) return false;
                 tc_fence_after();
-                const uint32_t pa = stages + st * kStageBytes, pb = pa + 16384;
+                // descriptors count addresses in units of 16 bytes
+                const uint64_t da = operand_a + (uint32_t)(st * kStageBytes / 16), db = operand_b + (uint32_t)(st * kStageBytes / 16);
 #pragma unroll
                 for (int k = 0; k < 4; k++) {
-                    const uint64_t da = tc_operand(pa + k * (a_mn ? 2048 : 32), a_mn ? 8192 : 16, 1024);
-                    const uint64_t db = tc_operand(pb + k * (b_mn ? 2048 : 32), b_mn ? 8192 : 16, 1024);
-                    tc_mma(d, da, db, idesc, more);
+                    tc_mma(d, da + k * (a_mn ? 128 : 2), db + k * (b_mn ? 128 : 2), idesc, more);
                     more = true;
                 }
                 tc_commit(&sh.empty[st]);
@@ -621,13 +626,13 @@ EncodeTiled encode_tiled() {
     return fn;
 }
 
-// A map of a rows x cols matrix of 16-bit elements, boxes of 64 x 64; what lies
+// A map of a rows x cols matrix of 16-bit elements, boxes of box_rows x 64; what lies
 // beyond the matrix reads as zero.
-bool make_map(CUtensorMap *m, int dtype, const void *ptr, long long rows, long long cols, long long stride) {
+bool make_map(CUtensorMap *m, int dtype, const void *ptr, long long rows, long long cols, long long stride, int box_rows) {
     const EncodeTiled encode = encode_tiled();
     if (!encode) return false;
     const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)stride * 2};
-    const cuuint32_t box[2] = {64, 64}, steps[2] = {1, 1};
+    const cuuint32_t box[2] = {64, (cuuint32_t)box_rows}, steps[2] = {1, 1};
     return encode(m, dtype == DT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
                   const_cast<void *>(ptr), dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -760,17 +765,21 @@ int vocab_xent(rar_ctx *h, const rar_vocab_xent_args *a, cudaStream_t stream) {
 
     k.limits = {h->status, h->opt.timeout_ns ? h->opt.timeout_ns : 2000000000ull};
 
-    XentMaps maps;
+    const bool few = k.tokens <= kFewTokens;
+    XentMaps logits, dh, dw;  // of the products that use them
     bool mapped = true;
     if (k.tokens) {
-        mapped = make_map(&maps.hidden, a->dtype, k.hidden, k.tokens, k.dim, k.hidden_stride);
+        mapped = make_map(&logits.one, a->dtype, k.hidden, k.tokens, k.dim, k.hidden_stride, few ? 64 : 128);
         for (int r = 0; r < k.p && mapped; r++) {
             const long long rows = k.base + (r < k.extra ? 1 : 0);
-            if (rows) mapped = make_map(&maps.w[r], a->dtype, k.w.inl[r], rows, k.dim, k.weight_stride);
+            if (rows) mapped = make_map(&logits.w[r], a->dtype, k.w.inl[r], rows, k.dim, k.weight_stride, 128);
+            if (rows && mapped && k.dhidden) mapped = make_map(&dh.w[r], a->dtype, k.w.inl[r], rows, k.dim, k.weight_stride, 64);
         }
-        if (grad && mapped)
-            mapped = make_map(&maps.hidden_used, a->dtype, k.hidden_used, k.tokens, k.dim, k.dim) &&
-                     make_map(&maps.g, a->dtype, k.g, k.tokens, k.window * kBlock, k.window * kBlock);
+        const long long pitch = (long long)k.window * kBlock;
+        if (k.dhidden) mapped = mapped && make_map(&dh.one, a->dtype, k.g, k.tokens, pitch, pitch, 128);
+        if (k.want_dw)
+            mapped = mapped && make_map(&dw.one, a->dtype, k.g, k.tokens, pitch, pitch, 64) &&
+                     make_map(&dw.w[0], a->dtype, k.hidden_used, k.tokens, k.dim, k.dim, 64);
     }
     if (!mapped) return fail(h, RAR_ECUDA, "rar_vocab_xent: the driver refused a tensor map");
 
@@ -784,21 +793,20 @@ int vocab_xent(rar_ctx *h, const rar_vocab_xent_args *a, cudaStream_t stream) {
             }
             return e;
         }
-        const bool few = k.tokens <= kFewTokens;
-        e = few ? launch_tiles<XENT_STATS_FEW, DT>(h, k, maps, 0, k.n_blocks, stream) : launch_tiles<XENT_STATS, DT>(h, k, maps, 0, k.n_blocks, stream);
+        e = few ? launch_tiles<XENT_STATS_FEW, DT>(h, k, logits, 0, k.n_blocks, stream) : launch_tiles<XENT_STATS, DT>(h, k, logits, 0, k.n_blocks, stream);
         if (e == cudaSuccess)
             e = launch_pdl(grad ? xent_join_kernel<DT, true> : xent_join_kernel<DT, false>, dim3((unsigned)((k.tokens + 7) / 8)),
                            dim3(256), 0, stream, k);
         if (!grad) return e;
         for (int b0 = 0; b0 < k.n_blocks && e == cudaSuccess; b0 += k.window) {
             const int nb = std::min(k.window, k.n_blocks - b0);
-            e = few ? launch_tiles<XENT_G_FEW, DT>(h, k, maps, b0, nb, stream) : launch_tiles<XENT_G, DT>(h, k, maps, b0, nb, stream);
+            e = few ? launch_tiles<XENT_G_FEW, DT>(h, k, logits, b0, nb, stream) : launch_tiles<XENT_G, DT>(h, k, logits, b0, nb, stream);
             if (e == cudaSuccess && k.dhidden) {
                 XentArgs kw = k;
                 kw.splits = std::min(k.splits, nb);
-                e = launch_tiles<XENT_DHIDDEN, DT>(h, kw, maps, b0, nb, stream);
+                e = launch_tiles<XENT_DHIDDEN, DT>(h, kw, dh, b0, nb, stream);
             }
-            if (e == cudaSuccess && k.want_dw) e = launch_tiles<XENT_DWEIGHT, DT>(h, k, maps, b0, nb, stream);
+            if (e == cudaSuccess && k.want_dw) e = launch_tiles<XENT_DWEIGHT, DT>(h, k, dw, b0, nb, stream);
         }
         if (e == cudaSuccess && k.dhidden && k.splits > 1) {
             const long long n = k.tokens * (k.dim / 8);
