@@ -23,14 +23,16 @@
 
 namespace rar {
 
-constexpr int kTcMaxStages = 8;
-constexpr int kTcRingBytes = 229376;       // stages of 32 KB (128 rows of A and of B a CTA) or less
+constexpr int kTcStages = 7;
+constexpr int kTcStageBytes = 32768;       // a CTA's share of A (128 x 64) and of B (128 x 64)
 constexpr int kTcEpilogueWarps = 8;        // two per quarter of the accumulator's lanes
 constexpr int kTcThreads = 32 * (kTcEpilogueWarps + 2);
 
+constexpr int kTcSmem = kTcStages * kTcStageBytes + 1024;  // + alignment to the swizzle's 1024 bytes
+
 struct TcShared {
-    uint64_t full[kTcMaxStages];   // leader: both CTAs' loads of a stage have landed
-    uint64_t empty[kTcMaxStages];  // each CTA: the products that read a stage are done
+    uint64_t full[kTcStages];   // leader: both CTAs' loads of a stage have landed
+    uint64_t empty[kTcStages];  // each CTA: the products that read a stage are done
     uint64_t acc_full[2];       // each CTA: an accumulator is complete
     uint64_t acc_empty[2];      // leader: both CTAs' epilogues have read it
     uint32_t tmem;
@@ -118,6 +120,9 @@ __device__ __forceinline__ void tc_drain(uint64_t *bar, uint32_t parity) {
     }
 }
 
+__device__ __forceinline__ void tc_prefetch_map(const CUtensorMap *map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
 __device__ __forceinline__ void tc_load_box(const CUtensorMap *map, uint32_t dst, uint32_t cluster_bar, int x, int y) {
     asm volatile(
         "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
@@ -187,7 +192,7 @@ __device__ __forceinline__ void load_32b(const void *p, uint32_t *r) {
 __device__ __forceinline__ void tc_begin(TcShared *sh) {
     if (threadIdx.x == 0) {
         sh->failed = 0;
-        for (int s = 0; s < kTcMaxStages; s++) {
+        for (int s = 0; s < kTcStages; s++) {
             tc_mbar_init(&sh->full[s], 1);
             tc_mbar_init(&sh->empty[s], 1);
         }

@@ -61,7 +61,7 @@ struct XentArgs {
 
 // Tensor maps of a launch: `one` is the operand that is one matrix (hidden or G),
 // `w` the pieces of W, or hidden as XENT_DWEIGHT's second operand.  Boxes are 64
-// elements of 128 rows where K runs along the rows, else (and for few tokens) of 64.
+// elements of 128 rows where K runs along the rows, else of 64.
 struct XentMaps {
     CUtensorMap one, w[kInlineP];
 };
@@ -100,22 +100,14 @@ __device__ __forceinline__ int g_exponent(const XentArgs &a) {
     return e > 120 ? 120 : e < -120 ? -120 : e;
 }
 
-// XENT_STATS, XENT_G: rows of a tile are tokens, columns a block of the
-// vocabulary.  The FEW forms turn the tile round (up to kFewTokens tokens): rows
-// are the block, columns the tokens, so that the product is no wider than
-// they are and most of the loads are of W.
-enum XentMode { XENT_STATS, XENT_G, XENT_DHIDDEN, XENT_DWEIGHT, XENT_STATS_FEW, XENT_G_FEW };
-constexpr int kFewTokens = 128;
+enum XentMode { XENT_STATS, XENT_G, XENT_DHIDDEN, XENT_DWEIGHT };
 template <int MODE>
 struct Mode {
-    static constexpr bool few = MODE == XENT_STATS_FEW || MODE == XENT_G_FEW;
-    static constexpr bool stats = MODE == XENT_STATS || MODE == XENT_STATS_FEW, logits = stats || MODE == XENT_G || MODE == XENT_G_FEW;
-    static constexpr int stage_bytes = few ? 24576 : 32768, stages = few ? 8 : kTcRingBytes / stage_bytes;
+    static constexpr bool logits = MODE == XENT_STATS || MODE == XENT_G;
     // whether a row of the operand is a row of K (MN-major); rows of a box; boxes of a stage
     static constexpr bool a_mn = MODE == XENT_DWEIGHT, b_mn = MODE == XENT_DHIDDEN || MODE == XENT_DWEIGHT;
-    static constexpr int a_box = a_mn ? 64 : 128, b_box = b_mn || few ? 64 : 128;
-    static constexpr int a_boxes = 128 / a_box, b_boxes = few ? 1 : 128 / b_box;
-    static_assert(stages <= kTcMaxStages, "barriers of a stage");
+    static constexpr int a_box = a_mn ? 64 : 128, b_box = b_mn ? 64 : 128;
+    static constexpr int a_boxes = 128 / a_box, b_boxes = 128 / b_box;
 };
 
 // One tile of a pair of CTAs: its place, and its range along K.
@@ -140,13 +132,6 @@ __device__ __forceinline__ XentItem xent_item(const XentArgs &a, int b0, int nb,
     o.block = 0;
     o.col = 0;
     o.k0 = 0;
-    if (Mode<MODE>::few) {
-        o.row = 0;
-        o.block = i;
-        o.n = round32((int)a.tokens);
-        o.k1 = (int)((a.dim + 63) / 64);
-        return o;
-    }
     const unsigned tb = (unsigned)tiles_of(a.tokens), db = (unsigned)tiles_of(a.dim);
     const unsigned rows = MODE == XENT_DWEIGHT ? (unsigned)nb : tb;
     const unsigned cols = MODE == XENT_DHIDDEN ? db * (unsigned)a.splits : MODE == XENT_DWEIGHT ? db : (unsigned)nb;
@@ -154,7 +139,7 @@ __device__ __forceinline__ XentItem xent_item(const XentArgs &a, int b0, int nb,
     const unsigned width = min(rows - g * 8, 8u), c = in / width;
     const int r = (int)(g * 8 + in - c * width);
     o.row = r * kTile;
-    if (MODE == XENT_STATS || MODE == XENT_G) {
+    if (Mode<MODE>::logits) {
         o.block = (int)c;
         o.n = round32(block_of(a, b0 + (int)c).rows);
         o.k1 = (int)((a.dim + 63) / 64);
@@ -174,7 +159,6 @@ __device__ __forceinline__ XentItem xent_item(const XentArgs &a, int b0, int nb,
 }
 template <int MODE>
 __host__ __device__ inline int xent_items(const XentArgs &a, int nb) {
-    if (Mode<MODE>::few) return nb;
     const int tb = tiles_of(a.tokens), db = tiles_of(a.dim);
     return MODE == XENT_DHIDDEN ? tb * db * a.splits : MODE == XENT_DWEIGHT ? nb * db : tb * nb;
 }
@@ -326,41 +310,6 @@ __device__ __forceinline__ void xent_columns(const XentArgs &a, XentRow &r, int 
     }
 }
 
-struct XentFew {
-    float2 part[2][4][kFewTokens];  // by tile parity and quarter of the rows: max and sum of a token
-    int target[kFewTokens];         // index in the vocabulary, or -1
-    float w[kFewTokens], lse[kFewTokens];
-};
-// Barrier 1: the epilogue warps only.
-__device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kTcEpilogueWarps) : "memory"); }
-
-// The epilogue of the FEW forms: lanes are rows of the block, so a token's
-// statistics are reduced over the lanes.  A warp's columns (tokens) are
-// [half, half + count).
-template <int MODE, int DT>
-__device__ __forceinline__ void few_columns(const XentArgs &a, const BlockOf &b, int block, int parity, XentFew &few, int row, int quarter,
-                                            int t0, int count, float (&v)[32]) {
-    const bool live = row < b.rows;
-    const int index = b.first + row;
-#pragma unroll
-    for (int c = 0; c < 32; c++) {
-        const int t = t0 + c;
-        if (c >= count) break;
-        if constexpr (MODE == XENT_STATS_FEW) {
-            const float z = live ? v[c] : -INFINITY;
-            if (live && few.target[t] == index) a.z_target[t] = z;
-            float m = z;
-#pragma unroll
-            for (int o = 16; o; o /= 2) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-            const float s = warp_sum(exp_of(z - (m == -INFINITY ? 0.0f : m)));
-            if (threadIdx.x % 32 == 0) few.part[parity][quarter][t] = make_float2(m, s);
-        } else {
-            const float w = few.w[t], p = exp_of(v[c] - few.lse[t]) - (few.target[t] == index ? 1.0f : 0.0f);
-            store_f<DT>(a.g, ((long long)t * a.window + block) * kBlock + row, live && w != 0.0f ? p * w : 0.0f);
-        }
-    }
-}
-
 // Adds sums of exponentials, each relative to its maximum.
 __device__ __forceinline__ void add_exp(float &m, float &s, float om, float os) {
     if (os == 0.0f) return;  // nothing there
@@ -379,15 +328,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
     xent_tile_kernel(const __grid_constant__ XentArgs a, const __grid_constant__ XentMaps maps, int b0, int nb) {
     extern __shared__ unsigned char dyn[];
     __shared__ TcShared sh;
-    constexpr bool kFew = Mode<MODE>::few;
-    constexpr int kStages = Mode<MODE>::stages, kStageBytes = Mode<MODE>::stage_bytes;
     const uint32_t stages = (smem_u32(dyn) + 1023u) & ~1023u;
     const uint32_t rank = cluster_rank();
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    if (threadIdx.x < 2) tc_prefetch_map(threadIdx.x ? &maps.w[0] : &maps.one);
     tc_begin(&sh);
     pdl_wait();
     pdl_launch_dependents();
-    if (Mode<MODE>::stats && blockIdx.x == 0 && threadIdx.x == 0) *a.w_max = 0u;
+    if (MODE == XENT_STATS && blockIdx.x == 0 && threadIdx.x == 0) *a.w_max = 0u;
     const int items = xent_items<MODE>(a, nb), pairs = gridDim.x / 2, first = blockIdx.x / 2;
     constexpr bool a_mn = Mode<MODE>::a_mn, b_mn = Mode<MODE>::b_mn;
     constexpr int kABoxes = Mode<MODE>::a_boxes, kLoaders = kABoxes + Mode<MODE>::b_boxes;
@@ -400,22 +348,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
         for (int i = first; i < items && !__any_sync(kLanes, *(volatile int *)&sh.failed); i += pairs) {
             const XentItem it = xent_item<MODE>(a, b0, nb, i);
             xent_steps<MODE>(a, b0, it, [&](int s, int k, const BlockOf &b) {
-                const int st = (int)(step % kStages);
-                const bool ok = step < kStages || tc_wait(&sh, a.limits, &sh.empty[st], (step / kStages - 1) & 1, 0);
+                const int st = (int)(step % kTcStages);
+                const bool ok = step < kTcStages || tc_wait(&sh, a.limits, &sh.empty[st], (step / kTcStages - 1) & 1, 0);
                 if (!__all_sync(kLanes, ok)) return false;
                 // a CTA whose rows of A all lie past the last loads none of them: its
                 // rows of the accumulator are never read
-                auto a_rows = [&](int r) { return MODE == XENT_DWEIGHT || (kFew ? r * 128 < b.rows : it.row + r * 128 < a.tokens); };
+                auto a_rows = [&](int r) { return MODE == XENT_DWEIGHT || it.row + r * 128 < a.tokens; };
                 if (rank == 0 && lane == 0)
-                    tc_expect_tx(&sh.full[st], (kFew ? 16384u : 32768u) + 16384u * (1u + a_rows(1)));
+                    tc_expect_tx(&sh.full[st], 32768u + 16384u * (1u + a_rows(1)));
                 const uint32_t bar = peer_addr(smem_u32(&sh.full[st]), 0);
-                const uint32_t to = stages + st * kStageBytes + (is_a ? 0 : 16384) + part * 128;
-                const CUtensorMap *map = (is_a != kFew) && (MODE != XENT_DWEIGHT || is_a) ? &maps.one : &maps.w[MODE == XENT_DWEIGHT ? 0 : b.piece];
-                const int row = (kFew ? b.row : it.row) + (int)rank * 128 + part, col = it.col + (int)rank * it.n / 2 + part;
+                const uint32_t to = stages + st * kTcStageBytes + (is_a ? 0 : 16384) + part * 128;
+                const CUtensorMap *map = is_a ? &maps.one : &maps.w[MODE == XENT_DWEIGHT ? 0 : b.piece];
+                const int row = it.row + (int)rank * 128 + part, col = it.col + (int)rank * it.n / 2 + part;
                 int x, y;
                 if (MODE == XENT_DHIDDEN) x = is_a ? k * kBlock + s * 64 : col, y = is_a ? row : b.row + s * 64;
                 else if (MODE == XENT_DWEIGHT) x = is_a ? row : col, y = s * 64;
-                else x = s * 64, y = is_a ? row : kFew ? col : b.row + col;
+                else x = s * 64, y = is_a ? row : b.row + col;
                 if (!is_a || a_rows((int)rank)) tc_load_box(map, to, bar, x, y);
                 step++;
                 return true;
@@ -423,10 +371,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
         }
         // neither CTA may leave while the pair's loads or arrivals are on their
         // way (the loads even after a wait that ran out)
-        for (unsigned k = step > kStages ? step - kStages : 0; k < step && lane == 0; k++) {
-            const int st = (int)(k % kStages);
-            if (rank == 0) tc_drain(&sh.full[st], (k / kStages) & 1);
-            tc_wait(&sh, a.limits, &sh.empty[st], (k / kStages) & 1, 1);
+        for (unsigned k = step > kTcStages ? step - kTcStages : 0; k < step && lane == 0; k++) {
+            const int st = (int)(k % kTcStages);
+            if (rank == 0) tc_drain(&sh.full[st], (k / kTcStages) & 1);
+            tc_wait(&sh, a.limits, &sh.empty[st], (k / kTcStages) & 1, 1);
         }
     } else if (warp == kTcEpilogueWarps + 1 && lane == 0 && rank == 0) {
         const uint64_t operand_a = tc_operand(stages, a_mn ? 8192 : 16, 1024), operand_b = tc_operand(stages + 16384, b_mn ? 8192 : 16, 1024);
@@ -439,11 +387,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
             const uint32_t d = sh.tmem + acc * kTile, idesc = tc_instruction(DT == DT_BF16, a_mn, b_mn, (uint32_t)it.n);
             bool more = false;
             const bool ok = xent_steps<MODE>(a, b0, it, [&](int, int, const BlockOf &) {
-                const int st = (int)(step % kStages);
-                if (!tc_wait(&sh, a.limits, &sh.full[st], (step / kStages) & 1, 3)) return false;
+                const int st = (int)(step % kTcStages);
+                if (!tc_wait(&sh, a.limits, &sh.full[st], (step / kTcStages) & 1, 3)) return false;
                 tc_fence_after();
                 // descriptors count addresses in units of 16 bytes
-                const uint64_t da = operand_a + (uint32_t)(st * kStageBytes / 16), db = operand_b + (uint32_t)(st * kStageBytes / 16);
+                const uint64_t da = operand_a + (uint32_t)(st * kTcStageBytes / 16), db = operand_b + (uint32_t)(st * kTcStageBytes / 16);
 #pragma unroll
                 for (int k = 0; k < 4; k++) {
                     tc_mma(d, da + k * (a_mn ? 128 : 2), db + k * (b_mn ? 128 : 2), idesc, more);
@@ -460,104 +408,75 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
         const int quarter = warp % 4;
         const float undo = MODE == XENT_DHIDDEN || MODE == XENT_DWEIGHT ? ldexpf(1.0f, -g_exponent<DT>(a)) : 1.0f;
         const bool first_window = b0 == 0, direct = a.direct && b0 + nb == a.n_blocks;
-        __shared__ XentFew few;
-        if (kFew) {
-            const int t = threadIdx.x;
-            if (t < kFewTokens && t < a.tokens) {
-                const long long y = load_index(a.targets, a.index_bytes, t);
-                few.target[t] = y >= 0 && y < a.vocab ? (int)y : -1;
-                if (MODE == XENT_G_FEW) {
-                    few.w[t] = ldexpf(a.row_weight[t], g_exponent<DT>(a));
-                    few.lse[t] = a.lse_ws[t];
-                }
-            }
-            epilogue_sync();
-        }
         unsigned tile = 0;
         for (int i = first; i < items; i += pairs, tile++) {
             const XentItem it = xent_item<MODE>(a, b0, nb, i);
-            const int acc = (int)(tile & 1), half = kFew ? warp / 4 * (it.n / 2) : warp / 4 * 128;
-            const int count = kFew ? min(it.n / 2, (int)a.tokens - half) : 128;  // columns of the half
-            const int row = (kFew ? 0 : it.row) + (int)rank * 128 + quarter * 32 + lane;
-            XentRow r;
-            BlockOf b;
-            if constexpr (kFew) b = block_of(a, b0 + it.block);
-            else r = xent_row<MODE, DT>(a, b0, it, row, half);
-            const bool ok = tc_wait(&sh, a.limits, &sh.acc_full[acc], (tile / 2) & 1, 4);
-            if (!ok && !kFew) break;  // (FEW: the warps still meet at their barriers)
+            const int acc = (int)(tile & 1), half = warp / 4 * 128, row = it.row + (int)rank * 128 + quarter * 32 + lane;
+            XentRow r = xent_row<MODE, DT>(a, b0, it, row, half);
+            if (!tc_wait(&sh, a.limits, &sh.acc_full[acc], (tile / 2) & 1, 4)) break;
             __syncwarp();
             tc_fence_after();
             const uint32_t at = sh.tmem + ((uint32_t)quarter << 21) + acc * kTile + half;
 #pragma unroll 1
-            for (int c0 = 0; c0 < count; c0 += 32) {
+            for (int c0 = 0; c0 < 128; c0 += 32) {
                 float v[32];
                 tc_read32(at + c0, v);
                 tc_read_wait();
-                if constexpr (kFew) few_columns<MODE, DT>(a, b, it.block, acc, few, row, quarter, half + c0, count - c0, v);
-                else xent_columns<MODE, DT>(a, r, c0, undo, first_window, direct, v);
+                xent_columns<MODE, DT>(a, r, c0, undo, first_window, direct, v);
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) tc_arrive_cluster(peer_addr(smem_u32(&sh.acc_empty[acc]), 0));
             if constexpr (MODE == XENT_STATS)
                 if (r.live) a.stats[(2ll * (b0 + it.block) + half / 128) * a.tokens + row] = make_float2(r.max, r.sum);
-            if constexpr (MODE == XENT_STATS_FEW) {  // the four warps of a token
-                epilogue_sync();
-                const int t = threadIdx.x;
-                if (t < a.tokens) {
-                    float m = -INFINITY, s = 0.0f;
-                    for (int q = 0; q < 4; q++) add_exp(m, s, few.part[acc][q][t].x, few.part[acc][q][t].y);
-                    a.stats[(2ll * (b0 + it.block) + rank) * a.tokens + t] = make_float2(m, s);
-                }
-            }
         }
     }
     __syncwarp();
     tc_end(&sh);
 }
 
-// Joins the blocks of 8 tokens to lse and loss; with gradients also their
+// Joins the blocks of 8 tokens, a warp a token, to lse and loss; with gradients also their
 // weights and hidden states, cleared where a token is left out (0 x NaN is not 0
 // in dweights' sum).
 template <int DT, bool GRAD>
 __global__ void __launch_bounds__(256) xent_join_kernel(const __grid_constant__ XentArgs a) {
-    __shared__ float sm[32][8], ss[32][8];
     __shared__ int counts[8];
     pdl_wait();
     pdl_launch_dependents();
-    const int j = threadIdx.x % 8, g = threadIdx.x / 8;
-    const long long t0 = (long long)blockIdx.x * 8, t = t0 + j;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, n = 2 * a.n_blocks;
+    const long long t0 = (long long)blockIdx.x * 8, t = t0 + warp;
     float m = -INFINITY, s = 0.0f;
-    auto add = [&](float om, float os) { add_exp(m, s, om, os); };
-    const int n = 2 * a.n_blocks;
-    for (int b0 = g; b0 < n && t < a.tokens; b0 += 32 * 8) {
-        float2 v[8];  // loads in flight together
+    if (t < a.tokens) {
+        const long long y = load_index(a.targets, a.index_bytes, t);
+        const bool ok = y >= 0 && y < a.vocab;
+        const float z = a.z_target[t], tw = !ok ? 0.0f : a.token_weight ? a.token_weight[t] : 1.0f;
+        for (int b0 = lane; b0 < n; b0 += 32 * 8) {
+            float2 v[8];  // loads in flight together
 #pragma unroll
-        for (int k = 0; k < 8; k++) v[k] = __ldcg(a.stats + (long long)min(b0 + 32 * k, n - 1) * a.tokens + t);
+            for (int k = 0; k < 8; k++) v[k] = __ldcg(a.stats + (long long)min(b0 + 32 * k, n - 1) * a.tokens + t);
 #pragma unroll
-        for (int k = 0; k < 8; k++)
-            if (b0 + 32 * k < n) add(v[k].x, v[k].y);
-    }
-    sm[g][j] = m;
-    ss[g][j] = s;
-    __syncthreads();
-    if (g == 0) {
-        for (int k = 1; k < 32; k++) add(sm[k][j], ss[k][j]);
-        const float lse = m + logf(s);
-        bool ok = false;
-        if (t < a.tokens) {
-            const long long y = load_index(a.targets, a.index_bytes, t);
-            ok = y >= 0 && y < a.vocab;
-            if (a.lse) a.lse[t] = lse;
-            if (a.loss) a.loss[t] = ok ? lse - a.z_target[t] : 0.0f;
-            if (GRAD) {
-                const float w = !ok ? 0.0f : a.token_weight ? a.token_weight[t] : 1.0f;
-                a.lse_ws[t] = lse;
-                a.row_weight[t] = w;
-                if (isfinite(w)) atomicMax(a.w_max, __float_as_uint(fabsf(w)));
-            }
+            for (int k = 0; k < 8; k++)
+                if (b0 + 32 * k < n) add_exp(m, s, v[k].x, v[k].y);
         }
-        counts[j] = ok;
+#pragma unroll
+        for (int o = 1; o < 32; o *= 2) {  // lanes in order: the same bits in every lane
+            const float om = __shfl_xor_sync(0xFFFFFFFFu, m, o), os = __shfl_xor_sync(0xFFFFFFFFu, s, o);
+            float lm = lane & o ? om : m, ls = lane & o ? os : s;
+            add_exp(lm, ls, lane & o ? m : om, lane & o ? s : os);
+            m = lm;
+            s = ls;
+        }
+        if (lane == 0) {
+            const float lse = m + logf(s);
+            if (a.lse) a.lse[t] = lse;
+            if (a.loss) a.loss[t] = ok ? lse - z : 0.0f;
+            if (GRAD) {
+                a.lse_ws[t] = lse;
+                a.row_weight[t] = tw;
+                if (isfinite(tw)) atomicMax(a.w_max, __float_as_uint(fabsf(tw)));
+            }
+            counts[warp] = ok;
+        }
     }
     if (!GRAD) return;
     __syncthreads();
@@ -641,11 +560,10 @@ bool make_map(CUtensorMap *m, int dtype, const void *ptr, long long rows, long l
 template <int MODE, int DT>
 cudaError_t launch_tiles(const rar_ctx *h, const XentArgs &k, const XentMaps &maps, int b0, int nb, cudaStream_t stream) {
     auto kern = xent_tile_kernel<MODE, DT>;
-    constexpr int smem = Mode<MODE>::stages * Mode<MODE>::stage_bytes + 1024;  // + alignment to the swizzle's 1024 bytes
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcSmem);
     if (e != cudaSuccess) return e;
     const int pairs = std::min(xent_items<MODE>(k, nb), h->sm_count / 2);
-    return launch_pdl(kern, dim3((unsigned)(2 * pairs)), dim3(kTcThreads), smem, stream, k, maps, b0, nb);
+    return launch_pdl(kern, dim3((unsigned)(2 * pairs)), dim3(kTcThreads), kTcSmem, stream, k, maps, b0, nb);
 }
 
 void plan_blocks(size_t vocab, int p, XentArgs *k) {
@@ -765,11 +683,10 @@ int vocab_xent(rar_ctx *h, const rar_vocab_xent_args *a, cudaStream_t stream) {
 
     k.limits = {h->status, h->opt.timeout_ns ? h->opt.timeout_ns : 2000000000ull};
 
-    const bool few = k.tokens <= kFewTokens;
     XentMaps logits, dh, dw;  // of the products that use them
     bool mapped = true;
     if (k.tokens) {
-        mapped = make_map(&logits.one, a->dtype, k.hidden, k.tokens, k.dim, k.hidden_stride, few ? 64 : 128);
+        mapped = make_map(&logits.one, a->dtype, k.hidden, k.tokens, k.dim, k.hidden_stride, 128);
         for (int r = 0; r < k.p && mapped; r++) {
             const long long rows = k.base + (r < k.extra ? 1 : 0);
             if (rows) mapped = make_map(&logits.w[r], a->dtype, k.w.inl[r], rows, k.dim, k.weight_stride, 128);
@@ -793,14 +710,14 @@ int vocab_xent(rar_ctx *h, const rar_vocab_xent_args *a, cudaStream_t stream) {
             }
             return e;
         }
-        e = few ? launch_tiles<XENT_STATS_FEW, DT>(h, k, logits, 0, k.n_blocks, stream) : launch_tiles<XENT_STATS, DT>(h, k, logits, 0, k.n_blocks, stream);
+        e = launch_tiles<XENT_STATS, DT>(h, k, logits, 0, k.n_blocks, stream);
         if (e == cudaSuccess)
             e = launch_pdl(grad ? xent_join_kernel<DT, true> : xent_join_kernel<DT, false>, dim3((unsigned)((k.tokens + 7) / 8)),
                            dim3(256), 0, stream, k);
         if (!grad) return e;
         for (int b0 = 0; b0 < k.n_blocks && e == cudaSuccess; b0 += k.window) {
             const int nb = std::min(k.window, k.n_blocks - b0);
-            e = few ? launch_tiles<XENT_G_FEW, DT>(h, k, logits, b0, nb, stream) : launch_tiles<XENT_G, DT>(h, k, logits, b0, nb, stream);
+            e = launch_tiles<XENT_G, DT>(h, k, logits, b0, nb, stream);
             if (e == cudaSuccess && k.dhidden) {
                 XentArgs kw = k;
                 kw.splits = std::min(k.splits, nb);
