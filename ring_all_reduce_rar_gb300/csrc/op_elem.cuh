@@ -59,7 +59,10 @@ __device__ __forceinline__ float warp_sum(float v) {
 // The scale of a group whose largest magnitude is amax: the e4m3 range
 // [-448, 448] spans the group; never 0, infinite or NaN.
 __device__ __forceinline__ float scale_of(float amax) {
-    return fmaxf(__fdiv_rn(fminf(amax, 3.402823466e38f), 448.0f), 1.175494351e-38f);
+    constexpr float kInv = 1.0f / 448.0f;
+    const float x = fminf(amax, 3.402823466e38f), q = x * kInv;
+    // the quotient, rounded once (see CodeOf; one below 2^-126 is not used)
+    return fmaxf(fmaf(fmaf(-q, 448.0f, x), kInv, q), 1.175494351e-38f);
 }
 // Codes of values divided by a scale.  The product with the reciprocal,
 // corrected once by its remainder, is the correctly rounded quotient (Markstein
@@ -70,7 +73,7 @@ struct CodeOf {
     float scale, inv;
     __device__ __forceinline__ explicit CodeOf(float s) {
         scale = s;
-        inv = __fdiv_rn(1.0f, s);
+        inv = __frcp_rn(s);
     }
     __device__ __forceinline__ float quotient(float v) const {
         const float q = v * inv, r = fmaf(-q, scale, v), c = fmaf(r, inv, q);
@@ -112,6 +115,15 @@ struct RowBits {
         else return widen<DT>(e % 2 ? w[e / 2] >> 16 : w[e / 2] & 0xFFFFu);
     }
 };
+// s += the vector, element by element; two elements an instruction.
+template <int DT>
+__device__ __forceinline__ void add_vec(float (&s)[RowBits<DT>::VE], const RowBits<DT> &b) {
+#pragma unroll
+    for (int e = 0; e < RowBits<DT>::VE; e += 2)
+        asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %3};\n\tadd.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+            : "+f"(s[e]), "+f"(s[e + 1])
+            : "f"(b.get(e)), "f"(b.get(e + 1)));
+}
 template <int DT>
 __device__ __forceinline__ void store_vec(void *row, int vec, const float *f) {
     uint4 q;

@@ -124,6 +124,9 @@ inline bool vec16(const void *ptr, size_t rows, long long stride, size_t e) {
     return (uintptr_t)ptr % 16 == 0 && (rows <= 1 || (size_t)stride * e % 16 == 0);
 }
 
+// The handle's bound on every wait of a call.
+inline unsigned long long op_timeout_ns(const rar_ctx *h) { return h->opt.timeout_ns ? h->opt.timeout_ns : 2000000000ull; }
+
 // Runs an entry point's body: no C++ exception leaves the library.
 template <typename F>
 int guarded(rar_ctx *h, F &&body) {

@@ -755,8 +755,9 @@ int rar_status(rar_handle h) {
                           "ring wait timed out: rank %d, step %d, slice %d, waiting on rank %d "
                           "(progress word 0x%llx, wanted 0x%llx)",
                           st.rank, st.step, st.slice, st.waited_on, st.flag_seen, st.flag_wanted);
-        else if (st.rank == -2)
-            std::snprintf(buf, sizeof(buf), "tile wait timed out: CTA %d, role %d (vocabulary cross entropy)", st.slice, st.step);
+        else if (st.rank <= -2)  // (WAIT_OF_XENT, WAIT_OF_NORM)
+            std::snprintf(buf, sizeof(buf), "%s wait timed out: CTA %d, role %d (%s)", st.rank == -2 ? "tile" : "row", st.slice, st.step,
+                          st.rank == -2 ? "vocabulary cross entropy" : "residual norm");
         else
             std::snprintf(buf, sizeof(buf),
                           "bulk-copy wait timed out: tile %d, step %d, waiting for rank %d's tile (fused streaming "

@@ -12,14 +12,11 @@
 //       apart, the next 64 columns are the next box; a step of 16 along K is 2048
 //       bytes further.
 // So no operand is transposed in memory.
-//
-// Every wait has a limit.  A wait that runs out raises the CTA's flag, which the other
-// waits of the CTA poll, and records it for rar_status.
 #pragma once
 
 #include <cuda.h>
 
-#include "op_elem.cuh"
+#include "async_copy.cuh"
 
 namespace rar {
 
@@ -39,7 +36,6 @@ struct TcShared {
     int failed;
 };
 
-__device__ __forceinline__ uint32_t smem_u32(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -54,70 +50,12 @@ __device__ __forceinline__ uint32_t peer_addr(uint32_t addr, uint32_t rank) {
 __device__ __forceinline__ void cluster_sync_all() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-__device__ __forceinline__ void tc_mbar_init(uint64_t *bar, uint32_t count) {
-    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(count) : "memory");
-}
-__device__ __forceinline__ void tc_expect_tx(uint64_t *bar, uint32_t bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
-}
 __device__ __forceinline__ void tc_arrive_cluster(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
-__device__ __forceinline__ bool tc_try_wait(uint32_t bar, uint32_t parity) {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred P;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 P, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, P;\n\t}"
-        : "=r"(done)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return done != 0;
-}
-__device__ __forceinline__ unsigned long long tc_now_ns() {
-    unsigned long long t;
-    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-    return t;
-}
-
-struct TcLimits {
-    RingStatus *status;
-    unsigned long long timeout_ns;
-};
-constexpr int kTcStatusRank = -2;  // RingStatus::rank of a wait that ran out here
-
-// Waits for the phase of `bar` with this parity; false once the limit has
-// passed or another wait of the CTA has given up.  role: what was waited for.
-__device__ __forceinline__ bool tc_wait(TcShared *sh, const TcLimits &lim, uint64_t *bar, uint32_t parity, int role) {
-    const uint32_t addr = smem_u32(bar);
-    if (tc_try_wait(addr, parity)) return true;
-    const unsigned long long t0 = tc_now_ns();
-    const unsigned long long most = lim.timeout_ns / 16ull + (1ull << 20);
-    for (unsigned long long it = 0; it < most; it++) {
-        if (tc_try_wait(addr, parity)) return true;
-        if ((it & 63) == 63) {
-            if (*(volatile int *)&sh->failed) return false;
-            if (tc_now_ns() - t0 > lim.timeout_ns) break;
-        }
-    }
-    *(volatile int *)&sh->failed = 1;
-    lim.status->code = RAR_ETIMEOUT;
-    lim.status->rank = kTcStatusRank;
-    lim.status->step = role;
-    lim.status->slice = (int)blockIdx.x;
-    __threadfence();
-    atomicAdd(&lim.status->seq, 1u);
-    return false;
-}
-
-// Waits for loads that were issued: they land by themselves, so the limit
-// (1 s) is only reached when the other CTA of a failed pair never issued its own.
-__device__ __forceinline__ void tc_drain(uint64_t *bar, uint32_t parity) {
-    const unsigned long long t0 = tc_now_ns();
-    for (unsigned long long it = 0; it < (1ull << 32); it++) {
-        if (tc_try_wait(smem_u32(bar), parity)) return;
-        if ((it & 63) == 63 && tc_now_ns() - t0 > 1000000000ull) return;
-    }
+// Waits for a barrier of the pair (see mbar_wait); role: what was waited for.
+__device__ __forceinline__ bool tc_wait(TcShared *sh, const WaitLimits &lim, uint64_t *bar, uint32_t parity, int role) {
+    return mbar_wait(&sh->failed, lim, bar, parity, WAIT_OF_XENT, role);
 }
 
 __device__ __forceinline__ void tc_prefetch_map(const CUtensorMap *map) {
@@ -193,14 +131,14 @@ __device__ __forceinline__ void tc_begin(TcShared *sh) {
     if (threadIdx.x == 0) {
         sh->failed = 0;
         for (int s = 0; s < kTcStages; s++) {
-            tc_mbar_init(&sh->full[s], 1);
-            tc_mbar_init(&sh->empty[s], 1);
+            mbar_init(&sh->full[s], 1);
+            mbar_init(&sh->empty[s], 1);
         }
         for (int s = 0; s < 2; s++) {
-            tc_mbar_init(&sh->acc_full[s], 1);
-            tc_mbar_init(&sh->acc_empty[s], 2 * kTcEpilogueWarps);
+            mbar_init(&sh->acc_full[s], 1);
+            mbar_init(&sh->acc_empty[s], 2 * kTcEpilogueWarps);
         }
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        mbar_fence_init();
     }
     if (threadIdx.x / 32 == kTcEpilogueWarps) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sh->tmem)) : "memory");

@@ -56,7 +56,7 @@ struct XentArgs {
     int window;           // blocks of a window
     int splits;           // of dhidden's sum over a window
     bool direct;          // one split: the last window writes dhidden itself
-    TcLimits limits;
+    WaitLimits limits;
 };
 
 // Tensor maps of a launch: `one` is the operand that is one matrix (hidden or G),
@@ -355,7 +355,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
                 // rows of the accumulator are never read
                 auto a_rows = [&](int r) { return MODE == XENT_DWEIGHT || it.row + r * 128 < a.tokens; };
                 if (rank == 0 && lane == 0)
-                    tc_expect_tx(&sh.full[st], 32768u + 16384u * (1u + a_rows(1)));
+                    mbar_expect_tx(&sh.full[st], 32768u + 16384u * (1u + a_rows(1)));
                 const uint32_t bar = peer_addr(smem_u32(&sh.full[st]), 0);
                 const uint32_t to = stages + st * kTcStageBytes + (is_a ? 0 : 16384) + part * 128;
                 const CUtensorMap *map = is_a ? &maps.one : &maps.w[MODE == XENT_DWEIGHT ? 0 : b.piece];
@@ -373,7 +373,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
         // way (the loads even after a wait that ran out)
         for (unsigned k = step > kTcStages ? step - kTcStages : 0; k < step && lane == 0; k++) {
             const int st = (int)(k % kTcStages);
-            if (rank == 0) tc_drain(&sh.full[st], (k / kTcStages) & 1);
+            if (rank == 0) mbar_drain(&sh.full[st], (k / kTcStages) & 1);
             tc_wait(&sh, a.limits, &sh.empty[st], (k / kTcStages) & 1, 1);
         }
     } else if (warp == kTcEpilogueWarps + 1 && lane == 0 && rank == 0) {
@@ -681,7 +681,7 @@ int vocab_xent(rar_ctx *h, const rar_vocab_xent_args *a, cudaStream_t stream) {
     k.want_dw = a->dweights != nullptr;
     note_op_call(h, a->p, stream);
 
-    k.limits = {h->status, h->opt.timeout_ns ? h->opt.timeout_ns : 2000000000ull};
+    k.limits = {h->status, op_timeout_ns(h)};
 
     XentMaps logits, dh, dw;  // of the products that use them
     bool mapped = true;
