@@ -21,7 +21,7 @@ LIB_PATH = os.path.join(BUILD_DIR, "librar.so")
 TORCH_OPS_PATH = os.path.join(BUILD_DIR, "_torch_ops.so")
 
 SOURCES = ["rar_api.cu", "fused.cu", "fused_stream.cu", "ring.cu", "ll.cu", "tree.cu", "noalloc.cu",
-           "rmsnorm.cu", "vocab_xent.cu", "embedding.cu"]
+           "rmsnorm.cu", "rmsnorm_grad.cu", "vocab_xent.cu", "embedding.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-ftz=false", "-prec-div=true",
               "-prec-sqrt=true", "-fmad=false", "-Xptxas", "-warn-spills", "-I", INCLUDE, "-I", CSRC]

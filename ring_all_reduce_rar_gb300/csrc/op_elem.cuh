@@ -131,6 +131,47 @@ __device__ __forceinline__ void store_vec(void *row, int vec, const float *f) {
     else q = narrow8<DT>(f);
     static_cast<uint4 *>(row)[vec] = q;
 }
+// A row of `dim` elements in 16-byte vectors.  ODD: the row begins anywhere in
+// one; its elements are [lo, lo + dim) from that vector's first, and the vectors
+// at its ends are accessed by the elements that belong to the row.
+template <int DT, bool ODD>
+struct RowView {
+    static constexpr int VE = RowBits<DT>::VE, EB = ElemInfo<DT>::bytes;
+    int lo, hi;  // lo 0 and hi a multiple of VE unless ODD; hi 0: no row
+    __device__ __forceinline__ bool has(int vec) const { return vec * VE < hi; }
+    __device__ __forceinline__ bool has(int vec, int e) const { return !ODD ? has(vec) : vec * VE + e >= lo && vec * VE + e < hi; }
+    __device__ __forceinline__ bool whole(int vec) const { return !ODD ? has(vec) : vec * VE >= lo && vec * VE + VE <= hi; }
+    // the row's element that element e of a vector is
+    __device__ __forceinline__ int column(int vec, int e) const { return vec * VE + e - lo; }
+    __device__ __forceinline__ void load_elems(const char *row, int vec, RowBits<DT> &b) const {
+        b.w[0] = b.w[1] = b.w[2] = b.w[3] = 0u;
+#pragma unroll
+        for (int e = 0; e < VE; e++)
+            if (has(vec, e)) {
+                const uint32_t x = load_elem<DT>(row, column(vec, e));
+                if (VE == 4) b.w[e] = x;
+                else b.w[e / 2] |= e % 2 ? x << 16 : x;
+            }
+    }
+    __device__ __forceinline__ void load(const char *row, int vec, RowBits<DT> &b) const {
+        if (!ODD || whole(vec)) b.load(row - lo * EB, vec, has(vec));
+        else load_elems(row, vec, b);
+    }
+    // of one vector of columns (weight), which has no part in the row's alignment
+    __device__ __forceinline__ void load_columns(const void *v, int vec, RowBits<DT> &b) const {
+        if (!ODD) b.load(v, vec, has(vec));
+        else load_elems(static_cast<const char *>(v), vec, b);
+    }
+    __device__ __forceinline__ void store(char *row, int vec, const float *f) const {
+        if (whole(vec)) {
+            store_vec<DT>(row - lo * EB, vec, f);
+        } else if (ODD) {
+#pragma unroll
+            for (int e = 0; e < VE; e++)
+                if (has(vec, e)) store_f<DT>(row, column(vec, e), f[e]);
+        }
+    }
+};
 // chunk_of with 32-bit divisions where the buffer allows them.
 struct Chunks {
     long long base, extra;
