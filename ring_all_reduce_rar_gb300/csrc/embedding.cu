@@ -152,17 +152,33 @@ __device__ __forceinline__ void sort_tokens(const SortArgs &s, unsigned *smem, i
                 }
             }
         };
-        auto digit = [&](int k, unsigned i0) { return i0 + 32 * k + lane < hi ? it[k].x >> (pass * width) & (bins - 1) : bins; };
+        auto digit = [&](int k) { return it[k].x >> (pass * width) & (bins - 1); };
+        // the lanes with the same digit in each round (a vote a bit: matching all
+        // lanes' values in one instruction takes ten times as long), 0 where the lane has no item
+        unsigned peers[kSortHeld];
+        auto match = [&](unsigned i0) {
+#pragma unroll
+            for (int k = 0; k < kSortHeld; k++) peers[k] = __ballot_sync(0xFFFFFFFFu, i0 + 32 * k + lane < hi);
+            for (int b = 0; b < width; b++)
+#pragma unroll
+                for (int k = 0; k < kSortHeld; k++) {
+                    const bool bit = digit(k) >> b & 1;
+                    const unsigned with = __ballot_sync(0xFFFFFFFFu, bit);
+                    peers[k] &= bit ? with : ~with;
+                }
+#pragma unroll
+            for (int k = 0; k < kSortHeld; k++)
+                if (i0 + 32 * k + lane >= hi) peers[k] = 0u;
+        };
         load(lo);
         for (unsigned i = threadIdx.x; i < bins * kSortPitch; i += kSortThreads) count[i] = 0u;
         __syncthreads();
         for (unsigned i0 = lo; i0 < hi; i0 += 32 * kSortHeld) {
             if (i0 != lo) load(i0);
+            match(i0);
 #pragma unroll
             for (int k = 0; k < kSortHeld; k++) {
-                if (i0 + 32 * k >= hi) break;
-                const unsigned d = digit(k, i0), peers = __match_any_sync(0xFFFFFFFFu, d);
-                if (d < bins && lane == __ffs(peers) - 1) count[d * kSortPitch + warp] += __popc(peers);
+                if (peers[k] && lane == __ffs(peers[k]) - 1) count[digit(k) * kSortPitch + warp] += __popc(peers[k]);
                 __syncwarp();
             }
         }
@@ -205,17 +221,15 @@ __device__ __forceinline__ void sort_tokens(const SortArgs &s, unsigned *smem, i
         if (threadIdx.x < bins) start[threadIdx.x] = base + x - all + before;
         __syncthreads();
         for (unsigned i0 = lo; i0 < hi; i0 += 32 * kSortHeld) {
-            if (!held) load(i0);
+            if (!held) load(i0), match(i0);
 #pragma unroll
             for (int k = 0; k < kSortHeld; k++) {
-                if (i0 + 32 * k >= hi) break;
-                const unsigned d = digit(k, i0), peers = __match_any_sync(0xFFFFFFFFu, d);
-                const unsigned ahead = __popc(peers & ((1u << lane) - 1));
-                const unsigned at = d < bins ? count[d * kSortPitch + warp] : 0u;
+                const unsigned d = digit(k), ahead = __popc(peers[k] & ((1u << lane) - 1));
+                const unsigned at = peers[k] ? count[d * kSortPitch + warp] : 0u;
                 __syncwarp();
-                if (d < bins) {
+                if (peers[k]) {
                     out[start[d] + at + ahead] = it[k];
-                    if (ahead == 0) count[d * kSortPitch + warp] = at + __popc(peers);
+                    if (ahead == 0) count[d * kSortPitch + warp] = at + __popc(peers[k]);
                 }
                 __syncwarp();
             }
@@ -342,67 +356,81 @@ struct GradCols {
     }
 };
 
+// What is done with an item of a chunk: its row of dout is added, and, where
+// its run leaves the chunk, the sum goes to `to`.
+struct RunStep {
+    const char *from;  // NULL: left out
+    char *to;          // NULL: the run goes on
+    bool table;        // `to` is the run's row of the table, else of the workspace
+};
+
 // ADD: accumulate.  The row that a run is added to is read together with the
 // run's last row of dout.
 template <int DT, bool VEC, bool ADD>
-__global__ void __launch_bounds__(kReduceThreads, ADD ? 2 : 3) embedding_runs_kernel(const __grid_constant__ SortArgs s) {
+__global__ void __launch_bounds__(kReduceThreads, 3) embedding_runs_kernel(const __grid_constant__ SortArgs s) {
     using Cols = GradCols<DT, VEC>;
     constexpr int N = Cols::N, EB = ElemInfo<DT>::bytes;
+    __shared__ RunStep steps[kMinChunk];
     const EmbedArgs &a = s.e;
     pdl_wait();
     pdl_launch_dependents();
     const Chunks chunks(a.vocab, a.p);
     const uint2 *items = s.items[s.passes & 1];
-    const Cols cols{a.dim, (long long)blockIdx.y * kReduceThreads * N, (int)threadIdx.x, kReduceThreads};
+    const Cols cols{a.dim, (long long)blockIdx.y * blockDim.x * N, (int)threadIdx.x, (int)blockDim.x};
     const int lo = blockIdx.x * s.chunk, hi = (int)min((long long)lo + s.chunk, a.n_tokens);
-    const unsigned none = (unsigned)a.vocab;  // left out: sorted last
     float sum[N] = {};
-    bool began = lo == 0 || items[lo - 1].x != items[lo].x;  // the run begins in this chunk
-    for (int i0 = lo; i0 < hi; i0 += kReduceAhead) {
-        uint2 it[kReduceAhead];
-        unsigned after[kReduceAhead];  // the next item's index
-#pragma unroll
-        for (int u = 0; u < kReduceAhead; u++) {
-            it[u] = i0 + u < hi ? items[i0 + u] : make_uint2(none, 0);
-            after[u] = i0 + u + 1 < a.n_tokens ? items[i0 + u + 1].x : none + 1;
+    for (int i0 = lo; i0 < hi; i0 += kMinChunk) {
+        if (threadIdx.x < kMinChunk) {
+            const int i = i0 + threadIdx.x;
+            const uint2 it = items[min(i, hi - 1)];
+            const unsigned none = (unsigned)a.vocab;  // left out: sorted last
+            const unsigned after = i + 1 < a.n_tokens ? items[i + 1].x : none + 1, before = lo ? items[lo - 1].x : none + 1;
+            const bool ends = it.x != after, began = it.x != before;  // the run, in this chunk
+            RunStep st{nullptr, nullptr, ends && began};
+            if (i < hi && it.x != none) {
+                st.from = static_cast<const char *>(a.dout) + it.y * a.row_stride * EB;
+                if (ends || i + 1 == hi)
+                    st.to = st.table ? table_row(a, chunks, it.x, EB) : reinterpret_cast<char *>(s.part + ((long long)blockIdx.x * 2 + (began ? 1 : 0)) * a.dim);
+            }
+            steps[threadIdx.x] = st;
         }
-        typename Cols::Bits f[kReduceAhead], old[ADD ? kReduceAhead : 1];
+        __syncthreads();
+#pragma unroll 1
+        for (int k0 = 0; k0 < kMinChunk; k0 += kReduceAhead) {
+            typename Cols::Bits f[kReduceAhead], old[ADD ? kReduceAhead : 1];
 #pragma unroll
-        for (int u = 0; u < kReduceAhead; u++) {
-            f[u] = cols.load(static_cast<const char *>(a.dout) + it[u].y * a.row_stride * EB, it[u].x != none);
-            if (ADD) {
-                const bool ends = it[u].x != none && it[u].x != after[u];
-                old[u] = cols.load(ends ? table_row(a, chunks, it[u].x, EB) : nullptr, ends);
+            for (int u = 0; u < kReduceAhead; u++) {
+                const RunStep &st = steps[k0 + u];
+                f[u] = cols.load(st.from, st.from != nullptr);
+                if (ADD) old[u] = cols.load(st.to, st.to && st.table);
+            }
+#pragma unroll
+            for (int u = 0; u < kReduceAhead; u++) {
+                const RunStep &st = steps[k0 + u];
+                if (!st.from) continue;
+#pragma unroll
+                for (int e = 0; e < N; e++) sum[e] += f[u].get(e);
+                if (!st.to) continue;
+                if (st.table) cols.finish(st.to, sum, a.scale, ADD, old[ADD ? u : 0]);
+                else cols.store_part(reinterpret_cast<float *>(st.to), sum);
+#pragma unroll
+                for (int e = 0; e < N; e++) sum[e] = 0.0f;
             }
         }
-#pragma unroll
-        for (int u = 0; u < kReduceAhead; u++) {
-            if (it[u].x == none) continue;
-#pragma unroll
-            for (int e = 0; e < N; e++) sum[e] += f[u].get(e);
-            const bool ends = it[u].x != after[u];
-            if (!ends && i0 + u + 1 < hi) continue;
-            if (began && ends) cols.finish(table_row(a, chunks, it[u].x, EB), sum, a.scale, ADD, old[ADD ? u : 0]);
-            else cols.store_part(s.part + ((long long)blockIdx.x * 2 + (began ? 1 : 0)) * a.dim, sum);
-            began = true;
-#pragma unroll
-            for (int e = 0; e < N; e++) sum[e] = 0.0f;
-        }
+        __syncthreads();
     }
 }
 
-// A run that begins in chunk blockIdx.x and goes on beyond it: 8 warps take every
-// eighth chunk, and their sums are added in order.
+// A run that begins in chunk blockIdx.x and goes on beyond it.
 template <int DT, bool VEC, bool ADD>
 __global__ void __launch_bounds__(kReduceThreads) embedding_join_kernel(const __grid_constant__ SortArgs s) {
     using Cols = GradCols<DT, VEC>;
-    constexpr int N = Cols::N, kWarps = kReduceThreads / 32;
-    __shared__ float sums[kWarps][N][32];
+    constexpr int N = Cols::N;
     const EmbedArgs &a = s.e;
     pdl_wait();
     pdl_launch_dependents();
     const uint2 *items = s.items[s.passes & 1];
-    const int c0 = blockIdx.x, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int c0 = blockIdx.x;
     const long long lo = (long long)c0 * s.chunk, hi = min(lo + s.chunk, a.n_tokens);
     if (hi == a.n_tokens) return;
     const unsigned key = items[hi - 1].x, next = items[hi].x, before = lo ? items[lo - 1].x : (unsigned)a.vocab;
@@ -410,31 +438,29 @@ __global__ void __launch_bounds__(kReduceThreads) embedding_join_kernel(const __
     if (key == (unsigned)a.vocab || next != key || before == key) return;
     // the chunk that it ends in: the chunks after c0 that begin with its key
     int last = c0;
-    for (int c = c0 + 1;; c += kReduceThreads) {
+    for (int c = c0 + 1;; c += blockDim.x) {
         const int mine = c + (int)threadIdx.x;
         const int more = __syncthreads_count(mine < s.n_chunks && items[(long long)mine * s.chunk].x == key);
         last += more;
-        if (more < kReduceThreads) break;
+        if (more < (int)blockDim.x) break;
     }
-    const Cols cols{a.dim, (long long)blockIdx.y * 32 * N, lane, 32};
+    const Cols cols{a.dim, (long long)blockIdx.y * blockDim.x * N, (int)threadIdx.x, (int)blockDim.x};
     char *row = table_row(a, Chunks(a.vocab, a.p), key, ElemInfo<DT>::bytes);
-    const typename Cols::Bits old = cols.load(row, ADD && warp == 0);
-    float sum[N] = {};
-    if (warp == 0) cols.load_part(s.part + ((long long)c0 * 2 + 1) * a.dim, sum);
-#pragma unroll 4
-    for (int c = c0 + 1 + warp; c <= last; c += kWarps) {
-        float f[N];
-        cols.load_part(s.part + (long long)c * 2 * a.dim, f);
+    const typename Cols::Bits old = cols.load(row, ADD);
+    float sum[N];
+    cols.load_part(s.part + ((long long)c0 * 2 + 1) * a.dim, sum);
+    constexpr int kAhead = 8;  // chunks whose loads are in flight together
+#pragma unroll 1
+    for (int c = c0 + 1; c <= last; c += kAhead) {
+        float f[kAhead][N];
 #pragma unroll
-        for (int e = 0; e < N; e++) sum[e] += f[e];
+        for (int u = 0; u < kAhead; u++) cols.load_part(s.part + (long long)min(c + u, last) * 2 * a.dim, f[u]);
+#pragma unroll
+        for (int u = 0; u < kAhead; u++)
+            if (c + u <= last)
+#pragma unroll
+                for (int e = 0; e < N; e++) sum[e] += f[u][e];
     }
-#pragma unroll
-    for (int e = 0; e < N; e++) sums[warp][e][lane] = sum[e];
-    __syncthreads();
-    if (warp) return;
-    for (int w = 1; w < kWarps; w++)
-#pragma unroll
-        for (int e = 0; e < N; e++) sum[e] += sums[w][e][lane];
     cols.finish(row, sum, a.scale, ADD, old);
 }
 
@@ -606,12 +632,14 @@ int embedding_grad(rar_ctx *h, const rar_embedding_grad_args *a, cudaStream_t st
             cudaError_t e1 = launch_clusters(embedding_sort_kernel<DT, VEC>, sorters + clear, cluster, stream, sort, (int)sorters);
             if (e1 != cudaSuccess || sorters == 0) return e1;
             constexpr int N = GradCols<DT, VEC>::N;
-            auto grid = [&](int threads) { return dim3((unsigned)sort.n_chunks, (unsigned)((a->dim + threads * N - 1) / (threads * N))); };
-            e1 = launch_pdl(a->accumulate ? embedding_runs_kernel<DT, VEC, true> : embedding_runs_kernel<DT, VEC, false>, grid(kReduceThreads),
-                            dim3(kReduceThreads), 0, stream, sort);
+            // no more threads than the row has columns for
+            const int threads = (int)std::min<size_t>(((a->dim + N - 1) / N + 31) / 32 * 32, kReduceThreads);
+            const dim3 grid((unsigned)sort.n_chunks, (unsigned)((a->dim + threads * N - 1) / (threads * N)));
+            e1 = launch_pdl(a->accumulate ? embedding_runs_kernel<DT, VEC, true> : embedding_runs_kernel<DT, VEC, false>, grid, dim3((unsigned)threads),
+                            0, stream, sort);
             if (e1 == cudaSuccess && sort.n_chunks > 1)
-                e1 = launch_pdl(a->accumulate ? embedding_join_kernel<DT, VEC, true> : embedding_join_kernel<DT, VEC, false>, grid(32),
-                                dim3(kReduceThreads), 0, stream, sort);
+                e1 = launch_pdl(a->accumulate ? embedding_join_kernel<DT, VEC, true> : embedding_join_kernel<DT, VEC, false>, grid,
+                                dim3((unsigned)threads), 0, stream, sort);
             return e1;
         };
         return vec ? steps(IntC<1>{}) : steps(IntC<0>{});
