@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(256) embedding_kernel(const __grid_constant__ 
 // ---- gradient
 //
 // 1. The tokens are sorted by index, equal ones in the order of their places
-//    (radix sort by one cluster); meanwhile the other CTAs clear the table.
+//    (radix sort by one cluster), while the table is cleared.
 // 2. The sorted places are cut into chunks.  A CTA adds up the runs of its chunk in
 //    order; a run inside the chunk is written to the table, one that goes
 //    on beyond it into the workspace.
@@ -102,7 +102,7 @@ constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32;
 constexpr int kSortMaxBits = 9;       // of a pass
 constexpr int kSortCluster = 8;       // CTAs that sort, for more than kSortOneCta tokens
 constexpr int kSortHeld = 8;          // items a thread in flight
-constexpr int kSortOneCta = kSortThreads * kSortHeld;
+constexpr int kSortOneCta = 2 * kSortThreads;
 constexpr int kSortPitch = kSortWarps + 1;  // counts of a digit, one a warp (odd: no bank conflicts)
 constexpr int kSortSmem = (kSortPitch + 2) * (1 << kSortMaxBits) * (int)sizeof(unsigned);
 
@@ -136,6 +136,7 @@ __device__ __forceinline__ void sort_tokens(const SortArgs &s, unsigned *smem, i
     for (int pass = 0; pass < s.passes; pass++) {
         const uint2 *in = s.items[pass & 1];
         uint2 *out = s.items[(pass & 1) ^ 1];
+        const int shift = pass * width;
         uint2 it[kSortHeld];
         // the items of kSortHeld rounds of 32 from place i0, loads in flight together
         auto load = [&](unsigned i0) {
@@ -152,23 +153,25 @@ __device__ __forceinline__ void sort_tokens(const SortArgs &s, unsigned *smem, i
                 }
             }
         };
-        auto digit = [&](int k) { return it[k].x >> (pass * width) & (bins - 1); };
+        auto digit = [&](int k) { return it[k].x >> shift & (bins - 1); };
         // the lanes with the same digit in each round (a vote a bit: matching all
-        // lanes' values in one instruction takes ten times as long), 0 where the lane has no item
+        // lanes' values in one instruction takes longer), 0 where the lane has no item
         unsigned peers[kSortHeld];
         auto match = [&](unsigned i0) {
 #pragma unroll
-            for (int k = 0; k < kSortHeld; k++) peers[k] = __ballot_sync(0xFFFFFFFFu, i0 + 32 * k + lane < hi);
-            for (int b = 0; b < width; b++)
+            for (int k = 0; k < kSortHeld; k++) {
+                peers[k] = 0u;
+                if (i0 + 32 * k >= hi) continue;
+                const unsigned d = digit(k);
+                const bool has = i0 + 32 * k + lane < hi;
+                unsigned same = __ballot_sync(0xFFFFFFFFu, has);
 #pragma unroll
-                for (int k = 0; k < kSortHeld; k++) {
-                    const bool bit = digit(k) >> b & 1;
-                    const unsigned with = __ballot_sync(0xFFFFFFFFu, bit);
-                    peers[k] &= bit ? with : ~with;
+                for (int b = 0; b < kSortMaxBits; b++) {
+                    const unsigned with = __ballot_sync(0xFFFFFFFFu, d >> b & 1);
+                    same &= d >> b & 1 ? with : ~with;
                 }
-#pragma unroll
-            for (int k = 0; k < kSortHeld; k++)
-                if (i0 + 32 * k + lane >= hi) peers[k] = 0u;
+                peers[k] = has ? same : 0u;
+            }
         };
         load(lo);
         for (unsigned i = threadIdx.x; i < bins * kSortPitch; i += kSortThreads) count[i] = 0u;
@@ -178,35 +181,48 @@ __device__ __forceinline__ void sort_tokens(const SortArgs &s, unsigned *smem, i
             match(i0);
 #pragma unroll
             for (int k = 0; k < kSortHeld; k++) {
+                if (i0 + 32 * k >= hi) break;
                 if (peers[k] && lane == __ffs(peers[k]) - 1) count[digit(k) * kSortPitch + warp] += __popc(peers[k]);
                 __syncwarp();
             }
         }
         __syncthreads();
-        // a digit's warps: a warp a digit, lane = warp
-        for (unsigned d = warp; d < bins; d += kSortWarps) {
-            const unsigned c = count[d * kSortPitch + lane];
-            unsigned x = c;
+        // a digit's warps: a warp a digit, lane = warp; four digits side by side
+        for (unsigned d0 = warp; d0 < bins; d0 += 4 * kSortWarps) {
+            unsigned c[4], x[4];
 #pragma unroll
-            for (int o = 1; o < 32; o *= 2) {
-                const unsigned y = __shfl_up_sync(0xFFFFFFFFu, x, o);
-                if (lane >= o) x += y;
+            for (int k = 0; k < 4; k++) x[k] = c[k] = d0 + k * kSortWarps < bins ? count[(d0 + k * kSortWarps) * kSortPitch + lane] : 0u;
+#pragma unroll
+            for (int o = 1; o < 32; o *= 2)
+#pragma unroll
+                for (int k = 0; k < 4; k++) {
+                    const unsigned y = __shfl_up_sync(0xFFFFFFFFu, x[k], o);
+                    if (lane >= o) x[k] += y;
+                }
+#pragma unroll
+            for (int k = 0; k < 4; k++) {
+                if (d0 + k * kSortWarps >= bins) break;
+                count[(d0 + k * kSortWarps) * kSortPitch + lane] = x[k] - c[k];
+                if (lane == 31) total[d0 + k * kSortWarps] = x[k];
             }
-            count[d * kSortPitch + lane] = x - c;
-            if (lane == 31) total[d] = x;
         }
         __syncthreads();
         if (ctas > 1) sort_cluster_sync();
         // where the digit's items begin, and this CTA's among them
         unsigned all = 0, before = 0;
         if (threadIdx.x < bins) {
-            if (ctas == 1) all = total[threadIdx.x];
-            else
-                for (int c = 0; c < ctas; c++) {
-                    const unsigned x = dsmem_load(total + threadIdx.x, c);
-                    all += x;
-                    if (c < cta) before += x;
+            if (ctas == 1) {
+                all = total[threadIdx.x];
+            } else {
+                unsigned t[kSortCluster];  // (ctas is kSortCluster: loads in flight together)
+#pragma unroll
+                for (int c = 0; c < kSortCluster; c++) t[c] = dsmem_load(total + threadIdx.x, c);
+#pragma unroll
+                for (int c = 0; c < kSortCluster; c++) {
+                    all += t[c];
+                    if (c < cta) before += t[c];
                 }
+            }
         }
         unsigned x = all;
 #pragma unroll
@@ -216,14 +232,16 @@ __device__ __forceinline__ void sort_tokens(const SortArgs &s, unsigned *smem, i
         }
         if (lane == 31) warp_sums[warp] = x;
         __syncthreads();
-        unsigned base = 0;
-        for (int w = 0; w < warp; w++) base += warp_sums[w];
+        unsigned base = lane < warp ? warp_sums[lane] : 0u;
+#pragma unroll
+        for (int o = 16; o; o /= 2) base += __shfl_xor_sync(0xFFFFFFFFu, base, o);
         if (threadIdx.x < bins) start[threadIdx.x] = base + x - all + before;
         __syncthreads();
         for (unsigned i0 = lo; i0 < hi; i0 += 32 * kSortHeld) {
             if (!held) load(i0), match(i0);
 #pragma unroll
             for (int k = 0; k < kSortHeld; k++) {
+                if (i0 + 32 * k >= hi) break;
                 const unsigned d = digit(k), ahead = __popc(peers[k] & ((1u << lane) - 1));
                 const unsigned at = peers[k] ? count[d * kSortPitch + warp] : 0u;
                 __syncwarp();
@@ -244,48 +262,65 @@ __device__ __forceinline__ void sort_tokens(const SortArgs &s, unsigned *smem, i
     }
 }
 
-constexpr int kClearBytes = 16384;  // zeros in shared memory, the source of the bulk stores
+// The sort, one cluster.  After a clearing launch (`beside`) it runs beside it: that
+// launch lets it start once all work before it is done, and it ends only when the clearing
+// has, so that what follows finds both done.
+template <int DT>
+__global__ void __launch_bounds__(kSortThreads) embedding_sort_kernel(const __grid_constant__ SortArgs s, bool beside) {
+    extern __shared__ unsigned sort_smem[];
+    if (!beside) pdl_wait();
+    pdl_launch_dependents();
+    sort_tokens(s, sort_smem, blockIdx.x, gridDim.x);
+    if (beside) pdl_wait();
+}
 
-// CTAs 0 .. sorters - 1 (one cluster) sort; the others clear the table.
-template <int DT, bool VEC>
-__global__ void __launch_bounds__(kSortThreads) embedding_sort_kernel(const __grid_constant__ SortArgs s, int sorters) {
-    extern __shared__ __align__(128) unsigned sort_smem[];
-    const EmbedArgs &a = s.e;
-    if ((int)blockIdx.x < sorters) {
-        pdl_wait();
-        pdl_launch_dependents();
-        sort_tokens(s, sort_smem, blockIdx.x, sorters);
-        return;
-    }
-    const Chunks chunks(a.vocab, a.p);
-    const int clearers = gridDim.x - sorters, me = blockIdx.x - sorters;
-    if constexpr (VEC) {
-        // every warp's lane 0 has one bulk store a row in flight after the other
-        for (int i = threadIdx.x; i < kClearBytes / 16; i += kSortThreads) reinterpret_cast<uint4 *>(sort_smem)[i] = make_uint4(0, 0, 0, 0);
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncthreads();
-        pdl_wait();
-        pdl_launch_dependents();
-        if (threadIdx.x % 32 == 0) {
-            const uint32_t zeros = (uint32_t)__cvta_generic_to_shared(sort_smem);
-            const long long bytes = a.dim * ElemInfo<DT>::bytes;
-            for (long long v = (long long)me * kSortWarps + threadIdx.x / 32; v < a.vocab; v += (long long)clearers * kSortWarps) {
-                char *row = table_row(a, chunks, v, ElemInfo<DT>::bytes);
-                for (long long at = 0; at < bytes; at += kClearBytes)
-                    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(row + at), "r"(zeros),
-                                 "r"((uint32_t)(bytes - at < kClearBytes ? bytes - at : kClearBytes))
-                                 : "memory");
-                asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-            }
-            asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+constexpr int kClearBytes = 16384;  // zeros in shared memory, the source of the bulk stores
+// CTAs an SM: they leave room for the sort.  (Fewer warps to issue the stores clear more
+// slowly beside other work: 65536 x 4096 bf16 with the gradient of 8192 tokens 110 us,
+// with 4 x 128 threads 171, with 128 threads 333.)
+constexpr int kClearThreads = 512, kClearCtas = 2;
+
+// The warps clear the table: 16 KB of a piece at a time where its rows are
+// packed, else a row.  The 16-byte lines inside go by one bulk store, the elements before and
+// after them one by one.
+template <int DT>
+__global__ void __launch_bounds__(kClearThreads) embedding_clear_kernel(const __grid_constant__ EmbedArgs a) {
+    __shared__ __align__(128) unsigned zero_smem[kClearBytes / 4];
+    constexpr int EB = ElemInfo<DT>::bytes;
+    for (int i = threadIdx.x; i < kClearBytes / 16; i += kClearThreads) reinterpret_cast<uint4 *>(zero_smem)[i] = make_uint4(0, 0, 0, 0);
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncthreads();
+    pdl_wait();
+    pdl_launch_dependents();
+    const uint32_t zeros = (uint32_t)__cvta_generic_to_shared(zero_smem);
+    const int lane = threadIdx.x % 32;
+    const long long warps = (long long)gridDim.x * (kClearThreads / 32), me = (long long)blockIdx.x * (kClearThreads / 32) + threadIdx.x / 32;
+    auto clear = [&](char *from, long long bytes) {
+        for (long long at = 0; at < bytes; at += kClearBytes) {
+            const uintptr_t p0 = (uintptr_t)from + at, p1 = p0 + (bytes - at < kClearBytes ? bytes - at : kClearBytes);
+            const uintptr_t a0 = min((p0 + 15) & ~(uintptr_t)15, p1), a1 = max(p1 & ~(uintptr_t)15, a0);
+            if (lane == 0 && a1 > a0)
+                asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(a0), "r"(zeros), "r"((uint32_t)(a1 - a0)) : "memory");
+            if (lane < (int)(a0 - p0) / EB) store_elem<DT>(reinterpret_cast<char *>(p0), lane, 0u);
+            if (lane < (int)(p1 - a1) / EB) store_elem<DT>(reinterpret_cast<char *>(a1), lane, 0u);
+        }
+    };
+    if (a.table_stride == a.dim) {
+        const long long base = a.vocab / a.p, extra = a.vocab % a.p, row = a.dim * EB;
+        const long long per_big = ((base + 1) * row + kClearBytes - 1) / kClearBytes, per_small = (base * row + kClearBytes - 1) / kClearBytes;
+        const long long big = extra * per_big, units = big + (a.p - extra) * per_small;
+        for (long long u = me; u < units; u += warps) {
+            const long long r = u < big ? u / per_big : extra + (u - big) / per_small, k = u < big ? u % per_big : (u - big) % per_small;
+            const long long left = (base + (r < extra ? 1 : 0)) * row - k * kClearBytes;
+            clear(rank_ptr(a.pieces, a.p, (int)r) + k * kClearBytes, left < kClearBytes ? left : kClearBytes);
         }
     } else {
-        pdl_wait();
-        pdl_launch_dependents();
-        for (long long v = me; v < a.vocab; v += clearers) {
-            char *row = table_row(a, chunks, v, ElemInfo<DT>::bytes);
-            for (long long j = threadIdx.x; j < a.dim; j += kSortThreads) store_f<DT>(row, j, 0.0f);
-        }
+        const Chunks chunks(a.vocab, a.p);
+        for (long long v = me; v < a.vocab; v += warps) clear(table_row(a, chunks, v, EB), a.dim * EB);
+    }
+    if (lane == 0) {
+        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
 }
 
@@ -421,11 +456,14 @@ __global__ void __launch_bounds__(kReduceThreads, 3) embedding_runs_kernel(const
     }
 }
 
-// A run that begins in chunk blockIdx.x and goes on beyond it.
+// A run that begins in chunk blockIdx.x and goes on beyond it.  `width` threads
+// have the columns; the CTA's kReduceThreads / width groups of them take the run's
+// chunks in turn, and their sums are added in order.
 template <int DT, bool VEC, bool ADD>
-__global__ void __launch_bounds__(kReduceThreads) embedding_join_kernel(const __grid_constant__ SortArgs s) {
+__global__ void __launch_bounds__(kReduceThreads, 4) embedding_join_kernel(const __grid_constant__ SortArgs s, int width) {
     using Cols = GradCols<DT, VEC>;
     constexpr int N = Cols::N;
+    __shared__ float sums[N][kReduceThreads];
     const EmbedArgs &a = s.e;
     pdl_wait();
     pdl_launch_dependents();
@@ -438,29 +476,38 @@ __global__ void __launch_bounds__(kReduceThreads) embedding_join_kernel(const __
     if (key == (unsigned)a.vocab || next != key || before == key) return;
     // the chunk that it ends in: the chunks after c0 that begin with its key
     int last = c0;
-    for (int c = c0 + 1;; c += blockDim.x) {
+    for (int c = c0 + 1;; c += kReduceThreads) {
         const int mine = c + (int)threadIdx.x;
         const int more = __syncthreads_count(mine < s.n_chunks && items[(long long)mine * s.chunk].x == key);
         last += more;
-        if (more < (int)blockDim.x) break;
+        if (more < kReduceThreads) break;
     }
-    const Cols cols{a.dim, (long long)blockIdx.y * blockDim.x * N, (int)threadIdx.x, (int)blockDim.x};
+    const int group = threadIdx.x / width, groups = kReduceThreads / width;
+    const Cols cols{a.dim, (long long)blockIdx.y * width * N, (int)threadIdx.x % width, width};
     char *row = table_row(a, Chunks(a.vocab, a.p), key, ElemInfo<DT>::bytes);
-    const typename Cols::Bits old = cols.load(row, ADD);
-    float sum[N];
-    cols.load_part(s.part + ((long long)c0 * 2 + 1) * a.dim, sum);
-    constexpr int kAhead = 8;  // chunks whose loads are in flight together
+    const typename Cols::Bits old = cols.load(row, ADD && group == 0);
+    float sum[N] = {};
+    // part 1 of the first chunk, part 0 of the others
+    auto part_of = [&](int c) { return s.part + ((long long)c * 2 + (c == c0 ? 1 : 0)) * a.dim; };
+    constexpr int kAhead = 4;  // chunks whose loads are in flight together
 #pragma unroll 1
-    for (int c = c0 + 1; c <= last; c += kAhead) {
+    for (int c = c0 + group; c <= last; c += kAhead * groups) {
         float f[kAhead][N];
 #pragma unroll
-        for (int u = 0; u < kAhead; u++) cols.load_part(s.part + (long long)min(c + u, last) * 2 * a.dim, f[u]);
+        for (int u = 0; u < kAhead; u++) cols.load_part(part_of(min(c + u * groups, last)), f[u]);
 #pragma unroll
         for (int u = 0; u < kAhead; u++)
-            if (c + u <= last)
+            if (c + u * groups <= last)
 #pragma unroll
                 for (int e = 0; e < N; e++) sum[e] += f[u][e];
     }
+#pragma unroll
+    for (int e = 0; e < N; e++) sums[e][threadIdx.x] = sum[e];
+    __syncthreads();
+    if (group) return;
+    for (int w = 1; w < groups; w++)
+#pragma unroll
+        for (int e = 0; e < N; e++) sum[e] += sums[e][w * width + threadIdx.x];
     cols.finish(row, sum, a.scale, ADD, old);
 }
 
@@ -536,8 +583,9 @@ int embedding(rar_ctx *h, const rar_embedding_args *a, cudaStream_t stream) {
 
 size_t grad_plan(void *base, size_t n_tokens, size_t vocab, size_t dim, SortArgs *s) {
     WorkspacePlan w(base);
-    // at most 4096 chunks, so that their sums stay small against dout
-    const size_t chunk = std::max<size_t>(kMinChunk, (n_tokens + 4095) / 4096), n = (n_tokens + chunk - 1) / chunk;
+    // chunks of 16 to 64 places while that makes about 1024 of them, and never
+    // more than 4096, so that their sums stay small against dout
+    const size_t chunk = std::max({(size_t)kMinChunk, std::min<size_t>(64, n_tokens / 1024), (n_tokens + 4095) / 4096}), n = (n_tokens + chunk - 1) / chunk;
     s->chunk = (int)chunk;
     s->n_chunks = (int)n;
     s->items[0] = w.take<uint2>(n_tokens);
@@ -549,13 +597,13 @@ size_t grad_plan(void *base, size_t n_tokens, size_t vocab, size_t dim, SortArgs
     return w.used;
 }
 
-// The launch of the sorting cluster and the clearing CTAs.
+// The launch of the sorting cluster.
 template <typename... Params, typename... Args>
-cudaError_t launch_clusters(void (*kern)(Params...), unsigned grid, unsigned cluster, cudaStream_t stream, Args &&...args) {
+cudaError_t launch_sort(void (*kern)(Params...), unsigned cluster, cudaStream_t stream, Args &&...args) {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSortSmem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
+    cfg.gridDim = dim3(cluster);
     cfg.blockDim = dim3(kSortThreads);
     cfg.dynamicSmemBytes = kSortSmem;
     cfg.stream = stream;
@@ -619,27 +667,28 @@ int embedding_grad(rar_ctx *h, const rar_embedding_grad_args *a, cudaStream_t st
     const size_t ve = 16 / e;
     bool vec = a->dim % ve == 0 && vec16(a->dout, a->n_tokens, k.row_stride, e);
     for (int r = 0; r < a->p && vec; r++) vec = vec16(a->dtables[r], a->vocab / a->p + 1, k.table_stride, e);
-    const unsigned sorters = a->n_tokens == 0 ? 0 : a->n_tokens <= (size_t)kSortOneCta ? 1 : kSortCluster;
-    const unsigned cluster = std::max(sorters, 1u);
-    // the clearing CTAs: as many as are resident (2 an SM), in whole clusters
-    unsigned clear = 0;
-    if (!a->accumulate) clear = (unsigned)std::min<size_t>(a->vocab, (size_t)h->sm_count * 2 - cluster) / cluster * cluster;
-    if (!a->accumulate && clear == 0) clear = cluster;
+    const unsigned sorters = a->n_tokens <= (size_t)kSortOneCta ? 1 : kSortCluster;
     cudaError_t ce = dispatch_float(a->dtype, [&](auto dt) {
         constexpr int DT = decltype(dt)::value;
         auto steps = [&](auto vv) {
             constexpr bool VEC = decltype(vv)::value != 0;
-            cudaError_t e1 = launch_clusters(embedding_sort_kernel<DT, VEC>, sorters + clear, cluster, stream, sort, (int)sorters);
-            if (e1 != cudaSuccess || sorters == 0) return e1;
+            cudaError_t e1 = cudaSuccess;
+            if (!a->accumulate)
+                e1 = launch_pdl(embedding_clear_kernel<DT>, dim3((unsigned)(h->sm_count * kClearCtas)), dim3(kClearThreads), 0, stream, k);
+            if (e1 != cudaSuccess || a->n_tokens == 0) return e1;
+            e1 = launch_sort(embedding_sort_kernel<DT>, sorters, stream, sort, !a->accumulate);
+            if (e1 != cudaSuccess) return e1;
             constexpr int N = GradCols<DT, VEC>::N;
             // no more threads than the row has columns for
             const int threads = (int)std::min<size_t>(((a->dim + N - 1) / N + 31) / 32 * 32, kReduceThreads);
             const dim3 grid((unsigned)sort.n_chunks, (unsigned)((a->dim + threads * N - 1) / (threads * N)));
             e1 = launch_pdl(a->accumulate ? embedding_runs_kernel<DT, VEC, true> : embedding_runs_kernel<DT, VEC, false>, grid, dim3((unsigned)threads),
                             0, stream, sort);
+            const int width = threads >= 128 ? 128 : threads >= 64 ? 64 : 32;  // divides the CTA
+            const dim3 joins((unsigned)sort.n_chunks, (unsigned)((a->dim + width * N - 1) / (width * N)));
             if (e1 == cudaSuccess && sort.n_chunks > 1)
-                e1 = launch_pdl(a->accumulate ? embedding_join_kernel<DT, VEC, true> : embedding_join_kernel<DT, VEC, false>, grid,
-                                dim3((unsigned)threads), 0, stream, sort);
+                e1 = launch_pdl(a->accumulate ? embedding_join_kernel<DT, VEC, true> : embedding_join_kernel<DT, VEC, false>, joins,
+                                dim3(kReduceThreads), 0, stream, sort, width);
             return e1;
         };
         return vec ? steps(IntC<1>{}) : steps(IntC<0>{});

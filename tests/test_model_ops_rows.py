@@ -109,3 +109,26 @@ def test_status_and_send_counts(h):  # noqa: F811
     parts = [normal(g, 2500, 1024) for _ in range(2)]
     h.add_rmsnorm(parts)
     assert h.status() == 0 and h.send_counts(2) == [0, 0]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("lengths,dim", [
+    ([1, 15, 16, 17, 31, 32, 33, 1, 47, 48, 49, 64], 72), ([16] * 9, 264), ([32, 16, 48], 24), ([5, 27, 32], 8),
+    ([16, 1, 15, 300, 1, 2, 3], 1025), ([31, 1], 64), ([40, 8], 520), ([3000], 2056),
+])
+def test_runs_against_the_chunks(h, dtype, accumulate, lengths, dim):  # noqa: F811
+    """Runs of equal tokens that begin and end anywhere in the chunks of 16,
+    cover chunks, and end with the last token."""
+    from tests.test_model_ops import check_embedding_grad, pieces
+    g = gen(sum(lengths) + dim)
+    for left_out in (0, 7):
+        tok = torch.cat([torch.full((n,), 3 * k + 1, device="cuda") for k, n in enumerate(lengths)]
+                        + [torch.full((left_out,), -5, device="cuda")])
+        tok = tok[torch.randperm(len(tok), generator=g, device="cuda")]
+        vocab = 3 * len(lengths) + 2
+        dout = normal(g, len(tok), dim, dtype=dtype)
+        old = normal(g, vocab, dim, dtype=dtype)
+        into = old.clone()
+        h.embedding_grad(dout, tok, pieces(into, 3), scale=0.5, accumulate=accumulate)
+        check_embedding_grad(into, dout, tok, old if accumulate else None, vocab, 0.5)
