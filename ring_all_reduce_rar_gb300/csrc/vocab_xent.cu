@@ -18,7 +18,9 @@
 // size that rounding dhidden and dweights has anyway.
 //
 // Bound by the tensor cores for many tokens (8 tokens x vocab x dim
-// operations against 6 if the logits were kept), by memory for few.
+// operations against 6 if the logits were kept): 8192 tokens by 65536 x 4096 bf16 run at 1.73
+// PFLOP/s forward and take 11.0 ms with gradients (1.6).  By memory and latency
+// for few: 16 by 32768 x 2048 40 us (134 MB of weights, 3.4 TB/s).
 #include <algorithm>
 
 #include "op_host.h"
@@ -100,10 +102,10 @@ __device__ __forceinline__ int g_exponent(const XentArgs &a) {
     return e > 120 ? 120 : e < -120 ? -120 : e;
 }
 
-enum XentMode { XENT_STATS, XENT_G, XENT_DHIDDEN, XENT_DWEIGHT };
+enum XentMode { XENT_STATS, XENT_G, XENT_DHIDDEN, XENT_DWEIGHT, XENT_STATS_SUMS };  // (the last: see kStepsPerSum)
 template <int MODE>
 struct Mode {
-    static constexpr bool logits = MODE == XENT_STATS || MODE == XENT_G;
+    static constexpr bool sums = MODE == XENT_STATS_SUMS, stats = MODE == XENT_STATS || sums, logits = stats || MODE == XENT_G;
     // whether a row of the operand is a row of K (MN-major); rows of a box; boxes of a stage
     static constexpr bool a_mn = MODE == XENT_DWEIGHT, b_mn = MODE == XENT_DHIDDEN || MODE == XENT_DWEIGHT;
     static constexpr int a_box = a_mn ? 64 : 128, b_box = b_mn ? 64 : 128;
@@ -195,6 +197,15 @@ __device__ __forceinline__ uint4 narrow8_scaled(const float *v, float scale) {
     return narrow8<DT>(f);
 }
 
+// The tensor cores add to a 32-bit accumulator by truncation: over the whole of dim the
+// logits, and with them lse, came out low by some 1e-6 of their size (dim 2048; a rounding
+// sum: 4e-7).  So XENT_STATS_SUMS, for a dim above that of one sum, ends its accumulators every 16
+// steps (1024 of dim) and adds them up in registers: 5e-7.  It costs 8 to 10 % of a long forward
+// pass (2048 tokens by 50021 x 2048 fp16 314 us against 282, 8192 by 65536 x 4096 bf16 2.54 ms
+// against 2.33), 3 % with gradients.  A dim of one sum keeps the plain form and its
+// time.  Products whose results are rounded to 16 bits do without.
+constexpr int kStepsPerSum = 16;
+
 // What an epilogue thread keeps of a tile: one row of it.
 struct XentRow {
     int row;          // of tokens (or of the block, XENT_DWEIGHT)
@@ -246,7 +257,7 @@ template <int MODE, int DT>
 __device__ __forceinline__ void xent_columns(const XentArgs &a, XentRow &r, int c0, float undo, bool first, bool direct, float (&v)[32]) {
     if (!r.live) return;
     const int cols = r.cols - c0;
-    if constexpr (MODE == XENT_STATS) {
+    if constexpr (Mode<MODE>::stats) {
         if (cols <= 0) return;
         if (cols < 32) {
 #pragma unroll
@@ -323,8 +334,10 @@ __device__ __forceinline__ void add_exp(float &m, float &s, float om, float os) 
 // 8: loads, 9 (of the pair's first CTA): products.  The epilogue reads its half
 // row 32 columns at a time: the code of all 128 at once is four times as long, and
 // its instruction fetches showed in calls of a few tiles.
+// At most 152 registers: three warps of this kernel then leave each quarter of an SM
+// room for a warp of 32, so that a CTA of the join can wait there for the end.
 template <int MODE, int DT>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __maxnreg__(152)
     xent_tile_kernel(const __grid_constant__ XentArgs a, const __grid_constant__ XentMaps maps, int b0, int nb) {
     extern __shared__ unsigned char dyn[];
     __shared__ TcShared sh;
@@ -335,7 +348,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
     tc_begin(&sh);
     pdl_wait();
     pdl_launch_dependents();
-    if (MODE == XENT_STATS && blockIdx.x == 0 && threadIdx.x == 0) *a.w_max = 0u;
+    if (Mode<MODE>::stats && blockIdx.x == 0 && threadIdx.x == 0) *a.w_max = 0u;
     const int items = xent_items<MODE>(a, nb), pairs = gridDim.x / 2, first = blockIdx.x / 2;
     constexpr bool a_mn = Mode<MODE>::a_mn, b_mn = Mode<MODE>::b_mn;
     constexpr int kABoxes = Mode<MODE>::a_boxes, kLoaders = kABoxes + Mode<MODE>::b_boxes;
@@ -345,12 +358,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
         const bool is_a = lane < kABoxes;
         const int part = is_a ? lane * Mode<MODE>::a_box : (lane - kABoxes) * Mode<MODE>::b_box;  // rows (columns) into the operand
         unsigned step = 0;
+        uint32_t st = 0, phase = 0;
         for (int i = first; i < items && !__any_sync(kLanes, *(volatile int *)&sh.failed); i += pairs) {
             const XentItem it = xent_item<MODE>(a, b0, nb, i);
             xent_steps<MODE>(a, b0, it, [&](int s, int k, const BlockOf &b) {
-                const int st = (int)(step % kTcStages);
-                const bool ok = step < kTcStages || tc_wait(&sh, a.limits, &sh.empty[st], (step / kTcStages - 1) & 1, 0);
-                if (!__all_sync(kLanes, ok)) return false;
+                // (a new barrier's preceding phase counts as complete: the first turn does not wait)
+                if (!__all_sync(kLanes, tc_wait(&sh, a.limits, &sh.empty[st], phase ^ 1, 0))) return false;
                 // a CTA whose rows of A all lie past the last loads none of them: its
                 // rows of the accumulator are never read
                 auto a_rows = [&](int r) { return MODE == XENT_DWEIGHT || it.row + r * 128 < a.tokens; };
@@ -366,6 +379,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
                 else x = s * 64, y = is_a ? row : b.row + col;
                 if (!is_a || a_rows((int)rank)) tc_load_box(map, to, bar, x, y);
                 step++;
+                if (++st == kTcStages) st = 0, phase ^= 1;
                 return true;
             });
         }
@@ -378,56 +392,105 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
         }
     } else if (warp == kTcEpilogueWarps + 1 && lane == 0 && rank == 0) {
         const uint64_t operand_a = tc_operand(stages, a_mn ? 8192 : 16, 1024), operand_b = tc_operand(stages + 16384, b_mn ? 8192 : 16, 1024);
-        unsigned step = 0, tile = 0;
-        for (int i = first; i < items; i += pairs, tile++) {
+        // the next stage and its phase; accumulators begun.  (This thread issues a step of 64
+        // every 512 cycles or so: what it computes between two steps is time lost.)
+        uint32_t st = 0, phase = 0, sums = 0;
+        for (int i = first; i < items; i += pairs) {
             const XentItem it = xent_item<MODE>(a, b0, nb, i);
-            const int acc = (int)(tile & 1);
-            if (tile >= 2 && !tc_wait(&sh, a.limits, &sh.acc_empty[acc], (tile / 2 - 1) & 1, 2)) break;
-            tc_fence_after();
-            const uint32_t d = sh.tmem + acc * kTile, idesc = tc_instruction(DT == DT_BF16, a_mn, b_mn, (uint32_t)it.n);
+            const uint32_t idesc = tc_instruction(DT == DT_BF16, a_mn, b_mn, (uint32_t)it.n);
+            uint32_t d = 0;
+            int left = 0;  // steps that the present accumulator takes yet
             bool more = false;
             const bool ok = xent_steps<MODE>(a, b0, it, [&](int, int, const BlockOf &) {
-                const int st = (int)(step % kTcStages);
-                if (!tc_wait(&sh, a.limits, &sh.full[st], (step / kTcStages) & 1, 3)) return false;
+                if (left == 0) {
+                    if (more) tc_commit(&sh.acc_full[(sums - 1) & 1]);
+                    if (sums >= 2 && !tc_wait(&sh, a.limits, &sh.acc_empty[sums & 1], (sums / 2 - 1) & 1, 2)) return false;
+                    tc_fence_after();
+                    d = sh.tmem + (sums & 1) * kTile;
+                    sums++;
+                    left = Mode<MODE>::sums ? kStepsPerSum : 0x7FFFFFFF;
+                    more = false;
+                }
+                if (!tc_wait(&sh, a.limits, &sh.full[st], phase, 3)) return false;
                 tc_fence_after();
                 // descriptors count addresses in units of 16 bytes
-                const uint64_t da = operand_a + (uint32_t)(st * kTcStageBytes / 16), db = operand_b + (uint32_t)(st * kTcStageBytes / 16);
+                const uint64_t da = operand_a + st * (kTcStageBytes / 16), db = operand_b + st * (kTcStageBytes / 16);
 #pragma unroll
                 for (int k = 0; k < 4; k++) {
                     tc_mma(d, da + k * (a_mn ? 128 : 2), db + k * (b_mn ? 128 : 2), idesc, more);
                     more = true;
                 }
                 tc_commit(&sh.empty[st]);
-                step++;
+                if (++st == kTcStages) st = 0, phase ^= 1;
+                left--;
                 return true;
             });
             if (!ok) break;
-            tc_commit(&sh.acc_full[acc]);
+            tc_commit(&sh.acc_full[(sums - 1) & 1]);
         }
     } else if (warp < kTcEpilogueWarps) {
         const int quarter = warp % 4;
         const float undo = MODE == XENT_DHIDDEN || MODE == XENT_DWEIGHT ? ldexpf(1.0f, -g_exponent<DT>(a)) : 1.0f;
         const bool first_window = b0 == 0, direct = a.direct && b0 + nb == a.n_blocks;
-        unsigned tile = 0;
-        for (int i = first; i < items; i += pairs, tile++) {
-            const XentItem it = xent_item<MODE>(a, b0, nb, i);
-            const int acc = (int)(tile & 1), half = warp / 4 * 128, row = it.row + (int)rank * 128 + quarter * 32 + lane;
-            XentRow r = xent_row<MODE, DT>(a, b0, it, row, half);
-            if (!tc_wait(&sh, a.limits, &sh.acc_full[acc], (tile / 2) & 1, 4)) break;
-            __syncwarp();
+        unsigned sums = 0;  // accumulators read
+        auto ready = [&] {
+            const bool ok = __all_sync(0xFFFFFFFFu, tc_wait(&sh, a.limits, &sh.acc_full[sums & 1], (sums / 2) & 1, 4));
             tc_fence_after();
-            const uint32_t at = sh.tmem + ((uint32_t)quarter << 21) + acc * kTile + half;
+            return ok;
+        };
+        auto release = [&] {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) tc_arrive_cluster(peer_addr(smem_u32(&sh.acc_empty[sums & 1]), 0));
+            sums++;
+        };
+        bool ok = true;
+        for (int i = first; i < items; i += pairs) {
+            const XentItem it = xent_item<MODE>(a, b0, nb, i);
+            const int half = warp / 4 * 128, row = it.row + (int)rank * 128 + quarter * 32 + lane;
+            XentRow r = xent_row<MODE, DT>(a, b0, it, row, half);
+            auto at = [&](int c) { return sh.tmem + ((uint32_t)quarter << 21) + (sums & 1) * kTile + half + c; };
+            if (Mode<MODE>::sums) {
+                // all sums but the last into registers, and these onto the last
+                float z[128];
+#pragma unroll
+                for (int c = 0; c < 128; c++) z[c] = 0.0f;
+#pragma unroll 1
+                for (int k = kStepsPerSum; k < it.k1; k += kStepsPerSum) {
+                    if (!(ok = ready())) break;
+#pragma unroll
+                    for (int q = 0; q < 128; q += 8) {
+                        float v[8];
+                        tc_read8(at(q), v);
+                        tc_read_wait();
+#pragma unroll
+                        for (int c = 0; c < 8; c++) z[q + c] += v[c];
+                    }
+                    release();
+                }
+                if (!ok || !(ok = ready())) break;
+#pragma unroll
+                for (int q = 0; q < 128; q += 8) {
+                    float v[8];
+                    tc_read8(at(q), v);
+                    tc_read_wait();
+#pragma unroll
+                    for (int c = 0; c < 8; c++) v[c] += z[q + c];
+                    tc_write8(at(q), v);
+                }
+                tc_write_wait();
+            } else if (!(ok = ready())) {
+                break;
+            }
 #pragma unroll 1
             for (int c0 = 0; c0 < 128; c0 += 32) {
                 float v[32];
-                tc_read32(at + c0, v);
+                tc_read32(at(c0), v);
                 tc_read_wait();
                 xent_columns<MODE, DT>(a, r, c0, undo, first_window, direct, v);
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) tc_arrive_cluster(peer_addr(smem_u32(&sh.acc_empty[acc]), 0));
-            if constexpr (MODE == XENT_STATS)
+            release();
+            if constexpr (Mode<MODE>::stats)
                 if (r.live) a.stats[(2ll * (b0 + it.block) + half / 128) * a.tokens + row] = make_float2(r.max, r.sum);
         }
     }
@@ -435,16 +498,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
     tc_end(&sh);
 }
 
-// Joins the blocks of 8 tokens, a warp a token, to lse and loss; with gradients also their
+// Joins the blocks of some tokens, a warp a token, to lse and loss; with gradients also their
 // weights and hidden states, cleared where a token is left out (0 x NaN is not 0
-// in dweights' sum).
+// in dweights' sum).  Without gradients a CTA is small enough to stand beside one of
+// the tile kernel and wait there for its end: 256 tokens by 32768 x 2048 took 37 us
+// so and 48 us with 8 tokens a CTA; with gradients 8 tokens, whose loads are in flight
+// together, took 262 us of a whole call against 281 (1024 by 32000 x 1024).
+template <bool GRAD>
+constexpr int kJoinTokens = GRAD ? 8 : 4;
 template <int DT, bool GRAD>
-__global__ void __launch_bounds__(256) xent_join_kernel(const __grid_constant__ XentArgs a) {
-    __shared__ int counts[8];
+__global__ void __launch_bounds__(32 * kJoinTokens<GRAD>, GRAD ? 1 : 16) xent_join_kernel(const __grid_constant__ XentArgs a) {
+    constexpr int kTokens = kJoinTokens<GRAD>;
+    __shared__ int counts[kTokens];
     pdl_wait();
     pdl_launch_dependents();
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, n = 2 * a.n_blocks;
-    const long long t0 = (long long)blockIdx.x * 8, t = t0 + warp;
+    const long long t0 = (long long)blockIdx.x * kTokens, t = t0 + warp;
     float m = -INFINITY, s = 0.0f;
     if (t < a.tokens) {
         const long long y = load_index(a.targets, a.index_bytes, t);
@@ -480,17 +549,17 @@ __global__ void __launch_bounds__(256) xent_join_kernel(const __grid_constant__ 
     }
     if (!GRAD) return;
     __syncthreads();
-    const int vecs = (int)(a.dim / 8), total = vecs * (int)(a.tokens - t0 < 8 ? a.tokens - t0 : 8);
-    for (int i0 = threadIdx.x; i0 < total; i0 += 4 * 256) {
+    const int vecs = (int)(a.dim / 8), total = vecs * (int)(a.tokens - t0 < kTokens ? a.tokens - t0 : kTokens);
+    for (int i0 = threadIdx.x; i0 < total; i0 += 4 * 32 * kTokens) {
         uint4 q[4];  // loads in flight together
 #pragma unroll
         for (int u = 0; u < 4; u++) {
-            const int i = min(i0 + u * 256, total - 1), k = i / vecs;
+            const int i = min(i0 + u * 32 * kTokens, total - 1), k = i / vecs;
             q[u] = *(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.hidden) + (t0 + k) * a.hidden_stride) + (i - k * vecs));
         }
 #pragma unroll
         for (int u = 0; u < 4; u++) {
-            const int i = i0 + u * 256, k = i / vecs;
+            const int i = i0 + u * 32 * kTokens, k = i / vecs;
             if (i < total)
                 *(reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.hidden_used) + (t0 + k) * a.dim) + (i - k * vecs)) =
                     counts[k] ? q[u] : make_uint4(0, 0, 0, 0);
@@ -710,10 +779,11 @@ int vocab_xent(rar_ctx *h, const rar_vocab_xent_args *a, cudaStream_t stream) {
             }
             return e;
         }
-        e = launch_tiles<XENT_STATS, DT>(h, k, logits, 0, k.n_blocks, stream);
+        e = k.dim > 64 * kStepsPerSum ? launch_tiles<XENT_STATS_SUMS, DT>(h, k, logits, 0, k.n_blocks, stream)
+                                      : launch_tiles<XENT_STATS, DT>(h, k, logits, 0, k.n_blocks, stream);
+        const int join = grad ? kJoinTokens<true> : kJoinTokens<false>;
         if (e == cudaSuccess)
-            e = launch_pdl(grad ? xent_join_kernel<DT, true> : xent_join_kernel<DT, false>, dim3((unsigned)((k.tokens + 7) / 8)),
-                           dim3(256), 0, stream, k);
+            e = launch_pdl(grad ? xent_join_kernel<DT, true> : xent_join_kernel<DT, false>, dim3((unsigned)((k.tokens + join - 1) / join)), dim3(32 * join), 0, stream, k);
         if (!grad) return e;
         for (int b0 = 0; b0 < k.n_blocks && e == cudaSuccess; b0 += k.window) {
             const int nb = std::min(k.window, k.n_blocks - b0);
