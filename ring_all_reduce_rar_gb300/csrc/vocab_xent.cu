@@ -102,6 +102,20 @@ __device__ __forceinline__ int g_exponent(const XentArgs &a) {
     return e > 120 ? 120 : e < -120 ? -120 : e;
 }
 
+// G is also divided by the largest weight's significand, in [1, 2).  Where all tokens weigh
+// the same (a mean), (softmax - 1) weight, the largest entry of a row, else
+// rounds in the same direction for every unforeseen target, by up to half a unit in
+// the last place: as much as the gradients' own rounding, and the same for all.
+__device__ __forceinline__ float g_unit(const XentArgs &a) {
+    const float m = __uint_as_float(*a.w_max);
+    return m > 0.0f ? ldexpf(m, -ilogbf(m)) : 1.0f;
+}
+// What undoes both.
+template <int DT>
+__device__ __forceinline__ float g_undo(const XentArgs &a) {
+    return ldexpf(g_unit(a), -g_exponent<DT>(a));
+}
+
 enum XentMode { XENT_STATS, XENT_G, XENT_DHIDDEN, XENT_DWEIGHT, XENT_STATS_SUMS };  // (the last: see kStepsPerSum)
 template <int MODE>
 struct Mode {
@@ -244,7 +258,7 @@ __device__ __forceinline__ XentRow xent_row(const XentArgs &a, int b0, const Xen
         r.max = -INFINITY;
         r.sum = 0.0f;
         if constexpr (MODE == XENT_G) {
-            r.w = r.live ? ldexpf(a.row_weight[row], g_exponent<DT>(a)) : 0.0f;
+            r.w = r.live ? ldexpf(a.row_weight[row] / g_unit(a), g_exponent<DT>(a)) : 0.0f;
             r.lse = r.live ? a.lse_ws[row] : 0.0f;
             r.out = static_cast<char *>(a.g) + (((long long)row * a.window + it.block) * kBlock + half) * 2;
         }
@@ -430,7 +444,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(152)
         }
     } else if (warp < kTcEpilogueWarps) {
         const int quarter = warp % 4;
-        const float undo = MODE == XENT_DHIDDEN || MODE == XENT_DWEIGHT ? ldexpf(1.0f, -g_exponent<DT>(a)) : 1.0f;
+        const float undo = MODE == XENT_DHIDDEN || MODE == XENT_DWEIGHT ? g_undo<DT>(a) : 1.0f;
         const bool first_window = b0 == 0, direct = a.direct && b0 + nb == a.n_blocks;
         unsigned sums = 0;  // accumulators read
         auto ready = [&] {
@@ -572,7 +586,7 @@ template <int DT>
 __global__ void __launch_bounds__(256) xent_dhidden_join_kernel(const __grid_constant__ XentArgs a) {
     pdl_wait();
     pdl_launch_dependents();
-    const float undo = ldexpf(1.0f, -g_exponent<DT>(a));
+    const float undo = g_undo<DT>(a);
     const long long vecs = a.dim / 8, n = a.tokens * vecs;
     for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (long long)gridDim.x * blockDim.x) {
         const long long t = n < 0x7FFFFFFF ? (long long)((uint32_t)i / (uint32_t)vecs) : i / vecs, d = (i - t * vecs) * 8;

@@ -837,3 +837,28 @@ def test_refusals(h):
     expect = h.add_rmsnorm([both[:, :64].clone()])
     assert lib.rar_add_rmsnorm(h.h, ctypes.byref(a), stream) == 0
     assert torch.equal(both[:, 64:], expect.out)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", HALF)
+def test_vocab_xent_equal_weights_round_once(h, dtype):
+    """Tokens that weigh the same, a weight halfway between two values of the type: a target's
+    row of dweights is off by its own rounding alone.  With p the softmax (logits of a
+    spread of 0.04, so p is below 1.5 / 16384), p - 1 is rounded by p at most, and the
+    four other tokens' entries of that row, p each, by u p."""
+    g = gen(77)
+    vocab, dim, tokens = 16384, 64, 5
+    u = U[dtype]
+    weights = normal(g, vocab, dim, dtype=dtype, std=0.005)
+    hidden = normal(g, tokens, dim, dtype=dtype)
+    targets = torch.tensor([3, 777, 5000, 9001, 16000], device="cuda")
+    w = torch.full((tokens,), 1.0 + u, device="cuda")
+    r = h.vocab_xent(hidden, pieces(weights, 3), targets, token_weight=w, grad=True)
+    logits = hidden.double() @ weights.double().t()
+    gm = torch.softmax(logits, 1)
+    gm[torch.arange(tokens), targets] -= 1.0
+    ref = ((gm * w.double()[:, None]).t() @ hidden.double())[targets]
+    size = hidden.double().abs()
+    assert float(torch.softmax(logits, 1).max()) < 1.5 / vocab
+    tol = u * ref.abs() + 1.5 / vocab * (1 + u) * (size + 4 * u * size.max()) * (1 + u) + TINY[dtype]
+    within(torch.cat(r.dweights)[targets], ref, tol, "dweights")
