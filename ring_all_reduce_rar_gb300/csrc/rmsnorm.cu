@@ -5,7 +5,8 @@
 //   rstd = 1 / sqrt(mean(s^2) + eps),  y = s rstd weight
 //
 // Bound by memory: (p + 1) reads and 2 writes an element against p + 6
-// operations.
+// operations.  Few rows are bound by latency: 4 rows of 2048 with 8 parts and 8-bit output
+// take 6 us, and 10.6 a call in a stream of calls, which is the host's time for one.
 #include "rmsnorm.cuh"
 
 namespace rar {
@@ -175,7 +176,9 @@ __device__ __forceinline__ void fold_vector(const NormArgs &a, const Chunks &chu
 // `warps` warps hold a row in registers, V vectors a thread (vector v of a
 // thread: tid + v n), in 32 bits.  Every input is read once, and before anything is
 // written (in-place outputs).  ODD: rows that begin anywhere in a 16-byte vector, at
-// the same place in all matrices.
+// the same place in all matrices.  One CTA a row and many of them: 8 x 4096 x 4096 bf16 with
+// 8-bit output took 76 us (4.6 TB/s) here, the ramp of each CTA's loads exposed; it
+// stays for rows too few for the ring to turn, too long for it or not of whole vectors.
 template <int DT, int V, int QUANT, bool ODD>
 __global__ void __launch_bounds__(kNormMaxThreads, V == 1 ? 2 : 1) add_rmsnorm_kernel(const __grid_constant__ NormArgs a) {
     constexpr int VE = RowBits<DT>::VE;
@@ -226,6 +229,8 @@ __global__ void __launch_bounds__(kNormMaxThreads, V == 1 ? 2 : 1) add_rmsnorm_k
 // row's reduction is a chain of waits, and a second row in the works fills them
 // (the ring alone holds too few rows for two CTAs an SM when p is 8).  Up to 256 threads a row:
 // what a thread does once a row is then shared by two vectors or more.
+// 8 x 4096 x 4096 bf16 with 8-bit output: 59 us, 5.9 TB/s of the 6.7 that a copy reaches
+// (68 us with one row in the works).
 template <int DT, int V, int QUANT>
 __global__ void __launch_bounds__(2 * kRingRowThreads + 32, 1) add_rmsnorm_ring_kernel(const __grid_constant__ NormArgs a) {
     constexpr int VE = RowBits<DT>::VE;
@@ -334,7 +339,8 @@ __global__ void __launch_bounds__(2 * kRingRowThreads + 32, 1) add_rmsnorm_ring_
 
 // Any other row (matrices whose rows begin at different places in a vector, rows too
 // long for the registers):
-// s in shared memory in 32 bits, single elements, a CTA a row.
+// s in shared memory in 32 bits, single elements, a CTA a row: 8 x 4096 x 4096 bf16 takes
+// 391 us.
 template <int DT>
 __global__ void __launch_bounds__(kNormMaxThreads) add_rmsnorm_any_kernel(const __grid_constant__ NormArgs a) {
     extern __shared__ float row[];  // [dim], then [n_groups] maxima

@@ -80,6 +80,9 @@ __device__ __forceinline__ void grad_part(const NormGradArgs &a, const RowView<D
 // the CTA's part of dweight, a fixed set of columns a thread.  ODD: rows that begin
 // anywhere in a 16-byte vector; n_partial is a multiple of a vector's elements
 // (or every CTA has one row), so that all of a CTA's rows begin at the same place.
+// Bound by latency at few rows: 1027 x 1001 float32 takes 13 us with the sum of dweight's
+// parts; 8192 x 1001 40 us (against 129 by single elements).  8192 x 4096 bf16 took 63 us
+// here: a row's loads, reduction and stores follow one another.
 template <int DT, int V, bool ODD>
 __global__ void __launch_bounds__(kNormMaxThreads, V == 1 ? 2 : 1) rmsnorm_grad_kernel(const __grid_constant__ NormGradArgs a) {
     constexpr int VE = RowBits<DT>::VE;
@@ -117,7 +120,7 @@ __global__ void __launch_bounds__(kNormMaxThreads, V == 1 ? 2 : 1) rmsnorm_grad_
 }
 
 // The same for many rows, brought `stages` rows ahead by a warp of its own (see
-// add_rmsnorm_ring_kernel).  needs dx.
+// add_rmsnorm_ring_kernel).  needs dx.  8192 x 4096 bf16: 47 us with dweight's join, 5.7 TB/s.
 template <int DT, int V>
 __global__ void __launch_bounds__(kNormMaxThreads + 32, V == 1 ? 2 : 1) rmsnorm_grad_ring_kernel(const __grid_constant__ NormGradArgs a) {
     constexpr int VE = RowBits<DT>::VE;
@@ -232,7 +235,8 @@ __global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_grad_any_kernel(const
 }
 
 // dweight from the CTAs' parts: 32 columns a CTA, 16 slices of the parts added
-// side by side and then in order.
+// side by side and then in order (no atomics: the order is fixed).  6 to 8 us alone, for 608 parts
+// of 1001 and 304 of 4096 columns: latency; its start overlaps the row kernel.
 template <int DT>
 __global__ void __launch_bounds__(512) rmsnorm_dweight_kernel(const __grid_constant__ NormGradArgs a) {
     __shared__ float part[16][33];
