@@ -57,6 +57,8 @@ size_t matrix(const std::string &name, const Tensor &t, int64_t rows, int64_t co
         refuse(name + " must be a (" + std::to_string(rows) + ", " + std::to_string(cols) + ") " + c10::toString(c.dtype) + " tensor on " +
                c.device.str());
     if (cols > 1 && rows > 0 && t.stride(1) != 1) refuse(name + " must have contiguous rows");
+    // (a row that expand() repeats has stride 0, which in C stands for packed rows)
+    if (rows > 1 && t.stride(0) < cols) refuse("the rows of " + name + " must not overlap: an expanded matrix has to be copied first");
     return (size_t)(rows > 1 ? t.stride(0) : cols);
 }
 void *vec(const std::string &name, const Tensor &t, int64_t n, at::ScalarType type, const Common &c) {
