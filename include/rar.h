@@ -406,7 +406,8 @@ typedef struct {
     void *out8;               /* out: codes, one byte each, or NULL */
     size_t out8_stride;
     float *scales;            /* out: rows x ceil(dim / group), needed with out8 */
-    size_t group;             /* columns per scale; 0: the whole row; else a multiple of 32 */
+    size_t group;             /* columns per scale; 0: the whole row; else a multiple of 32
+                                 (one of dim or more: the whole row, too) */
 } rar_rmsnorm_args;
 
 #define RAR_NORM_MAX_DIM 32768

@@ -394,7 +394,8 @@ int add_rmsnorm(rar_ctx *h, const rar_rmsnorm_args *a, cudaStream_t stream) {
     if (!a->parts) return c.bad("parts is NULL");
     if (a->out8 && !a->scales) return c.bad("scales is NULL");
     const size_t e = (size_t)elem_bytes(a->dtype);
-    const size_t group = a->group ? a->group : a->dim, n_groups = (a->dim + group - 1) / group;
+    // (one longer than any row is the row's; the kernels count columns in 32 bits)
+    const size_t group = a->group ? std::min<size_t>(a->group, RAR_NORM_MAX_DIM) : a->dim, n_groups = (a->dim + group - 1) / group;
     MatrixSpan s;
     for (int r = 0; r < a->p; r++) {
         if ((rc = c.matrix("a part", a->parts[r], a->rows, a->dim, a->part_stride, e, e, &s)) != RAR_OK) return rc;

@@ -190,7 +190,7 @@ PyObject *add_rmsnorm(PyObject *, PyObject *const *args, Py_ssize_t nargs) {
         }
         if (group >= 0) {
             out8 = c.make({rows, dim}, at::kFloat8_e4m3fn);
-            scales = c.make({rows, group ? (dim + group - 1) / group : 1}, at::kFloat);
+            scales = c.make({rows, group && group < dim ? (dim + group - 1) / group : 1}, at::kFloat);
             a.out8 = out8.data_ptr();
             a.scales = (float *)scales.data_ptr();
             a.group = (size_t)group;

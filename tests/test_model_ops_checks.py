@@ -1,10 +1,13 @@
 """What the model operators' calls refuse and what their host code decides
 before a launch: matrices that torch holds in ways of its own, sizes far out of
 range, calls from several threads, waits that run out."""
+import ctypes
+
 import pytest
 import torch
 
 import ring_all_reduce_rar_gb300 as rar
+from ring_all_reduce_rar_gb300 import _ops
 from tests.test_model_ops import DTYPES, gen, h, normal, pieces  # noqa: F401  (h is the fixture)
 
 gpu = pytest.mark.gpu
@@ -56,3 +59,26 @@ def test_one_expanded_row_is_a_row(h):  # noqa: F811
     x = normal(gen(3), 1, 64)
     one = x.as_strided((1, 64), (0, 1))
     assert torch.equal(h.add_rmsnorm([one]).out, h.add_rmsnorm([x]).out)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows,dim", [(3, 2048), (5, 200), (4, 33), (700, 1024), (2, 32768)])
+@pytest.mark.parametrize("group", [32768, 1 << 32, (1 << 32) + 32, 1 << 62, (1 << 64) - 32])
+def test_groups_longer_than_the_row(h, dtype, rows, dim, group):  # noqa: F811
+    """A run of columns that covers the row is the row, also where its length
+    passes 32 bits."""
+    parts = [normal(gen(dim), rows, dim, dtype=dtype) for _ in range(2)]
+    ref = h.add_rmsnorm(parts, quant_group=0)
+    if group < 1 << 63:
+        r = h.add_rmsnorm(parts, quant_group=group)
+        assert r.scales.shape == (rows, 1)
+        assert torch.equal(r.scales, ref.scales) and torch.equal(r.out8.view(torch.uint8), ref.out8.view(torch.uint8))
+    codes, scales = torch.empty(rows, dim, dtype=torch.uint8, device="cuda"), torch.empty(rows, 1, device="cuda")
+    a = _ops.RmsNormArgs()
+    ptrs = (ctypes.c_void_p * 2)(*[t.data_ptr() for t in parts])
+    a.parts, a.p, a.rows, a.dim, a.eps, a.group = ctypes.addressof(ptrs), 2, rows, dim, 1e-6, group
+    a.dtype = {torch.float32: 1, torch.bfloat16: 2, torch.float16: 3}[dtype]
+    a.out8, a.scales = codes.data_ptr(), scales.data_ptr()
+    assert rar.load_library().rar_add_rmsnorm(h.h, ctypes.byref(a), torch.cuda.current_stream().cuda_stream) == 0
+    assert torch.equal(scales, ref.scales) and torch.equal(codes, ref.out8.view(torch.uint8))
