@@ -59,12 +59,17 @@ cudaError_t dispatch_v(int v, F &&f) {
     }
     return cudaErrorInvalidValue;
 }
-// A launch of a kernel whose shared memory may pass 48 KB (with what it declares
-// itself, a few KB).
+// Shared memory that a launch may ask for: the 227 KB of a CTA without 1 KB, which is
+// more than any of these kernels declares itself.
+constexpr size_t kNormMaxSmem = 226 * 1024;
+
+// A launch of a kernel whose shared memory may pass 48 KB.  The limit belongs to the
+// kernel in the whole process: it is the same in every call, so that a call in another
+// thread cannot lower it between this one's two steps.
 template <typename Args>
 cudaError_t launch_any(void (*kern)(Args), dim3 grid, int threads, size_t smem, cudaStream_t stream, const Args &k) {
     if (smem > 32 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kNormMaxSmem);
         if (e != cudaSuccess) return e;
     }
     return launch_pdl(kern, grid, dim3((unsigned)threads), smem, stream, k);

@@ -2,6 +2,7 @@
 before a launch: matrices that torch holds in ways of its own, sizes far out of
 range, calls from several threads, waits that run out."""
 import ctypes
+import threading
 
 import pytest
 import torch
@@ -82,3 +83,48 @@ def test_groups_longer_than_the_row(h, dtype, rows, dim, group):  # noqa: F811
     a.out8, a.scales = codes.data_ptr(), scales.data_ptr()
     assert rar.load_library().rar_add_rmsnorm(h.h, ctypes.byref(a), torch.cuda.current_stream().cuda_stream) == 0
     assert torch.equal(scales, ref.scales) and torch.equal(codes, ref.out8.view(torch.uint8))
+
+
+@gpu
+@pytest.mark.parametrize("op,dims", [("norm", (8, 2)), ("norm any", (30011, 17011)), ("gradient any", (30011, 17011))])
+def test_two_threads_share_no_launch_state(h, op, dims):  # noqa: F811
+    """Two threads, a handle and a stream each, whose calls run one kernel with
+    different amounts of shared memory (8 and 2 parts; rows of different lengths)."""
+    lib, calls, errors = rar.load_library(), 1500, []
+    start = threading.Barrier(2)
+
+    def work(n):
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream), rar.Handle(0, skip_pointer_check=True) as mine:
+            keep = []
+
+            def matrix(rows, cols):
+                keep.append(torch.ones(rows, cols, dtype=torch.bfloat16, device="cuda"))
+                return keep[-1].data_ptr()
+            if op == "norm":
+                a = _ops.RmsNormArgs()
+                a._parts = (ctypes.c_void_p * n)(*[matrix(640, 2048) for _ in range(n)])
+                a.parts, a.p, a.rows, a.dim, a.out = ctypes.addressof(a._parts), n, 640, 2048, matrix(640, 2048)
+            elif op == "norm any":
+                a = _ops.RmsNormArgs()
+                a._parts = (ctypes.c_void_p * 1)(matrix(2, n))
+                a.parts, a.p, a.rows, a.dim, a.out = ctypes.addressof(a._parts), 1, 2, n, matrix(2, n)
+            else:
+                a = _ops.RmsNormGradArgs()
+                rstd = torch.ones(2, device="cuda")
+                a.rows, a.dim, a.dout, a.sum, a.rstd, a.dx = 2, n, matrix(2, n), matrix(2, n), rstd.data_ptr(), matrix(2, n)
+            a.dtype = 2
+            call = lib.rar_add_rmsnorm_grad if op == "gradient any" else lib.rar_add_rmsnorm
+            start.wait()
+            for _ in range(calls):
+                if call(mine.h, ctypes.byref(a), stream.cuda_stream):
+                    errors.append((n, rar.rar_last_error(mine.h)))
+                    break
+            stream.synchronize()
+
+    threads = [threading.Thread(target=work, args=(n,)) for n in dims]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors
