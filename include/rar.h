@@ -137,8 +137,10 @@ typedef struct {
     int fault_mode;                /* rar_fault_mode (tests): ring and tree engines; and
                                       RAR_FAULT_MUTE on the fused streaming path, where
                                       the loads of rank fault_rank are never issued, as
-                                      if that rank had died */
-    int fault_rank;                /* rank the fault applies to */
+                                      if that rank had died, and in the same way in
+                                      rar_add_rmsnorm and its gradient, for many rows */
+    int fault_rank;                /* rank the fault applies to (rar_add_rmsnorm_grad: 0 dout,
+                                      1 sum, 2 dsum) */
     unsigned fault_delay_ns;       /* RAR_FAULT_DELAY: pause before each slice */
     int fused_path;                /* RAR_ENGINE_FUSED data path, same results on both:
                                       0 auto; 1 per-thread 128-bit loads of all p

@@ -46,6 +46,7 @@ __device__ __forceinline__ unsigned long long now_ns() {
 struct WaitLimits {
     RingStatus *status;
     unsigned long long timeout_ns;
+    int mute;  // RAR_FAULT_MUTE: the rank whose copies are not issued, or -1
 };
 // RingStatus::rank of a wait that ran out here; `step` then says what was
 // waited for, `slice` which CTA waited.
@@ -55,6 +56,7 @@ enum { WAIT_OF_XENT = -2, WAIT_OF_NORM = -3 };
 // passed or another wait of the CTA has given up.
 __device__ __forceinline__ bool mbar_wait(int *failed, const WaitLimits &lim, uint64_t *bar, uint32_t parity, int of, int what) {
     if (mbar_try_wait(bar, parity)) return true;
+    if (*(volatile int *)failed) return false;
     const unsigned long long t0 = now_ns();
     const unsigned long long most = lim.timeout_ns / 16ull + (1ull << 20);
     for (unsigned long long it = 0; it < most; it++) {
@@ -75,14 +77,16 @@ __device__ __forceinline__ bool mbar_wait(int *failed, const WaitLimits &lim, ui
 }
 
 // Waits for loads that were issued: they land by themselves, so the limit
-// (1 s) is only reached on a broken device, or when the other CTA of a failed
-// pair never issued its own.
-__device__ __forceinline__ void mbar_drain(uint64_t *bar, uint32_t parity) {
+// (1 s) is only reached on a broken device, or where some of a stage's were never
+// issued (by the other CTA of a failed pair, or a muted rank).  False then: whatever the
+// CTA did issue has landed meanwhile.
+__device__ __forceinline__ bool mbar_drain(uint64_t *bar, uint32_t parity) {
     const unsigned long long t0 = now_ns();
     for (unsigned long long it = 0; it < (1ull << 32); it++) {
-        if (mbar_try_wait(bar, parity)) return;
-        if ((it & 63) == 63 && now_ns() - t0 > 1000000000ull) return;
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((it & 63) == 63 && now_ns() - t0 > 1000000000ull) break;
     }
+    return false;
 }
 
 }  // namespace rar

@@ -127,6 +127,9 @@ inline bool vec16(const void *ptr, size_t rows, long long stride, size_t e) {
 // The handle's bound on every wait of a call.
 inline unsigned long long op_timeout_ns(const rar_ctx *h) { return h->opt.timeout_ns ? h->opt.timeout_ns : 2000000000ull; }
 
+// The rank that RAR_FAULT_MUTE names, or -1.
+inline int op_muted_rank(const rar_ctx *h) { return h->opt.fault_mode == RAR_FAULT_MUTE ? h->opt.fault_rank : -1; }
+
 // Runs an entry point's body: no C++ exception leaves the library.
 template <typename F>
 int guarded(rar_ctx *h, F &&body) {

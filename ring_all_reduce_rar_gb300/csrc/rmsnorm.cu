@@ -245,6 +245,7 @@ __global__ void __launch_bounds__(2 * kRingRowThreads + 32, 1) add_rmsnorm_ring_
         for (int s = 0; s < a.stages; s++) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], (uint32_t)a.warps);
+            row_chunk[s] = 0;  // (read also after a wait that ran out)
         }
         mbar_fence_init();
     }
@@ -270,14 +271,16 @@ __global__ void __launch_bounds__(2 * kRingRowThreads + 32, 1) add_rmsnorm_ring_
                 mbar_expect_tx(&full[st], stage_bytes);
             }
             __syncwarp();
-            for (int r = tid; r < matrices; r += 32)
+            for (int r = tid; r < matrices; r += 32) {
+                if (r == a.limits.mute) continue;
                 bulk_load(ring + (size_t)st * stage_bytes + (size_t)r * row_bytes,
                           r < a.p ? row_of<DT>((const void *)rank_ptr(a.parts, a.p, r), t, a.part_stride) : row_of<DT>(a.residual, t, a.residual_stride),
                           row_bytes, &full[st]);
+            }
         }
         // the CTA stays until its copies have landed
         for (unsigned q = k > (unsigned)a.stages ? k - (unsigned)a.stages : 0; q < k; q++)
-            mbar_drain(&full[q % (unsigned)a.stages], (q / (unsigned)a.stages) & 1);
+            if (!mbar_drain(&full[q % (unsigned)a.stages], (q / (unsigned)a.stages) & 1)) break;
         return;
     }
     const int vecs = (int)(a.dim / VE), bar = 1 + group;
@@ -322,7 +325,7 @@ __global__ void __launch_bounds__(2 * kRingRowThreads + 32, 1) add_rmsnorm_ring_
                 if (has) ss = fmaf(s[v][e], s[v][e], ss);
         }
         __syncwarp();
-        if (tid % 32 == 0) mbar_arrive(&empty[st]);
+        if (tid % 32 == 0) free_stage(&failed, &empty[st]);
         // the row's sum over the warps (two buffers: one barrier a row)
         ss = warp_sum(ss);
         if (tid % 32 == 0) red[group][parity][tid / 32] = ss;
@@ -480,7 +483,7 @@ int add_rmsnorm(rar_ctx *h, const rar_rmsnorm_args *a, cudaStream_t stream) {
         const RingShape ring = vec ? ring_shape(h, a->rows, ring_row, ring_threads, 682, 2, stage_bytes) : RingShape{0, 0};
         if (ring.ctas) k.warps = ring_row.warps;
         k.stages = ring.stages;
-        k.limits = {h->status, op_timeout_ns(h)};
+        k.limits = {h->status, op_timeout_ns(h), op_muted_rank(h)};
         const size_t rows_cta = (size_t)std::max(1, 4 / shape.warps);
         const dim3 grid((unsigned)((a->rows + rows_cta - 1) / rows_cta)), block((unsigned)(rows_cta * shape.warps * 32));
         const size_t smem = quant == 2 ? sizeof(unsigned) * rows_cta * n_groups : 0;

@@ -38,6 +38,13 @@ constexpr int kNormMaxStages = 8;
 // Barrier `bar`: the n threads of a row, without the loading warp.
 __device__ __forceinline__ void row_threads_sync(int bar, int n) { asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(n) : "memory"); }
 
+// A warp has read a stage of a ring; one lane comes here, after its warp's __syncwarp.
+// After a wait of the CTA that ran out no stage is free any more: the row that a warp
+// gave up may still be on its way, and its barrier must not be armed a second time.
+__device__ __forceinline__ void free_stage(int *failed, uint64_t *empty) {
+    if (!*(volatile int *)failed) mbar_arrive(empty);
+}
+
 // Warps a row and vectors a thread, both powers of two, for `vecs` vectors: up to
 // `most` threads of one vector, then up to 4 vectors; v is 0 where that does not hold the row.
 struct RowShape {

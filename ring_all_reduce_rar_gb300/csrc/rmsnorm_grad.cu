@@ -155,13 +155,13 @@ __global__ void __launch_bounds__(kNormMaxThreads + 32, V == 1 ? 2 : 1) rmsnorm_
                 mbar_arrive(&full[st]);
             }
             __syncwarp();
-            if (lane < matrices)
+            if (lane < matrices && lane != a.limits.mute)
                 bulk_load(ring + (size_t)st * stage_bytes + (size_t)lane * row_bytes,
                           lane == 0 ? row_of<DT>(a.dout, t, a.dout_stride) : lane == 1 ? row_of<DT>(a.sum, t, a.sum_stride) : row_of<DT>(a.dsum, t, a.dsum_stride),
                           row_bytes, &full[st]);
         }
         for (unsigned q = k > (unsigned)a.stages ? k - (unsigned)a.stages : 0; q < k; q++)
-            mbar_drain(&full[q % (unsigned)a.stages], (q / (unsigned)a.stages) & 1);
+            if (!mbar_drain(&full[q % (unsigned)a.stages], (q / (unsigned)a.stages) & 1)) break;
         return;
     }
     const int vecs = (int)(a.dim / VE);
@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(kNormMaxThreads + 32, V == 1 ? 2 : 1) rmsnorm_
         }
         const float rstd = s_rstd[st];
         __syncwarp();
-        if (tid % 32 == 0) mbar_arrive(&empty[st]);
+        if (tid % 32 == 0) free_stage(&failed, &empty[st]);
         float dot = warp_sum(grad_sums<DT, V>(a, dy, x, w, rstd, dw));
         if (tid % 32 == 0) red[parity][tid / 32] = dot;  // two buffers: one barrier a row
         row_threads_sync(1, n);
@@ -345,7 +345,7 @@ int add_rmsnorm_grad(rar_ctx *h, const rar_rmsnorm_grad_args *a, cudaStream_t st
     // 1024 threads an SM, and parts of dweight as the workspace has them
     const int ctas = std::min<int>(ring.ctas ? ring.ctas : std::max(1, 1024 / (shape.warps * 32)), (int)kNormGradCtas / h->sm_count);
     k.stages = ring.stages;
-    k.limits = {h->status, op_timeout_ns(h)};
+    k.limits = {h->status, op_timeout_ns(h), op_muted_rank(h)};
     k.n_partial = (int)std::min<size_t>(k.n_partial, (size_t)h->sm_count * ctas);
     const bool odd = !vec && alike && ((size_t)k.n_partial == a->rows || k.n_partial % 8 == 0);
     const dim3 grid((unsigned)k.n_partial);

@@ -764,7 +764,7 @@ int vocab_xent(rar_ctx *h, const rar_vocab_xent_args *a, cudaStream_t stream) {
     k.want_dw = a->dweights != nullptr;
     note_op_call(h, a->p, stream);
 
-    k.limits = {h->status, op_timeout_ns(h)};
+    k.limits = {h->status, op_timeout_ns(h), op_muted_rank(h)};
 
     XentMaps logits, dh, dw;  // of the products that use them
     bool mapped = true;

@@ -11,6 +11,8 @@ import ring_all_reduce_rar_gb300 as rar
 from ring_all_reduce_rar_gb300 import _ops
 from tests.test_model_ops import DTYPES, gen, h, normal, pieces  # noqa: F401  (h is the fixture)
 
+MUTE = dict(timeout_ns=50_000_000, fault_mode="mute")
+
 gpu = pytest.mark.gpu
 
 
@@ -128,3 +130,43 @@ def test_two_threads_share_no_launch_state(h, op, dims):  # noqa: F811
     for t in threads:
         t.join()
     assert not errors
+
+
+def check_time_out(call, ref, handle, words):
+    """`call` on a handle with a muted rank reports RAR_ETIMEOUT once; the same
+    call on it without the fault has the results `ref`."""
+    call()
+    assert handle.status() == 5  # RAR_ETIMEOUT
+    assert words in rar.rar_last_error(handle.h)
+    assert handle.status() == 0
+    handle.set_options()
+    for got, want in zip(call(), ref):
+        assert torch.equal(got, want)
+    handle.check()
+
+
+@gpu
+@pytest.mark.parametrize("mute", [0, 2])
+@pytest.mark.parametrize("p,rows,dim", [(3, 640, 2048), (4, 5000, 4096)])
+def test_residual_norm_muted_rank_times_out(h, p, rows, dim, mute):  # noqa: F811
+    """A rank whose rows never arrive: the waits for them run out, no stage is
+    handed back to the loads before its row has landed, and the kernel ends."""
+    g = gen(p + mute)
+    parts, res = [normal(g, rows, dim, dtype=torch.bfloat16) for _ in range(p)], normal(g, rows, dim, dtype=torch.bfloat16)
+    for group in (None, 128, 0):
+        def call(handle):
+            r = handle.add_rmsnorm(parts, residual=res, quant_group=group, keep_out=True)
+            return [r.sum, r.rstd, r.out] + ([] if group is None else [r.scales])
+        with rar.Handle(0, fault_rank=mute, **MUTE) as faulty:
+            check_time_out(lambda: call(faulty), call(h), faulty, "residual norm")
+
+
+@gpu
+@pytest.mark.parametrize("mute", [0, 1, 2])
+def test_residual_norm_gradient_muted_matrix_times_out(h, mute):  # noqa: F811
+    g = gen(mute)
+    dout, s, dsum = (normal(g, 5000, 2048, dtype=torch.bfloat16) for _ in range(3))
+    rstd = torch.ones(5000, device="cuda")
+    with rar.Handle(0, fault_rank=mute, **MUTE) as faulty:
+        check_time_out(lambda: faulty.add_rmsnorm_grad(dout, s, rstd, dsum=dsum), h.add_rmsnorm_grad(dout, s, rstd, dsum=dsum), faulty,
+                       "residual norm")
