@@ -138,7 +138,8 @@ typedef struct {
                                       RAR_FAULT_MUTE on the fused streaming path, where
                                       the loads of rank fault_rank are never issued, as
                                       if that rank had died, and in the same way in
-                                      rar_add_rmsnorm and its gradient, for many rows */
+                                      rar_add_rmsnorm and its gradient, for many rows,
+                                      and rar_vocab_xent (fault_rank: a piece) */
     int fault_rank;                /* rank the fault applies to (rar_add_rmsnorm_grad: 0 dout,
                                       1 sum, 2 dsum) */
     unsigned fault_delay_ns;       /* RAR_FAULT_DELAY: pause before each slice */

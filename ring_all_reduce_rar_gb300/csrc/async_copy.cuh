@@ -46,7 +46,7 @@ __device__ __forceinline__ unsigned long long now_ns() {
 struct WaitLimits {
     RingStatus *status;
     unsigned long long timeout_ns;
-    int mute;  // RAR_FAULT_MUTE: the rank whose copies are not issued, or -1
+    int mute;  // RAR_FAULT_MUTE: the rank (matrix, piece) whose copies never complete, or -1
 };
 // RingStatus::rank of a wait that ran out here; `step` then says what was
 // waited for, `slice` which CTA waited.

@@ -397,12 +397,13 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(152)
                 return true;
             });
         }
-        // neither CTA may leave while the pair's loads or arrivals are on their
-        // way (the loads even after a wait that ran out)
+        // neither CTA may leave while the pair's loads, products or arrivals are under way,
+        // nor give its tensor memory back, even after a wait that ran out: products in flight
+        // belong to the last stages, whose `empty` they arrive at in both CTAs
         for (unsigned k = step > kTcStages ? step - kTcStages : 0; k < step && lane == 0; k++) {
             const int st = (int)(k % kTcStages);
-            if (rank == 0) mbar_drain(&sh.full[st], (k / kTcStages) & 1);
-            tc_wait(&sh, a.limits, &sh.empty[st], (k / kTcStages) & 1, 1);
+            if (rank == 0 && !mbar_drain(&sh.full[st], (k / kTcStages) & 1)) break;
+            if (!mbar_drain(&sh.empty[st], (k / kTcStages) & 1)) break;
         }
     } else if (warp == kTcEpilogueWarps + 1 && lane == 0 && rank == 0) {
         const uint64_t operand_a = tc_operand(stages, a_mn ? 8192 : 16, 1024), operand_b = tc_operand(stages + 16384, b_mn ? 8192 : 16, 1024);
@@ -772,8 +773,9 @@ int vocab_xent(rar_ctx *h, const rar_vocab_xent_args *a, cudaStream_t stream) {
         mapped = make_map(&logits.one, a->dtype, k.hidden, k.tokens, k.dim, k.hidden_stride, 128);
         for (int r = 0; r < k.p && mapped; r++) {
             const long long rows = k.base + (r < k.extra ? 1 : 0);
-            if (rows) mapped = make_map(&logits.w[r], a->dtype, k.w.inl[r], rows, k.dim, k.weight_stride, 128);
-            if (rows && mapped && k.dhidden) mapped = make_map(&dh.w[r], a->dtype, k.w.inl[r], rows, k.dim, k.weight_stride, 64);
+            const int short_of = r == k.limits.mute ? 1 : 0;  // a box without its last row completes no stage
+            if (rows) mapped = make_map(&logits.w[r], a->dtype, k.w.inl[r], rows, k.dim, k.weight_stride, 128 - short_of);
+            if (rows && mapped && k.dhidden) mapped = make_map(&dh.w[r], a->dtype, k.w.inl[r], rows, k.dim, k.weight_stride, 64 - short_of);
         }
         const long long pitch = (long long)k.window * kBlock;
         if (k.dhidden) mapped = mapped && make_map(&dh.one, a->dtype, k.g, k.tokens, pitch, pitch, 128);

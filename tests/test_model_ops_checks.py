@@ -170,3 +170,20 @@ def test_residual_norm_gradient_muted_matrix_times_out(h, mute):  # noqa: F811
     with rar.Handle(0, fault_rank=mute, **MUTE) as faulty:
         check_time_out(lambda: faulty.add_rmsnorm_grad(dout, s, rstd, dsum=dsum), h.add_rmsnorm_grad(dout, s, rstd, dsum=dsum), faulty,
                        "residual norm")
+
+
+@gpu
+@pytest.mark.parametrize("mute", [0, 2])
+@pytest.mark.parametrize("tokens,dim,vocab,grad", [(300, 256, 5000, True), (20, 64, 40, True), (600, 1288, 20000, False), (130, 1288, 9000, True)])
+def test_cross_entropy_muted_piece_times_out(h, tokens, dim, vocab, grad, mute):  # noqa: F811
+    """A piece whose tiles never arrive: loads, products and epilogues of both
+    CTAs of a pair give up, the products under way are waited for, and the kernels end."""
+    g = gen(tokens + mute)
+    hidden, whole = normal(g, tokens, dim, dtype=torch.bfloat16), normal(g, vocab, dim, dtype=torch.bfloat16, std=0.1)
+    targets = torch.randint(0, vocab, (tokens,), generator=g, device="cuda")
+
+    def call(handle):
+        r = handle.vocab_xent(hidden, pieces(whole, 3), targets, grad=grad)
+        return [r.loss, r.lse] + ([r.dhidden, *r.dweights] if grad else [])
+    with rar.Handle(0, fault_rank=mute, **MUTE) as faulty:
+        check_time_out(lambda: call(faulty), call(h), faulty, "vocabulary cross entropy")
