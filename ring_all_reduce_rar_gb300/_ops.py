@@ -108,12 +108,19 @@ def _module():
 
 
 def _run(handle, stream, function, *args):
-    """function(handle, *args) with `stream` as the current stream; its results."""
+    """function(handle, *args) with `stream`, which belongs to the device of the
+    tensors (args[0], a tensor or several), as the current stream; its results."""
     if stream is None:
         r = function(handle, *args)
     else:
         import torch
-        s = torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
+        first = args[0][0] if isinstance(args[0], (list, tuple)) and args[0] else args[0]
+        device = getattr(first, "device", None)
+        if getattr(device, "type", None) != "cuda":
+            raise ValueError("the operators take CUDA tensors")
+        s = torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream
+        if s.device != device:
+            raise ValueError(f"the stream belongs to {s.device}, the tensors are on {device}")
         with torch.cuda.stream(s):
             r = function(handle, *args)
     if type(r) is int:

@@ -1,8 +1,10 @@
 """What the model operators' calls refuse and what their host code decides
 before a launch: matrices that torch holds in ways of its own, sizes far out of
 range, calls from several threads, waits that run out."""
+import contextlib
 import ctypes
 import threading
+import types
 
 import pytest
 import torch
@@ -187,3 +189,56 @@ def test_cross_entropy_muted_piece_times_out(h, tokens, dim, vocab, grad, mute):
         return [r.loss, r.lse] + ([r.dhidden, *r.dweights] if grad else [])
     with rar.Handle(0, fault_rank=mute, **MUTE) as faulty:
         check_time_out(lambda: call(faulty), call(h), faulty, "vocabulary cross entropy")
+
+
+OPS = [("add_rmsnorm", lambda t, s: rar.rar_add_rmsnorm(7, [t], stream=s)),
+       ("add_rmsnorm_grad", lambda t, s: rar.rar_add_rmsnorm_grad(7, t, t, t, stream=s)),
+       ("vocab_xent", lambda t, s: rar.rar_vocab_xent(7, t, [t], t, stream=s)),
+       ("embedding", lambda t, s: rar.rar_embedding(7, (t,), t, stream=s)),
+       ("embedding_grad", lambda t, s: rar.rar_embedding_grad(7, t, t, [t], stream=s))]
+
+
+@pytest.mark.parametrize("name,call", OPS)
+def test_a_stream_belongs_to_the_tensors_device(monkeypatch, name, call):
+    """The current device has no part in a stream that is given as an integer;
+    a stream object of another device is refused.  (Stands in for two devices.)"""
+    seen = []
+
+    def operator(handle, *args):
+        seen.append(("call", handle))
+        return (None,) * {"add_rmsnorm": 5, "vocab_xent": 4}.get(name, 1)
+
+    @contextlib.contextmanager
+    def current(stream):
+        seen.append((stream.cuda_stream, stream.device))
+        yield
+    # (a stream without a device is one of the current device, 0)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda ptr, device=torch.device("cuda", 0):
+                        types.SimpleNamespace(cuda_stream=ptr, device=device))
+    monkeypatch.setattr(torch.cuda, "stream", current)
+    monkeypatch.setattr(_ops, "_module", lambda: types.SimpleNamespace(**{name: operator}))
+    on = types.SimpleNamespace(device=torch.device("cuda", 1))
+    call(on, 1234)
+    assert seen == [(1234, torch.device("cuda", 1)), ("call", 7)]
+    seen.clear()
+    other = types.SimpleNamespace(cuda_stream=5, device=torch.device("cuda", 0))
+    with pytest.raises(ValueError, match="stream"):
+        call(on, other)
+    assert not seen
+    call(on, None)
+    assert seen == [("call", 7)]
+
+
+@gpu
+def test_a_stream_as_an_integer(h):  # noqa: F811
+    g = gen(5)
+    table, tok = normal(g, 50, 64), torch.tensor([3, 49, 50, 0], device="cuda")
+    ref = h.embedding([table], tok)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    y = h.embedding([table], tok, stream=side.cuda_stream)
+    side.synchronize()
+    assert torch.equal(y, ref)
+    y = h.embedding([table], tok, stream=0)  # the legacy default stream
+    torch.cuda.synchronize()
+    assert torch.equal(y, ref)
