@@ -8,8 +8,10 @@ from __future__ import annotations
 
 import importlib.util
 import os
+import shutil
 import subprocess
 import sysconfig
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -41,7 +43,7 @@ def _inputs():
 
 
 def up_to_date() -> bool:
-    outputs = [LIB_PATH] + ([TORCH_OPS_PATH] if _torch_dir() else [])
+    outputs = [LIB_PATH] + ([] if binding_lacks() else [TORCH_OPS_PATH])
     if not all(os.path.exists(f) for f in outputs):
         return False
     t = min(os.path.getmtime(f) for f in outputs)
@@ -54,9 +56,30 @@ def _torch_dir() -> str | None:
     return os.path.dirname(spec.origin) if spec and spec.origin else None
 
 
+def _cuda_include() -> str:
+    return os.path.join(os.path.dirname(os.path.dirname(shutil.which(_nvcc()) or _nvcc())), "include")
+
+
+def binding_lacks() -> str | None:
+    """What the module on torch tensors needs, beyond what the library needs,
+    and this machine does not have; None where it can be built."""
+    torch_dir = _torch_dir()
+    if not torch_dir:
+        return "torch"
+    if not shutil.which("g++"):
+        return "g++"
+    needs = [os.path.join(sysconfig.get_paths()["include"], "Python.h"),
+             os.path.join(torch_dir, "include", "torch", "csrc", "autograd", "python_variable.h"),
+             os.path.join(torch_dir, "include", "c10", "cuda", "CUDAStream.h"),
+             os.path.join(torch_dir, "lib", "libtorch_python.so"),
+             os.path.join(torch_dir, "lib", "libc10_cuda.so"),
+             os.path.join(_cuda_include(), "cuda_runtime_api.h")]
+    return next((f for f in needs if not os.path.exists(f)), None)
+
+
 def _compile_torch_ops(obj: str) -> None:
     torch_dir = _torch_dir()
-    cuda = os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")
+    cuda = _cuda_include()
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-c", "-I", INCLUDE, "-I", sysconfig.get_paths()["include"],
            "-isystem", os.path.join(torch_dir, "include"), "-isystem",
            os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"), "-isystem", cuda,
@@ -94,18 +117,20 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
         return obj
 
     torch_obj = os.path.join(BUILD_DIR, "torch_ops.o")
+    lacks = binding_lacks()
+    if lacks not in (None, "torch"):
+        warnings.warn(f"_torch_ops.so is not built (the operators on torch tensors): {lacks} is missing")
     with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        torch_ops = ex.submit(_compile_torch_ops, torch_obj) if _torch_dir() else None
+        torch_ops = None if lacks else ex.submit(_compile_torch_ops, torch_obj)
         objs = list(ex.map(compile_one, SOURCES))
-        if torch_ops:
-            torch_ops.result()
     tmp = LIB_PATH + f".tmp{os.getpid()}"
     cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB_PATH)
-    if torch_ops:
+    if torch_ops:  # (last: the library does without it)
+        torch_ops.result()
         _link_torch_ops(torch_obj)
     return LIB_PATH
 

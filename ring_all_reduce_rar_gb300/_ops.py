@@ -99,8 +99,9 @@ def _module():
     _abi.load_library()
     path = _build.TORCH_OPS_PATH
     if not os.path.exists(path):
-        raise RuntimeError(f"{path} is missing: build the library first "
-                           "(python -c 'import __graft_entry__ as g; g.build()')")
+        lacks = _build.binding_lacks()
+        raise RuntimeError(f"{path} is missing: " + (f"it cannot be built without {lacks}" if lacks else
+                           "build the library first (python -c 'import __graft_entry__ as g; g.build()')"))
     loader = importlib.machinery.ExtensionFileLoader("_torch_ops", path)
     module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_torch_ops", loader))
     loader.exec_module(module)
