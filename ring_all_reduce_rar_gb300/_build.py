@@ -46,6 +46,8 @@ def up_to_date() -> bool:
     outputs = [LIB_PATH] + ([] if binding_lacks() else [TORCH_OPS_PATH])
     if not all(os.path.exists(f) for f in outputs):
         return False
+    if len(outputs) > 1 and _built_against() != _torch_version():
+        return False
     t = min(os.path.getmtime(f) for f in outputs)
     return all(os.path.getmtime(f) <= t for f in _inputs())
 
@@ -54,6 +56,21 @@ def _torch_dir() -> str | None:
     """Where torch is installed (it is not imported)."""
     spec = importlib.util.find_spec("torch")
     return os.path.dirname(spec.origin) if spec and spec.origin else None
+
+
+def _torch_version() -> str:
+    """The torch and Python that the binding's ABI belongs to."""
+    with open(os.path.join(_torch_dir(), "version.py")) as f:
+        version = next((line.split("=")[1].strip(" '\"\n") for line in f if line.startswith("__version__")), "")
+    return f"{version} in {_torch_dir()}, {sysconfig.get_config_var('EXT_SUFFIX')}"
+
+
+def _built_against() -> str | None:
+    try:
+        with open(TORCH_OPS_PATH + ".torch") as f:
+            return f.read()
+    except FileNotFoundError:
+        return None
 
 
 def _cuda_include() -> str:
@@ -97,6 +114,8 @@ def _link_torch_ops(obj: str) -> None:
     if r.returncode != 0:
         raise RuntimeError(f"linking _torch_ops.so failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, TORCH_OPS_PATH)
+    with open(TORCH_OPS_PATH + ".torch", "w") as f:
+        f.write(_torch_version())
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | None = None) -> str:

@@ -65,3 +65,19 @@ def test_both_are_built(tree):
     n = len(tree.commands)
     _build.build()
     assert len(tree.commands) == n
+
+
+@binding
+def test_another_torch_is_seen(tree, monkeypatch):
+    """The binding belongs to the torch that it was built against."""
+    _build.build()
+    assert _build.up_to_date()
+    monkeypatch.setattr(_build, "_torch_version", lambda: "another version")
+    assert not _build.up_to_date()
+    _build.build()
+    assert _build.up_to_date()
+
+
+def test_torch_version_without_importing_it():
+    torch = pytest.importorskip("torch")
+    assert torch.__version__ in _build._torch_version()
