@@ -487,7 +487,7 @@ typedef struct {
     size_t table_stride;       /* of every piece */
     int p;                     /* 1 .. RAR_MAX_P */
     int dtype;
-    size_t vocab, dim;         /* at least 1 */
+    size_t vocab, dim;         /* at least 1; dim at most 2^31 - 1 */
     const void *tokens;        /* n_tokens indices */
     int index_bytes;
     size_t n_tokens;           /* 0: nothing is done */

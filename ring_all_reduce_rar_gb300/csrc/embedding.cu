@@ -542,6 +542,7 @@ int embedding(rar_ctx *h, const rar_embedding_args *a, cudaStream_t stream) {
     if (rc != RAR_OK) return rc;
     if (a->p < 1 || a->p > RAR_MAX_P) return c.bad("p must be in [1, RAR_MAX_P]");
     if (a->vocab < 1 || a->dim < 1) return c.bad("vocab and dim must be at least 1");
+    if (a->dim > 0x7FFFFFFFu) return c.bad("dim must be at most 2^31 - 1");  // (columns are counted in 32 bits)
     if (a->index_bytes != 4 && a->index_bytes != 8) return c.bad("index_bytes must be 4 or 8");
     if (a->n_tokens == 0) return RAR_OK;
     const size_t e = (size_t)elem_bytes(a->dtype);

@@ -242,3 +242,17 @@ def test_a_stream_as_an_integer(h):  # noqa: F811
     y = h.embedding([table], tok, stream=0)  # the legacy default stream
     torch.cuda.synchronize()
     assert torch.equal(y, ref)
+
+
+@gpu
+@pytest.mark.parametrize("dim", [1 << 31, (1 << 33) + 8, 1 << 57])
+def test_lookup_of_rows_beyond_32_bits_is_refused(h, dim):  # noqa: F811
+    """Columns are counted in 32 bits.  (Refused before the pointers are looked at:
+    the matrices here hold nothing of that length.)"""
+    x, tok = torch.zeros(64, device="cuda"), torch.zeros(1, dtype=torch.int64, device="cuda")
+    a = _ops.EmbeddingArgs()
+    ptrs = (ctypes.c_void_p * 1)(x.data_ptr())
+    a.tables, a.p, a.dtype, a.vocab, a.dim, a.tokens = ctypes.addressof(ptrs), 1, 1, 1, dim, tok.data_ptr()
+    a.index_bytes, a.n_tokens, a.scale, a.out = 8, 1, 1.0, None
+    assert rar.load_library().rar_embedding(h.h, ctypes.byref(a), torch.cuda.current_stream().cuda_stream) == 1
+    assert "dim" in rar.rar_last_error(h.h)
