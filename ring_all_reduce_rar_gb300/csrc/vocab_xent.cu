@@ -634,6 +634,7 @@ EncodeTiled encode_tiled() {
 bool make_map(CUtensorMap *m, int dtype, const void *ptr, long long rows, long long cols, long long stride, int box_rows) {
     const EncodeTiled encode = encode_tiled();
     if (!encode) return false;
+    if (rows == 1) stride = cols;  // (no distance to a next row: any value is accepted)
     const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)stride * 2};
     const cuuint32_t box[2] = {64, (cuuint32_t)box_rows}, steps[2] = {1, 1};
     return encode(m, dtype == DT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,

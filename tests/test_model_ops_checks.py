@@ -256,3 +256,23 @@ def test_lookup_of_rows_beyond_32_bits_is_refused(h, dim):  # noqa: F811
     a.index_bytes, a.n_tokens, a.scale, a.out = 8, 1, 1.0, None
     assert rar.load_library().rar_embedding(h.h, ctypes.byref(a), torch.cuda.current_stream().cuda_stream) == 1
     assert "dim" in rar.rar_last_error(h.h)
+
+
+@gpu
+def test_cross_entropy_of_single_rows_with_any_stride(h):  # noqa: F811
+    """One token and pieces of one row each: the strides, which nothing is
+    read by, need not suit a tensor map."""
+    g = gen(9)
+    hidden, whole = normal(g, 1, 64, dtype=torch.bfloat16), normal(g, 3, 64, dtype=torch.bfloat16)
+    tok = torch.tensor([2], device="cuda")
+    ref = h.vocab_xent(hidden, pieces(whole, 3), tok)
+    lib = rar.load_library()
+    for stride in (65, 68, 1 << 45):
+        loss, ws = torch.empty(1, device="cuda"), torch.empty(lib.rar_vocab_xent_workspace(1, 64, 3, 3, 0), dtype=torch.uint8, device="cuda")
+        a = _ops.VocabXentArgs()
+        ptrs = (ctypes.c_void_p * 3)(*[t.data_ptr() for t in pieces(whole, 3)])
+        a.hidden, a.hidden_stride, a.weights, a.weight_stride = hidden.data_ptr(), stride, ctypes.addressof(ptrs), stride
+        a.p, a.dtype, a.tokens, a.dim, a.vocab, a.targets, a.index_bytes = 3, 2, 1, 64, 3, tok.data_ptr(), 8
+        a.loss, a.workspace, a.workspace_bytes = loss.data_ptr(), ws.data_ptr(), ws.numel()
+        assert lib.rar_vocab_xent(h.h, ctypes.byref(a), torch.cuda.current_stream().cuda_stream) == 0, rar.rar_last_error(h.h)
+        assert torch.equal(loss, ref.loss)
