@@ -241,6 +241,7 @@ PyObject *vocab_xent(PyObject *, PyObject *const *args, Py_ssize_t nargs) {
         const Pieces w("a weight piece", weights, c);
         const int64_t tokens = hidden.size(0);
         const bool grad = PyObject_IsTrue(args[5]) == 1;
+        if (PyErr_Occurred()) return nullptr;
         rar_vocab_xent_args a{};
         a.hidden_stride = matrix("hidden", hidden, tokens, w.dim, c);
         a.hidden = hidden.data_ptr();

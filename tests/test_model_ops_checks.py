@@ -276,3 +276,14 @@ def test_cross_entropy_of_single_rows_with_any_stride(h):  # noqa: F811
         a.loss, a.workspace, a.workspace_bytes = loss.data_ptr(), ws.data_ptr(), ws.numel()
         assert lib.rar_vocab_xent(h.h, ctypes.byref(a), torch.cuda.current_stream().cuda_stream) == 0, rar.rar_last_error(h.h)
         assert torch.equal(loss, ref.loss)
+
+
+@gpu
+def test_flags_without_a_truth_value(h):  # noqa: F811
+    """An exception while a flag is read is that exception, before anything runs."""
+    x, tok = torch.ones(4, 64, dtype=torch.bfloat16, device="cuda"), torch.zeros(4, dtype=torch.int64, device="cuda")
+    neither = torch.ones(2)
+    for call in (lambda: h.vocab_xent(x, [x], tok, grad=neither), lambda: h.add_rmsnorm([x], keep_out=neither),
+                 lambda: h.embedding_grad(x, tok, [x.clone()], accumulate=neither)):
+        with pytest.raises(RuntimeError, match="ambiguous"):
+            call()
