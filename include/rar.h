@@ -395,7 +395,7 @@ typedef struct {
     const void *const *parts; /* host array of p matrices rows x dim */
     int p;                    /* 1 .. RAR_MAX_P */
     int dtype;                /* of parts, residual, weight, sum and out */
-    size_t rows, dim;         /* 0 rows: nothing is done; dim 1 .. RAR_NORM_MAX_DIM */
+    size_t rows, dim;         /* rows 0 (nothing is done) .. 2^31 - 1; dim 1 .. RAR_NORM_MAX_DIM */
     size_t part_stride;
     const void *residual;     /* rows x dim, or NULL */
     size_t residual_stride;

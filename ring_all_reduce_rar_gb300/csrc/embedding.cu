@@ -557,6 +557,16 @@ int embedding(rar_ctx *h, const rar_embedding_args *a, cudaStream_t stream) {
     c.output(s);
     if ((rc = c.overlaps([](const MatrixSpan &, const MatrixSpan &) { return false; })) != RAR_OK) return rc;
 
+    const long long table_stride = (long long)(a->table_stride ? a->table_stride : a->dim), row_stride = (long long)(a->out_stride ? a->out_stride : a->dim);
+    const size_t ve = 16 / e;
+    bool vec = a->dim % ve == 0 && vec16(a->out, a->n_tokens, row_stride, e);
+    for (int r = 0; r < a->p && vec; r++) vec = vec16(a->tables[r], a->vocab / a->p + 1, table_stride, e);
+    // 4 loads in flight a thread where that still leaves 4 CTAs an SM, else one
+    const size_t count = vec ? a->n_tokens * (a->dim / ve) : a->n_tokens * a->dim;
+    const bool many = count >= (size_t)h->sm_count * 4 * 1024;
+    const size_t ctas = many ? (count + 1023) / 1024 : (count + 255) / 256;
+    if (ctas > 0x7FFFFFFFu) return c.bad("the lookup is too large");
+
     DeviceGuard dg(h->device);
     if (dg.err != cudaSuccess) return cuda_fail(h, dg.err, "selecting the device");
     EmbedArgs k{};
@@ -565,21 +575,13 @@ int embedding(rar_ctx *h, const rar_embedding_args *a, cudaStream_t stream) {
     k.vocab = (long long)a->vocab;
     k.dim = (long long)a->dim;
     k.n_tokens = (long long)a->n_tokens;
-    k.table_stride = (long long)(a->table_stride ? a->table_stride : a->dim);
-    k.row_stride = (long long)(a->out_stride ? a->out_stride : a->dim);
+    k.table_stride = table_stride;
+    k.row_stride = row_stride;
     k.tokens = a->tokens;
     k.index_bytes = a->index_bytes;
     k.scale = a->scale;
     k.out = a->out;
     note_op_call(h, a->p, stream);
-    const size_t ve = 16 / e;
-    bool vec = a->dim % ve == 0 && vec16(a->out, a->n_tokens, k.row_stride, e);
-    for (int r = 0; r < a->p && vec; r++) vec = vec16(a->tables[r], a->vocab / a->p + 1, k.table_stride, e);
-    // 4 loads in flight a thread where that still leaves 4 CTAs an SM, else one
-    const size_t count = vec ? a->n_tokens * (a->dim / ve) : a->n_tokens * a->dim;
-    const bool many = count >= (size_t)h->sm_count * 4 * 1024;
-    const size_t ctas = many ? (count + 1023) / 1024 : (count + 255) / 256;
-    if (ctas > 0x7FFFFFFFu) return c.bad("the lookup is too large");
     cudaError_t ce = dispatch_float(a->dtype, [&](auto dt) {
         constexpr int DT = decltype(dt)::value;
         return launch_pdl(vec ? (many ? embedding_kernel<DT, true, 4> : embedding_kernel<DT, true, 1>)

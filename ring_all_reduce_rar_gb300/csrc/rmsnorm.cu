@@ -393,6 +393,7 @@ int add_rmsnorm(rar_ctx *h, const rar_rmsnorm_args *a, cudaStream_t stream) {
     if (a->dim < 1 || a->dim > RAR_NORM_MAX_DIM) return c.bad("dim must be in [1, RAR_NORM_MAX_DIM]");
     if (!(a->eps >= 0.0f)) return c.bad("eps must be at least 0");
     if (a->group % 32) return c.bad("group must be a multiple of 32");
+    if (a->rows > 0x7FFFFFFFu) return c.bad("rows must be at most 2^31 - 1");  // (a CTA a row)
     if (a->rows == 0) return RAR_OK;
     if (!a->parts) return c.bad("parts is NULL");
     if (a->out8 && !a->scales) return c.bad("scales is NULL");
@@ -467,7 +468,6 @@ int add_rmsnorm(rar_ctx *h, const rar_rmsnorm_args *a, cudaStream_t stream) {
     vec = vec && (uintptr_t)k.weight % 16 == 0 &&
           (!k.out8 || ((uintptr_t)k.out8 % ve == 0 && (a->rows <= 1 || (size_t)k.out8_stride % ve == 0)));
     const RowShape shape = row_shape(vec ? a->dim / ve : (a->dim + ve - 1) / ve + 1);
-    if (a->rows > 0x7FFFFFFFu) return c.bad("too many rows");
     cudaError_t ce;
     if ((vec || alike) && shape.v) {
         const size_t gv = group / ve;

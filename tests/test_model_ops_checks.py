@@ -287,3 +287,22 @@ def test_flags_without_a_truth_value(h):  # noqa: F811
                  lambda: h.embedding_grad(x, tok, [x.clone()], accumulate=neither)):
         with pytest.raises(RuntimeError, match="ambiguous"):
             call()
+
+
+@gpu
+def test_a_refused_size_leaves_the_last_call():
+    """Too many rows are an argument error: nothing is enqueued, and status and
+    send counts still belong to the call before.  (One more row than a launch has
+    CTAs; the call is refused on the host.)"""
+    with rar.Handle(0, engine="ring", skip_pointer_check=True) as mine:
+        bufs = [torch.ones(4096, device="cuda") for _ in range(4)]
+        mine.allreduce(bufs)
+        counts = mine.send_counts(4)
+        assert all(counts)
+        a = _ops.RmsNormArgs()
+        ptrs = (ctypes.c_void_p * 4)(*[t.data_ptr() for t in bufs])
+        a.parts, a.p, a.dtype, a.rows, a.dim, a.eps = ctypes.addressof(ptrs), 4, 2, 1 << 31, 1, 1e-6
+        assert rar.load_library().rar_add_rmsnorm(mine.h, ctypes.byref(a), torch.cuda.current_stream().cuda_stream) == 1
+        assert "rows" in rar.rar_last_error(mine.h)
+        assert mine.send_counts(4) == counts
+        mine.check()
