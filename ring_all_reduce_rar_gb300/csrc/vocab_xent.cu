@@ -116,10 +116,11 @@ __device__ __forceinline__ float g_undo(const XentArgs &a) {
     return ldexpf(g_unit(a), -g_exponent<DT>(a));
 }
 
-enum XentMode { XENT_STATS, XENT_G, XENT_DHIDDEN, XENT_DWEIGHT, XENT_STATS_SUMS };  // (the last: see kStepsPerSum)
+enum XentMode { XENT_STATS, XENT_G, XENT_DHIDDEN, XENT_DWEIGHT, XENT_STATS_SUMS, XENT_G_SUMS };  // (_SUMS: see kStepsPerSum)
 template <int MODE>
 struct Mode {
-    static constexpr bool sums = MODE == XENT_STATS_SUMS, stats = MODE == XENT_STATS || sums, logits = stats || MODE == XENT_G;
+    static constexpr bool sums = MODE == XENT_STATS_SUMS || MODE == XENT_G_SUMS;
+    static constexpr bool stats = MODE == XENT_STATS || MODE == XENT_STATS_SUMS, g = MODE == XENT_G || MODE == XENT_G_SUMS, logits = stats || g;
     // whether a row of the operand is a row of K (MN-major); rows of a box; boxes of a stage
     static constexpr bool a_mn = MODE == XENT_DWEIGHT, b_mn = MODE == XENT_DHIDDEN || MODE == XENT_DWEIGHT;
     static constexpr int a_box = a_mn ? 64 : 128, b_box = b_mn ? 64 : 128;
@@ -211,13 +212,15 @@ __device__ __forceinline__ uint4 narrow8_scaled(const float *v, float scale) {
     return narrow8<DT>(f);
 }
 
-// The tensor cores add to a 32-bit accumulator by truncation: over the whole of dim the
-// logits, and with them lse, came out low by some 1e-6 of their size (dim 2048; a rounding
-// sum: 4e-7).  So XENT_STATS_SUMS, for a dim above that of one sum, ends its accumulators every 16
-// steps (1024 of dim) and adds them up in registers: 5e-7.  It costs 8 to 10 % of a long forward
-// pass (2048 tokens by 50021 x 2048 fp16 314 us against 282, 8192 by 65536 x 4096 bf16 2.54 ms
-// against 2.33), 3 % with gradients.  A dim of one sum keeps the plain form and its
-// time.  Products whose results are rounded to 16 bits do without.
+// The tensor cores add to a 32-bit accumulator by truncation: an instruction loses some
+// 1.5 x 2^-23 of it, always towards zero.  Over the whole of dim the logits came out low by some
+// 1e-6 of their size at dim 2048 (a rounding sum: 4e-7), and where all products have one sign
+// by 1e-4 at dim 16384, so that exp(z - lse) with logits near 9000 was off by a factor of 0.4.  So
+// both passes that make logits, for a dim above that of one sum, end their accumulators
+// every 16 steps (1024 of dim) and add them up in registers: 5e-7.  It costs 8 to 10 % of
+// a long forward pass (2048 tokens by 50021 x 2048 fp16 314 us against 282, 8192 by 65536 x 4096
+// bf16 2.54 ms against 2.33), 3 to 4 % with gradients.  A dim of one sum keeps the plain form
+// and its time.  Products whose results are rounded to 16 bits do without.
 constexpr int kStepsPerSum = 16;
 
 // What an epilogue thread keeps of a tile: one row of it.
@@ -226,8 +229,8 @@ struct XentRow {
     bool live;        // the row exists
     int cols;         // columns of its half that exist
     int target;       // column of its target in its half, or one out of range
-    float w, lse;     // XENT_G
-    float max, sum;   // XENT_STATS
+    float w, lse;     // logits for G
+    float max, sum;   // logits for the statistics
     char *out;        // where the row's half begins
     float *part;      // XENT_DHIDDEN: the sums so far
 };
@@ -257,7 +260,7 @@ __device__ __forceinline__ XentRow xent_row(const XentArgs &a, int b0, const Xen
         r.target = y >= 0 && y < r.cols ? (int)y : -1;
         r.max = -INFINITY;
         r.sum = 0.0f;
-        if constexpr (MODE == XENT_G) {
+        if constexpr (Mode<MODE>::g) {
             r.w = r.live ? ldexpf(a.row_weight[row] / g_unit(a), g_exponent<DT>(a)) : 0.0f;
             r.lse = r.live ? a.lse_ws[row] : 0.0f;
             r.out = static_cast<char *>(a.g) + (((long long)row * a.window + it.block) * kBlock + half) * 2;
@@ -295,7 +298,7 @@ __device__ __forceinline__ void xent_columns(const XentArgs &a, XentRow &r, int 
         for (int c = 0; c < 32; c++) s += exp_of(v[c] - ref);
         r.max = m;
         r.sum = s;
-    } else if constexpr (MODE == XENT_G) {
+    } else if constexpr (Mode<MODE>::g) {
         const int y = r.target - c0;
 #pragma unroll
         for (int c = 0; c < 32; c++) {
@@ -796,15 +799,16 @@ int vocab_xent(rar_ctx *h, const rar_vocab_xent_args *a, cudaStream_t stream) {
             }
             return e;
         }
-        e = k.dim > 64 * kStepsPerSum ? launch_tiles<XENT_STATS_SUMS, DT>(h, k, logits, 0, k.n_blocks, stream)
-                                      : launch_tiles<XENT_STATS, DT>(h, k, logits, 0, k.n_blocks, stream);
+        const bool sums = k.dim > 64 * kStepsPerSum;
+        e = sums ? launch_tiles<XENT_STATS_SUMS, DT>(h, k, logits, 0, k.n_blocks, stream)
+                 : launch_tiles<XENT_STATS, DT>(h, k, logits, 0, k.n_blocks, stream);
         const int join = grad ? kJoinTokens<true> : kJoinTokens<false>;
         if (e == cudaSuccess)
             e = launch_pdl(grad ? xent_join_kernel<DT, true> : xent_join_kernel<DT, false>, dim3((unsigned)((k.tokens + join - 1) / join)), dim3(32 * join), 0, stream, k);
         if (!grad) return e;
         for (int b0 = 0; b0 < k.n_blocks && e == cudaSuccess; b0 += k.window) {
             const int nb = std::min(k.window, k.n_blocks - b0);
-            e = launch_tiles<XENT_G, DT>(h, k, logits, b0, nb, stream);
+            e = sums ? launch_tiles<XENT_G_SUMS, DT>(h, k, logits, b0, nb, stream) : launch_tiles<XENT_G, DT>(h, k, logits, b0, nb, stream);
             if (e == cudaSuccess && k.dhidden) {
                 XentArgs kw = k;
                 kw.splits = std::min(k.splits, nb);

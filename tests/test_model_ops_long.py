@@ -4,7 +4,8 @@ against plain forms in 64 bits.  The bounds are those of test_model_ops."""
 import pytest
 import torch
 
-from tests.test_model_ops import DTYPES, F, HALF, check_xent, gen, h, normal, pieces, within, xent_inputs, xent_reference  # noqa: F401
+from tests.test_model_ops import (DTYPES, F, HALF, TINY, U, check_xent, gen, h, normal, pieces, within,  # noqa: F401
+                                  xent_inputs, xent_reference)
 
 pytestmark = pytest.mark.gpu
 
@@ -35,23 +36,49 @@ def test_sums_of_1024(h, dtype, p, tokens, dim, vocab):  # noqa: F811
     check_gradients(h, tokens, dim, vocab, p, dtype)
 
 
-@pytest.mark.parametrize("dtype", HALF)
-@pytest.mark.parametrize("dim", [1032, 16384])
-def test_lse_is_that_of_sums_of_1024(h, dtype, dim):  # noqa: F811
-    """Products that are all positive, so that every cut goes the same way.  An
-    instruction adds 16 products: they are aligned to the largest term and the accumulator is
-    cut to its 24 bits, two errors of up to 2^-23 of the accumulator.  With an accumulator a
-    1024 of dim these are sums over at most 64 prefixes; one accumulator for all of dim
-    16384 would lose some sixteen times that."""
+def positive_inputs(dim, dtype, tokens=40, vocab=300):
+    """(hidden, whole, targets, logits in 64 bits, bound of a logit by sums of 1024):
+    products that are all positive, so that every cut goes the same way.  An instruction
+    adds 16 products: they are aligned to the largest term and the accumulator is cut
+    to its 24 bits, two errors of up to 2^-23 of the accumulator, which here is a
+    prefix of the sum."""
     g = gen(dim)
-    tokens, vocab = 40, 300
     hidden = (0.5 + 0.5 * torch.rand(tokens, dim, generator=g, device="cuda")).to(dtype)
     whole = (0.5 + 0.5 * torch.rand(vocab, dim, generator=g, device="cuda")).to(dtype)
     targets = torch.randint(0, vocab, (tokens,), generator=g, device="cuda")
-    r = h.vocab_xent(hidden, pieces(whole, 2), targets)
     steps = torch.nn.functional.pad(hidden.double()[:, None, :] * whole.double()[None], (0, -dim % 1024)).view(tokens, vocab, -1, 64, 16).sum(-1)
     z, sums = steps.sum((2, 3)), steps.shape[2]
-    dz = (2 * 2.0 ** -23 * steps.cumsum(3).sum((2, 3)) + sums * F * z).amax(1)
+    return hidden, whole, targets, z, (2 * 2.0 ** -23 * steps.cumsum(3).sum((2, 3)) + sums * F * z).amax(1)
+
+
+@pytest.mark.parametrize("dtype", HALF)
+@pytest.mark.parametrize("dim", [1000, 8192, 16384])
+def test_gradients_are_those_of_sums_of_1024(h, dtype, dim):  # noqa: F811
+    """G = softmax - onehot takes an error of the logits as its own relative
+    error: the pass that makes it needs the logits as well as the one that makes lse."""
+    hidden, whole, targets, z, dz = positive_inputs(dim, dtype)
+    tokens, vocab = z.shape
+    r = h.vocab_xent(hidden, pieces(whole, 2), targets, grad=True)
+    lse = torch.logsumexp(z, 1)
+    dlse = dz + 2.0 ** -18 + 4 * F * lse
+    prob = torch.exp(z - lse[:, None])
+    gmat = prob.scatter_add(1, targets[:, None], -torch.ones_like(lse)[:, None])
+    u = U[dtype]
+    dg = torch.expm1(dz + dlse + 2.0 ** -18 + 8 * F * lse)[:, None] * prob + (u + 4 * F) * gmat.abs() + 2.0 ** -37
+    hid, w = hidden.double(), whole.double()
+    for got, ref, mag, err, n in ((r.dhidden, gmat @ w, gmat.abs() @ w, dg @ w, vocab),
+                                  (torch.cat(r.dweights), gmat.T @ hid, gmat.abs().T @ hid, dg.T @ hid, tokens)):
+        err = err + 2 * (n + 8) * F * mag
+        within(got, ref, err + u * (ref.abs() + err) + TINY[dtype], "gradient")
+
+
+@pytest.mark.parametrize("dtype", HALF)
+@pytest.mark.parametrize("dim", [1032, 16384])
+def test_lse_is_that_of_sums_of_1024(h, dtype, dim):  # noqa: F811
+    """With an accumulator a 1024 of dim a logit's error is a sum over at most 64
+    prefixes; one accumulator for all of dim 16384 would lose some sixteen times that."""
+    hidden, whole, targets, z, dz = positive_inputs(dim, dtype)
+    r = h.vocab_xent(hidden, pieces(whole, 2), targets)
     lse = torch.logsumexp(z, 1)
     # exponentials, their sum, and the rounding of lse itself
     dlse = dz + 2.0 ** -18 + 4 * F * lse
