@@ -499,9 +499,11 @@ typedef struct {
 int rar_embedding(rar_handle h, const rar_embedding_args *a, void *stream);
 
 /* Gradient of rar_embedding for the table, dtables[v] = scale x sum of dout[t]
- * over the t with tokens[t] = v: the tokens are sorted and each row's gradients
- * added in the order of t in 32 bits.  accumulate: added to what dtables holds (rows
- * without a token stay untouched); otherwise every row is written. */
+ * over the t with tokens[t] = v.  The tokens are sorted by index and cut into chunks of
+ * 16 places or more; a row's gradients are added in 32 bits, in the order of t within a
+ * chunk, and the sums of a token that lies in several chunks in an order that the
+ * sizes decide.  accumulate: added to what dtables holds (rows without a token stay
+ * untouched); otherwise every row is written. */
 typedef struct {
     const void *dout;          /* n_tokens x dim */
     size_t dout_stride;

@@ -2,8 +2,8 @@
 // gradient (rar_embedding, rar_embedding_grad).
 //
 //   out[t] = scale table[tokens[t]]
-//   dtables[v] = scale sum over the t with tokens[t] = v, in the order of t,
-//                of dout[t]   (+ what dtables[v] held, with accumulate)
+//   dtables[v] = scale sum over the t with tokens[t] = v of dout[t]
+//                (+ what dtables[v] held, with accumulate), in a fixed order
 //
 // Bound by memory: a read and a write an element.
 #include <algorithm>
@@ -89,7 +89,8 @@ __global__ void __launch_bounds__(256) embedding_kernel(const __grid_constant__ 
 // 2. The sorted places are cut into chunks.  A CTA adds up the runs of its chunk in
 //    order; a run inside the chunk is written to the table, one that goes
 //    on beyond it into the workspace.
-// 3. Runs over several chunks are joined, chunk by chunk.
+// 3. Runs over several chunks are joined: groups of threads add every groups-th
+//    chunk, and then the groups' sums in order.
 // So a frequent token costs no more than others, and no sum depends on timing.
 
 struct SortArgs {

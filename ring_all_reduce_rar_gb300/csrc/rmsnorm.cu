@@ -6,7 +6,8 @@
 //
 // Bound by memory: (p + 1) reads and 2 writes an element against p + 6
 // operations.  Few rows are bound by latency: 4 rows of 2048 with 8 parts and 8-bit output
-// take 6 us, and 10.6 a call in a stream of calls, which is the host's time for one.
+// take 6 us, and a call in a stream of calls 11.7, or 10.4 without the check of its pointers, which is
+// the host's time for one.
 #include "rmsnorm.cuh"
 
 namespace rar {

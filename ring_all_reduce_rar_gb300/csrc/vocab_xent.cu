@@ -17,10 +17,11 @@
 // type of the products that it enters: an error of half a unit in its last place, of the
 // size that rounding dhidden and dweights has anyway.
 //
-// Bound by the tensor cores for many tokens (8 tokens x vocab x dim
-// operations against 6 if the logits were kept): 8192 tokens by 65536 x 4096 bf16 run at 1.73
-// PFLOP/s forward and take 11.0 ms with gradients (1.6).  By memory and latency
-// for few: 16 by 32768 x 2048 40 us (134 MB of weights, 3.4 TB/s).
+// Bound by the tensor cores for many tokens (8 tokens x vocab x dim operations
+// against 6 if the logits were kept): 8192 tokens by 65536 x 4096 bf16 take 2.5 ms forward
+// (1.76 PFLOP/s; 2.7 ms back to back) and 11.4 ms with gradients (1.54 PFLOP/s) at the power
+// limit (1.37 kW, which leaves 1725 of 2070 MHz).  For few tokens by the fill of full tiles in two
+// uneven waves: 16 by 32768 x 2048 take 38 us, as 256 do (134 MB of weights, 3.5 TB/s).
 #include <algorithm>
 
 #include "op_host.h"
@@ -198,7 +199,10 @@ __device__ __forceinline__ bool xent_steps(const XentArgs &a, int b0, const Xent
     return true;
 }
 
-__device__ __forceinline__ float exp_of(float x) {  // ex2.approx: 2 units in the last place
+// Good to (2 + |x|) 2^-23: ex2.approx to 2 units in the last place, the rounding of its argument
+// to |x| 2^-24 and a little for the constant.  A large |x| has a weight of exp(-|x|) in the sums
+// of exponentials, and in G, which is rounded to 8 or 11 bits, no relative error of its size shows.
+__device__ __forceinline__ float exp_of(float x) {
     float r;
     asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x * 1.4426950408889634f));
     return r;
@@ -521,7 +525,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(152)
 // in dweights' sum).  Without gradients a CTA is small enough to stand beside one of
 // the tile kernel and wait there for its end: 256 tokens by 32768 x 2048 took 37 us
 // so and 48 us with 8 tokens a CTA; with gradients 8 tokens, whose loads are in flight
-// together, took 262 us of a whole call against 281 (1024 by 32000 x 1024).
+// together, took 262 us of a whole call against 281 (1024 by 32000 x 1024; the call takes 230 now).
 template <bool GRAD>
 constexpr int kJoinTokens = GRAD ? 8 : 4;
 template <int DT, bool GRAD>
