@@ -125,9 +125,10 @@ typedef struct {
     int channels;                  /* ring engines: CTAs per rank, 0 = chosen from the SM count */
     int slice_elems;               /* ring engines: elements per pipelined slice, 0 = auto */
     int block_threads;             /* threads per CTA (multiple of 32, <= 1024), 0 = auto */
-    unsigned long long timeout_ns; /* bound on every wait of the ring and tree engines and
-                                      of the fused engine's streaming path (a bulk load
-                                      that does not arrive); 0 = 2 s; nonzero values
+    unsigned long long timeout_ns; /* bound on every wait of the ring and tree engines, of
+                                      the fused engine's streaming path (a bulk load
+                                      that does not arrive) and of the model operators;
+                                      0 = 2 s; nonzero values
                                       below 1 ms (1000000) are refused with RAR_EINVAL.
                                       A wait that runs out ends the call with
                                       RAR_ETIMEOUT (rar_status); the streaming path
