@@ -5,7 +5,9 @@ The functions check their tensors, allocate results and workspaces with
 torch's caching allocator on the stream that the call runs on, and call the C
 functions: that part is the compiled module _torch_ops (csrc/torch_ops.cpp),
 which is built with the library; there is no other path.  Tensors that a call
-takes must be ready on its stream, as for every call of this package.
+takes must be ready on its stream, as for every call of this package; `stream`
+is a torch stream or an integer of the tensors' device.  Matrices have
+contiguous rows that do not overlap: an expanded one has to be copied first.
 
 The ctypes structures below mirror the C ones, for callers with results of
 their own: load_library().rar_add_rmsnorm(handle, ctypes.byref(args), stream).
