@@ -140,7 +140,8 @@ typedef struct {
                                       the loads of rank fault_rank are never issued, as
                                       if that rank had died, and in the same way in
                                       rar_add_rmsnorm and its gradient, for many rows,
-                                      and rar_vocab_xent (fault_rank: a piece) */
+                                      rar_vocab_xent, rar_vocab_logprobs and its gradient
+                                      (fault_rank: a piece) */
     int fault_rank;                /* rank the fault applies to (rar_add_rmsnorm_grad: 0 dout,
                                       1 sum, 2 dsum) */
     unsigned fault_delay_ns;       /* RAR_FAULT_DELAY: pause before each slice */
@@ -348,12 +349,13 @@ int rar_debug_set_epoch(rar_handle h, unsigned epoch);
 /* ---------------------------------------------------------------------------
  * Operators of a tensor-parallel language model.
  *
- * Such a model meets the reduction over its p ranks in three places: the
+ * Such a model meets the reduction over its p ranks in several places: the
  * residual stream joins the sum of the ranks' partial outputs and is
  * normalised (rar_add_rmsnorm); the output layer's vocabulary is cut into one
- * piece per rank, over which the softmax is reduced (rar_vocab_xent); and the
- * input table is cut the same way (rar_embedding).  The source pages have no
- * such calls.  Here the reduction is part of the operator, and what every rank
+ * piece per rank, over which the softmax is reduced (rar_vocab_xent,
+ * rar_vocab_logprobs); the input table is cut the same way (rar_embedding); and
+ * all ranks' gradients have one norm (rar_grad_norm, rar_grad_clip).  The source
+ * pages have no such calls.  Here the reduction is part of the operator, and what every rank
  * would hold afterwards is written once, since the ranks share one memory.
  *
  * Conventions of these calls, beyond those at the top of this file:
@@ -524,6 +526,113 @@ typedef struct {
 
 size_t rar_embedding_grad_workspace(size_t n_tokens, size_t vocab, size_t dim);
 int rar_embedding_grad(rar_handle h, const rar_embedding_grad_args *a, void *stream);
+
+/* What the model answers with, from the hidden states and the pieces of
+ * rar_vocab_xent: with z = hidden W^T and l = logit_scale z (1 / temperature),
+ *   lse = log sum exp(l),  logprob = l[target] - lse,
+ *   entropy = lse - sum exp(l - lse) l,
+ * and the `top` largest logits of each token, in falling order, equal ones from
+ * the lowest index on, with their log probabilities.  A token whose target is left out has
+ * logprob 0; its entropy, lse and alternatives are computed.  A logit of NaN or
+ * -infinity is no alternative: where fewer than `top` are left, the rest have
+ * index -1 and log probability -infinity.
+ * dtype, dim, alignment, strides and p as in rar_vocab_xent. */
+#define RAR_LOGPROBS_MAX_TOP 32
+
+typedef struct {
+    const void *hidden;         /* tokens x dim */
+    size_t hidden_stride;
+    const void *const *weights; /* host array of p pieces, rows x dim */
+    size_t weight_stride;       /* of every piece */
+    int p;
+    int dtype;
+    size_t tokens, dim, vocab;  /* tokens may be 0, dim and vocab at least 1 */
+    const void *targets;        /* tokens indices */
+    int index_bytes;
+    float logit_scale;          /* positive and finite */
+    int top;                    /* 0 .. RAR_LOGPROBS_MAX_TOP, at most vocab */
+    float *logprob;             /* out: tokens, or NULL */
+    float *entropy;             /* out: tokens, or NULL */
+    float *lse;                 /* out: tokens, or NULL */
+    float *top_logprob;         /* out: tokens x top */
+    long long *top_token;       /* out: tokens x top */
+    void *workspace;
+    size_t workspace_bytes;
+} rar_vocab_logprobs_args;
+
+/* 0 where the sizes are refused. */
+size_t rar_vocab_logprobs_workspace(size_t tokens, size_t dim, size_t vocab, int p, int top);
+int rar_vocab_logprobs(rar_handle h, const rar_vocab_logprobs_args *a, void *stream);
+
+/* Gradients of rar_vocab_logprobs, from those of logprob (a) and entropy (b):
+ *   G = logit_scale (a onehot(target) - q (a + b (log q + entropy))),
+ *   q = exp(l - lse),  dhidden = G W,  dweights = G^T hidden,
+ * with lse and entropy as the call above gave them.  A token whose target is
+ * left out, or with a = b = 0, has no part in them, whatever its hidden state holds.
+ * G is held in the dtype for a window of the vocabulary at a time. */
+typedef struct {
+    const void *hidden;         /* as in rar_vocab_logprobs_args, down to logit_scale */
+    size_t hidden_stride;
+    const void *const *weights;
+    size_t weight_stride;
+    int p;
+    int dtype;
+    size_t tokens, dim, vocab;
+    const void *targets;
+    int index_bytes;
+    float logit_scale;
+    const float *lse;           /* tokens */
+    const float *entropy;       /* tokens; needed with dentropy */
+    const float *dlogprob;      /* tokens, or NULL: zeros */
+    const float *dentropy;      /* tokens, or NULL: zeros; one of the two is needed */
+    void *dhidden;              /* out: tokens x dim, or NULL */
+    size_t dhidden_stride;
+    void *const *dweights;      /* out: host array of p pieces, or NULL */
+    size_t dweight_stride;
+    void *workspace;
+    size_t workspace_bytes;
+} rar_vocab_logprobs_grad_args;
+
+size_t rar_vocab_logprobs_grad_workspace(size_t tokens, size_t dim, size_t vocab, int p);
+int rar_vocab_logprobs_grad(rar_handle h, const rar_vocab_logprobs_grad_args *a, void *stream);
+
+/* A matrix in a list of tensors; a tensor without gaps, of any shape, is one of one row. */
+typedef struct {
+    void *data;
+    int dtype;         /* RAR_FLOAT32, RAR_BFLOAT16 or RAR_FLOAT16, each its own */
+    size_t rows, cols; /* 0 of either: an empty tensor */
+    size_t stride;     /* between rows, in elements; 0: packed */
+} rar_tensor;
+
+/* norms[i] = sqrt(sum x^2) over tensor i, norm = sqrt(sum norms^2): the norm of all
+ * ranks' gradients together.  Any values of the tensors' types are squared without
+ * overflow or loss; a norm beyond binary32 is infinity.  A tensor given twice counts twice. */
+typedef struct {
+    const rar_tensor *tensors; /* host array */
+    size_t n;                  /* may be 0 (norm 0); at most 2^24, with 2^40 elements in all */
+    float *norm;               /* out: one value, or NULL */
+    float *norms;              /* out: n, or NULL; one of the two is needed */
+    void *workspace;
+    size_t workspace_bytes;
+} rar_grad_norm_args;
+
+size_t rar_grad_norm_workspace(const rar_tensor *tensors, size_t n);
+int rar_grad_norm(rar_handle h, const rar_grad_norm_args *a, void *stream);
+
+/* x * f for every element, f = max_norm / (norm + eps) where that is below 1, else 1:
+ * gradients clipped to a largest norm.  A norm that is NaN, or infinite, gives what the
+ * formula gives (NaN; 0, and NaN for infinite elements): the caller may look at it first.
+ * Tensors that are scaled where they lie must not overlap. */
+typedef struct {
+    const rar_tensor *tensors; /* host array */
+    size_t n;
+    const rar_tensor *out;     /* host array of the same sizes, each of its tensor's dtype or RAR_FLOAT32
+                                  and its tensor itself or apart from all of them; NULL: in place */
+    const float *norm;         /* device memory: as rar_grad_norm gave it */
+    float max_norm, eps;       /* finite, not negative */
+} rar_grad_clip_args;
+
+int rar_grad_clip(rar_handle h, const rar_grad_clip_args *a, void *stream);
 
 #ifdef __cplusplus
 }

@@ -10,6 +10,8 @@ over device pointers and streams.
         x = h.embedding(tables, tokens)    # a table in p pieces
         r = h.add_rmsnorm(parts, weight, residual=x)     # p ranks' partial results
         y = h.vocab_xent(r.out, pieces, targets, grad=True)  # a vocabulary in p pieces
+        s = h.vocab_logprobs(r.out, pieces, tokens, top=5)   # what the model answers with
+        h.grad_clip(grads, max_norm=1.0)                     # all ranks' gradients
 """
 from ._abi import (DTYPE_CODES, ENGINE_CODES, FAULT_CODES, OP_CODES, RAR_MAX_P, STATUS_NAMES, Handle, Options,
                    RarError, library_path, load_library, make_options, rar_all_gather, rar_allreduce,
@@ -18,7 +20,8 @@ from ._abi import (DTYPE_CODES, ENGINE_CODES, FAULT_CODES, OP_CODES, RAR_MAX_P, 
                    rar_init, rar_last_error, rar_reduce_scatter, rar_send_counts, rar_set_options, rar_status,
                    rar_trace, rar_version)
 from ._build import build
-from ._ops import (AddRmsNorm, VocabXent, rar_add_rmsnorm, rar_add_rmsnorm_grad, rar_embedding, rar_embedding_grad,
+from ._ops import (AddRmsNorm, GradNorm, VocabLogprobs, VocabXent, rar_add_rmsnorm, rar_add_rmsnorm_grad, rar_embedding,
+                   rar_embedding_grad, rar_grad_clip, rar_grad_norm, rar_vocab_logprobs, rar_vocab_logprobs_grad,
                    rar_vocab_xent)
 
 __all__ = [
@@ -28,5 +31,6 @@ __all__ = [
     "rar_destroy",
     "rar_init", "rar_last_error", "rar_reduce_scatter", "rar_send_counts", "rar_set_options", "rar_status",
     "rar_trace", "rar_version", "rar_add_rmsnorm", "rar_add_rmsnorm_grad", "rar_embedding", "rar_embedding_grad",
-    "rar_vocab_xent",
+    "rar_vocab_xent", "GradNorm", "VocabLogprobs", "rar_grad_clip", "rar_grad_norm", "rar_vocab_logprobs",
+    "rar_vocab_logprobs_grad",
 ]

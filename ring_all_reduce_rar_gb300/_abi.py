@@ -325,6 +325,18 @@ class Handle:
     def embedding_grad(self, dout, tokens, dtables, **kw):
         return _ops.rar_embedding_grad(self.h, dout, tokens, dtables, **kw)
 
+    def vocab_logprobs(self, hidden, weights, targets, **kw):
+        return _ops.rar_vocab_logprobs(self.h, hidden, weights, targets, **kw)
+
+    def vocab_logprobs_grad(self, hidden, weights, targets, lse, entropy=None, dlogprob=None, **kw):
+        return _ops.rar_vocab_logprobs_grad(self.h, hidden, weights, targets, lse, entropy, dlogprob, **kw)
+
+    def grad_norm(self, tensors, **kw):
+        return _ops.rar_grad_norm(self.h, tensors, **kw)
+
+    def grad_clip(self, tensors, max_norm, **kw):
+        return _ops.rar_grad_clip(self.h, tensors, max_norm, **kw)
+
     def status(self) -> int:
         return rar_status(self.h)
 

@@ -1,5 +1,6 @@
 """Python binding of the model operators in include/rar.h (rar_add_rmsnorm,
-rar_vocab_xent, rar_embedding and their gradients).
+rar_vocab_xent, rar_vocab_logprobs, rar_embedding and their gradients,
+rar_grad_norm, rar_grad_clip).
 
 The functions check their tensors, allocate results and workspaces with
 torch's caching allocator on the stream that the call runs on, and call the C
@@ -63,6 +64,38 @@ class EmbeddingGradArgs(ctypes.Structure):
                 ("scale", _f32), ("accumulate", _i32), ("workspace", _vp), ("workspace_bytes", _sz)]
 
 
+class VocabLogprobsArgs(ctypes.Structure):
+    """rar_vocab_logprobs_args."""
+    _fields_ = [("hidden", _vp), ("hidden_stride", _sz), ("weights", _vp), ("weight_stride", _sz), ("p", _i32),
+                ("dtype", _i32), ("tokens", _sz), ("dim", _sz), ("vocab", _sz), ("targets", _vp), ("index_bytes", _i32),
+                ("logit_scale", _f32), ("top", _i32), ("logprob", _vp), ("entropy", _vp), ("lse", _vp),
+                ("top_logprob", _vp), ("top_token", _vp), ("workspace", _vp), ("workspace_bytes", _sz)]
+
+
+class VocabLogprobsGradArgs(ctypes.Structure):
+    """rar_vocab_logprobs_grad_args."""
+    _fields_ = [("hidden", _vp), ("hidden_stride", _sz), ("weights", _vp), ("weight_stride", _sz), ("p", _i32),
+                ("dtype", _i32), ("tokens", _sz), ("dim", _sz), ("vocab", _sz), ("targets", _vp), ("index_bytes", _i32),
+                ("logit_scale", _f32), ("lse", _vp), ("entropy", _vp), ("dlogprob", _vp), ("dentropy", _vp),
+                ("dhidden", _vp), ("dhidden_stride", _sz), ("dweights", _vp), ("dweight_stride", _sz),
+                ("workspace", _vp), ("workspace_bytes", _sz)]
+
+
+class Tensor(ctypes.Structure):
+    """rar_tensor."""
+    _fields_ = [("data", _vp), ("dtype", _i32), ("rows", _sz), ("cols", _sz), ("stride", _sz)]
+
+
+class GradNormArgs(ctypes.Structure):
+    """rar_grad_norm_args."""
+    _fields_ = [("tensors", _vp), ("n", _sz), ("norm", _vp), ("norms", _vp), ("workspace", _vp), ("workspace_bytes", _sz)]
+
+
+class GradClipArgs(ctypes.Structure):
+    """rar_grad_clip_args."""
+    _fields_ = [("tensors", _vp), ("n", _sz), ("out", _vp), ("norm", _vp), ("max_norm", _f32), ("eps", _f32)]
+
+
 class AddRmsNorm(NamedTuple):
     """Results of add_rmsnorm; those that were not asked for are None."""
     sum: torch.Tensor
@@ -80,15 +113,34 @@ class VocabXent(NamedTuple):
     dweights: Optional[list]
 
 
+class VocabLogprobs(NamedTuple):
+    """Results of vocab_logprobs; the alternatives are None unless asked for."""
+    logprob: torch.Tensor
+    entropy: torch.Tensor
+    lse: torch.Tensor
+    top_logprob: Optional[torch.Tensor]
+    top_token: Optional[torch.Tensor]
+
+
+class GradNorm(NamedTuple):
+    """Results of grad_norm: of all tensors together, and of each."""
+    norm: torch.Tensor
+    norms: torch.Tensor
+
+
 def declare(lib) -> None:
     """Argument types of the operators' C functions."""
-    for name in ("rar_add_rmsnorm", "rar_add_rmsnorm_grad", "rar_vocab_xent", "rar_embedding", "rar_embedding_grad"):
+    for name in ("rar_add_rmsnorm", "rar_add_rmsnorm_grad", "rar_vocab_xent", "rar_embedding", "rar_embedding_grad",
+                 "rar_vocab_logprobs", "rar_vocab_logprobs_grad", "rar_grad_norm", "rar_grad_clip"):
         f = getattr(lib, name)
         f.argtypes = [_vp, _vp, _vp]
         f.restype = _i32
     for name, argtypes in (("rar_add_rmsnorm_grad_workspace", [_sz, _sz]),
                            ("rar_vocab_xent_workspace", [_sz, _sz, _sz, _i32, _i32]),
-                           ("rar_embedding_grad_workspace", [_sz, _sz, _sz])):
+                           ("rar_embedding_grad_workspace", [_sz, _sz, _sz]),
+                           ("rar_vocab_logprobs_workspace", [_sz, _sz, _sz, _i32, _i32]),
+                           ("rar_vocab_logprobs_grad_workspace", [_sz, _sz, _sz, _i32]),
+                           ("rar_grad_norm_workspace", [_vp, _sz])):
         f = getattr(lib, name)
         f.argtypes = argtypes
         f.restype = _sz
@@ -169,3 +221,37 @@ def rar_embedding_grad(handle, dout, tokens, dtables, scale=1.0, accumulate=Fals
     added to them with accumulate=True, else written whole.  Returns dtables."""
     _run(handle, stream, _module().embedding_grad, dout, tokens, dtables, scale, accumulate)
     return dtables
+
+
+def rar_vocab_logprobs(handle, hidden, weights, targets, top=0, logit_scale=1.0, stream=None) -> VocabLogprobs:
+    """Log probabilities of `targets`, entropy and log sum exp of each token's
+    distribution, with the logits hidden W^T scaled by logit_scale (1 /
+    temperature), over a vocabulary in p pieces (see rar_vocab_logprobs in
+    rar.h).  top > 0 (at most 32): also the `top` most likely tokens (int64)
+    in falling order, the lowest first among equal ones, and their log
+    probabilities.  A target outside the vocabulary has log probability 0."""
+    return VocabLogprobs._make(_run(handle, stream, _module().vocab_logprobs, hidden, weights, targets, top, logit_scale))
+
+
+def rar_vocab_logprobs_grad(handle, hidden, weights, targets, lse, entropy=None, dlogprob=None, dentropy=None,
+                            logit_scale=1.0, stream=None):
+    """(dhidden, dweights) of rar_vocab_logprobs from the gradients of its
+    log probabilities and entropies (float32 vectors; None: zeros).  lse and
+    entropy are its results; entropy is needed with dentropy."""
+    return _run(handle, stream, _module().vocab_logprobs_grad, hidden, weights, targets, lse, entropy, dlogprob, dentropy,
+                logit_scale)
+
+
+def rar_grad_norm(handle, tensors, stream=None) -> GradNorm:
+    """The norm of all tensors together (float32, no dimensions) and of each
+    (see rar_grad_norm in rar.h).  The tensors may differ in shape and dtype;
+    each has no gaps, or is a matrix with contiguous rows."""
+    return GradNorm._make(_run(handle, stream, _module().grad_norm, tensors))
+
+
+def rar_grad_clip(handle, tensors, max_norm, norm=None, out=None, eps=1e-6, stream=None):
+    """Scales the tensors by max_norm / (norm + eps) where that is below 1
+    (see rar_grad_clip in rar.h): in place, or into `out`, tensors of the same
+    shapes, each of its tensor's dtype or float32.  norm: their norm, a float32
+    tensor of one value, where it is known.  Returns the norm."""
+    return _run(handle, stream, _module().grad_clip, tensors, max_norm, norm, out, eps)[0]

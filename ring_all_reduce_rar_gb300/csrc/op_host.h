@@ -4,6 +4,7 @@
 // C++ exceptions into status codes.
 #pragma once
 
+#include <algorithm>
 #include <cstdint>
 #include <exception>
 #include <new>
@@ -98,6 +99,30 @@ class OpCheck {
             for (const MatrixSpan &in : inputs_)
                 if (spans_meet(outputs_[i], in) && !(outputs_[i].same_as(in) && in_place(outputs_[i], in)))
                     return bad(std::string(outputs_[i].name) + " and " + in.name + " overlap");
+        }
+        return RAR_OK;
+    }
+
+    // A list of matrices that are read, each written to `outs` at the same place of that list
+    // (NULL: where it lies, and it may be its own output there), and one more input.  In the order of
+    // their addresses: only those whose extents overlap are compared.
+    int list_overlaps(const std::vector<MatrixSpan> &ins, const std::vector<MatrixSpan> *outs, const MatrixSpan &also) {
+        struct Item { const MatrixSpan *s; size_t at; bool out; };
+        std::vector<Item> items, open;
+        items.reserve(ins.size() * (outs ? 2 : 1) + 1);
+        for (size_t i = 0; i < ins.size(); i++) items.push_back({&ins[i], i, !outs});
+        for (size_t i = 0; outs && i < outs->size(); i++) items.push_back({&(*outs)[i], i, true});
+        items.push_back({&also, ins.size(), false});
+        std::sort(items.begin(), items.end(), [](const Item &a, const Item &b) { return a.s->base < b.s->base; });
+        for (const Item &x : items) {
+            size_t kept = 0;
+            for (const Item &y : open)
+                if (y.s->base + y.s->extent() > x.s->base) open[kept++] = y;
+            open.resize(kept);
+            for (const Item &y : open)
+                if ((x.out || y.out) && spans_meet(*x.s, *y.s) && !(x.at == y.at && x.out != y.out && x.s->same_as(*y.s)))
+                    return bad(std::string(x.s->name) + " and " + (x.s->name == y.s->name ? "another" : y.s->name) + " overlap");
+            open.push_back(x);
         }
         return RAR_OK;
     }

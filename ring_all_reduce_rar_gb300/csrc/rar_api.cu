@@ -757,7 +757,7 @@ int rar_status(rar_handle h) {
                           st.rank, st.step, st.slice, st.waited_on, st.flag_seen, st.flag_wanted);
         else if (st.rank <= -2)  // (WAIT_OF_XENT, WAIT_OF_NORM)
             std::snprintf(buf, sizeof(buf), "%s wait timed out: CTA %d, role %d (%s)", st.rank == -2 ? "tile" : "row", st.slice, st.step,
-                          st.rank == -2 ? "vocabulary cross entropy" : "residual norm");
+                          st.rank == -2 ? "vocabulary cross entropy or log probabilities" : "residual norm");
         else
             std::snprintf(buf, sizeof(buf),
                           "bulk-copy wait timed out: tile %d, step %d, waiting for rank %d's tile (fused streaming "

@@ -31,19 +31,22 @@ const Tensor &tensor(const std::string &name, PyObject *o) {
     return THPVariable_Unpack(o);
 }
 
+int code_of(at::ScalarType dtype) {
+    switch (dtype) {
+    case at::kInt: return RAR_INT32;
+    case at::kFloat: return RAR_FLOAT32;
+    case at::kBFloat16: return RAR_BFLOAT16;
+    case at::kHalf: return RAR_FLOAT16;
+    default: refuse(std::string("unsupported dtype ") + c10::toString(dtype));
+    }
+}
+
 // What a call's matrices share.
 struct Common {
     at::ScalarType dtype;
     int code;
     at::Device device;
-    Common(const char *name, const Tensor &t) : dtype(t.scalar_type()), device(t.device()) {
-        switch (dtype) {
-        case at::kInt: code = RAR_INT32; break;
-        case at::kFloat: code = RAR_FLOAT32; break;
-        case at::kBFloat16: code = RAR_BFLOAT16; break;
-        case at::kHalf: code = RAR_FLOAT16; break;
-        default: refuse(std::string("unsupported dtype ") + c10::toString(dtype));
-        }
+    Common(const char *name, const Tensor &t) : dtype(t.scalar_type()), code(code_of(dtype)), device(t.device()) {
         if (!device.is_cuda()) refuse(std::string(name) + " must be a CUDA tensor");
         if (t.dim() != 2) refuse(std::string(name) + " must have two dimensions");
     }
@@ -113,7 +116,50 @@ struct Pieces : Matrices {
     }
 };
 
-void *stream_of(const Common &c) { return c10::cuda::getCurrentCUDAStream(c.device.index()).stream(); }
+void *stream_of(const at::Device &device) { return c10::cuda::getCurrentCUDAStream(device.index()).stream(); }
+void *stream_of(const Common &c) { return stream_of(c.device); }
+
+// Places of a list of tensors of any shape.  One without gaps is a single row (its elements
+// in the order of memory); any other must be a matrix with contiguous rows that do not overlap.
+// `like`: tensors of the same shapes, element by element.
+struct Tensors {
+    std::vector<rar_tensor> at;
+    at::Device device;
+    Tensors(const std::string &name, const std::vector<const Tensor *> &v, const std::vector<const Tensor *> *like = nullptr) : device(v[0]->device()) {
+        if (!device.is_cuda()) refuse(name + " must be a CUDA tensor");
+        if (like && like->size() != v.size()) refuse(name + ": one for each tensor");
+        at.reserve(v.size());
+        for (size_t i = 0; i < v.size(); i++) {
+            const Tensor &t = *v[i];
+            if (t.device() != device) refuse(name + ": all of them must be on " + device.str());
+            if (!t.defined() || t.layout() != at::kStrided) refuse(name + " must be a dense tensor");
+            rar_tensor r{};
+            r.dtype = code_of(t.scalar_type());
+            r.data = t.data_ptr();
+            bool whole = t.is_non_overlapping_and_dense();
+            if (like) {
+                const Tensor &o = *(*like)[i];
+                if (t.sizes() != o.sizes()) refuse(name + " must have its tensor's shape");
+                if (t.device() != o.device()) refuse(name + " must be on its tensor's device");
+                whole = whole && o.is_non_overlapping_and_dense();
+                for (int64_t d = 0; whole && d < t.dim(); d++) whole = t.size(d) <= 1 || t.stride(d) == o.stride(d);
+            }
+            if (t.numel() == 0) {
+                r.rows = r.cols = 0;
+            } else if (whole) {
+                r.rows = 1;
+                r.cols = (size_t)t.numel();
+            } else {
+                if (t.dim() != 2 || (t.size(1) > 1 && t.stride(1) != 1) || (t.size(0) > 1 && t.stride(0) < t.size(1)))
+                    refuse(name + " must have no gaps, or be a matrix with contiguous rows that do not overlap" + (like ? ", as its tensor has them" : ""));
+                r.rows = (size_t)t.size(0);
+                r.cols = (size_t)t.size(1);
+                r.stride = (size_t)(t.size(0) > 1 ? t.stride(0) : t.size(1));
+            }
+            at.push_back(r);
+        }
+    }
+};
 
 PyObject *tuple(std::initializer_list<Tensor> ts) {
     PyObject *t = PyTuple_New((Py_ssize_t)ts.size());
@@ -128,6 +174,24 @@ PyObject *tuple(std::initializer_list<Tensor> ts) {
         PyTuple_SET_ITEM(t, i++, o);
     }
     return t;
+}
+
+// (first, list of others)
+PyObject *with_list(const Tensor &first, const std::vector<Tensor> &others) {
+    PyObject *r = tuple({first, Tensor()});
+    PyObject *l = r ? PyList_New((Py_ssize_t)others.size()) : nullptr;
+    for (size_t i = 0; l && i < others.size(); i++) {
+        PyObject *o = THPVariable_Wrap(others[i]);
+        if (!o) Py_CLEAR(l);
+        else PyList_SET_ITEM(l, (Py_ssize_t)i, o);
+    }
+    if (!l) {
+        Py_XDECREF(r);
+        return nullptr;
+    }
+    Py_DECREF(PyTuple_GET_ITEM(r, 1));
+    PyTuple_SET_ITEM(r, 1, l);
+    return r;
 }
 
 // Runs `body`, whose exceptions become Python's.
@@ -343,9 +407,159 @@ PyObject *embedding_grad(PyObject *, PyObject *const *args, Py_ssize_t nargs) {
     });
 }
 
+// What the two calls on log probabilities share.
+template <typename Args>
+Pieces logprob_inputs(Args &a, const Tensor &hidden, const Tensor &targets, const std::vector<const Tensor *> &weights, PyObject *scale, const Common &c) {
+    Pieces w("a weight piece", weights, c);
+    const int64_t tokens = hidden.size(0);
+    a.hidden_stride = matrix("hidden", hidden, tokens, w.dim, c);
+    a.hidden = hidden.data_ptr();
+    a.weight_stride = w.stride;
+    a.p = (int)w.p;
+    a.dtype = c.code;
+    a.tokens = (size_t)tokens;
+    a.dim = (size_t)w.dim;
+    a.vocab = (size_t)w.vocab;
+    a.index_bytes = indices("targets", targets, tokens, c);
+    a.targets = targets.data_ptr();
+    a.logit_scale = (float)PyFloat_AsDouble(scale);
+    return w;
+}
+
+// (handle, hidden, weights, targets, top, logit_scale) -> (logprob, entropy, lse, top_logprob, top_token)
+PyObject *vocab_logprobs(PyObject *, PyObject *const *args, Py_ssize_t nargs) {
+    return call(nargs, 6, [&]() -> PyObject * {
+        const Tensor &hidden = tensor("hidden", args[1]), &targets = tensor("targets", args[3]);
+        const auto weights = list("weights", args[2]);
+        const Common c("hidden", hidden);
+        rar_vocab_logprobs_args a{};
+        const Pieces w = logprob_inputs(a, hidden, targets, weights, args[5], c);
+        const int64_t tokens = hidden.size(0), top = PyLong_AsLongLong(args[4]);
+        if (PyErr_Occurred()) return nullptr;
+        if (top < 0 || top > RAR_LOGPROBS_MAX_TOP || top > w.vocab) refuse("top must be in [0, 32] and at most the vocabulary");
+        a.weights = w.ptr.data();
+        a.top = (int)top;
+        a.workspace_bytes = rar_vocab_logprobs_workspace(a.tokens, a.dim, a.vocab, a.p, a.top);
+        Tensor logprob = c.make({tokens}, at::kFloat), entropy = c.make({tokens}, at::kFloat), lse = c.make({tokens}, at::kFloat), ws = c.bytes(a.workspace_bytes);
+        Tensor top_logprob, top_token;
+        a.logprob = (float *)logprob.data_ptr();
+        a.entropy = (float *)entropy.data_ptr();
+        a.lse = (float *)lse.data_ptr();
+        a.workspace = ws.data_ptr();
+        if (top) {
+            top_logprob = c.make({tokens, top}, at::kFloat);
+            top_token = c.make({tokens, top}, at::kLong);
+            a.top_logprob = (float *)top_logprob.data_ptr();
+            a.top_token = (long long *)top_token.data_ptr();
+        }
+        const int rc = rar_vocab_logprobs(handle(args[0]), &a, stream_of(c));
+        return rc ? PyLong_FromLong(rc) : tuple({logprob, entropy, lse, top_logprob, top_token});
+    });
+}
+
+// (handle, hidden, weights, targets, lse, entropy, dlogprob, dentropy, logit_scale) -> (dhidden, list of dweights)
+PyObject *vocab_logprobs_grad(PyObject *, PyObject *const *args, Py_ssize_t nargs) {
+    return call(nargs, 9, [&]() -> PyObject * {
+        const Tensor &hidden = tensor("hidden", args[1]), &targets = tensor("targets", args[3]);
+        const auto weights = list("weights", args[2]);
+        const Common c("hidden", hidden);
+        rar_vocab_logprobs_grad_args a{};
+        const Pieces w = logprob_inputs(a, hidden, targets, weights, args[8], c);
+        const int64_t tokens = hidden.size(0);
+        if (PyErr_Occurred()) return nullptr;
+        auto given = [&](const char *name, PyObject *o) {
+            return o == Py_None ? nullptr : (const float *)vec(name, tensor(name, o), tokens, at::kFloat, c);
+        };
+        a.weights = w.ptr.data();
+        a.lse = given("lse", args[4]);
+        a.entropy = given("entropy", args[5]);
+        a.dlogprob = given("dlogprob", args[6]);
+        a.dentropy = given("dentropy", args[7]);
+        if (!a.lse && tokens) refuse("lse must be a tensor");
+        if (args[6] == Py_None && args[7] == Py_None) refuse("one of dlogprob and dentropy must be a tensor");
+        if (args[7] != Py_None && args[5] == Py_None) refuse("dentropy needs entropy");
+        a.workspace_bytes = rar_vocab_logprobs_grad_workspace(a.tokens, a.dim, a.vocab, a.p);
+        Tensor dhidden = c.make({tokens, w.dim}, c.dtype), ws = c.bytes(a.workspace_bytes);
+        a.dhidden = dhidden.data_ptr();
+        a.workspace = ws.data_ptr();
+        std::vector<Tensor> dweights;
+        std::vector<void *> dptrs;
+        for (const Tensor *t : weights) {
+            dweights.push_back(c.make({t->size(0), w.dim}, c.dtype));
+            dptrs.push_back(dweights.back().data_ptr());
+        }
+        a.dweights = dptrs.data();
+        const int rc = rar_vocab_logprobs_grad(handle(args[0]), &a, stream_of(c));
+        return rc ? PyLong_FromLong(rc) : with_list(dhidden, dweights);
+    });
+}
+
+// rar_grad_norm of tensors, into norm and, if there is one, norms.
+int norm_of(PyObject *h, const Tensors &t, const Tensor &norm, const Tensor &norms) {
+    rar_grad_norm_args a{};
+    a.tensors = t.at.data();
+    a.n = t.at.size();
+    a.workspace_bytes = rar_grad_norm_workspace(a.tensors, a.n);
+    Tensor ws = at::empty({(int64_t)a.workspace_bytes}, norm.options().dtype(at::kByte));
+    a.norm = (float *)norm.data_ptr();
+    a.norms = norms.defined() ? (float *)norms.data_ptr() : nullptr;
+    a.workspace = ws.data_ptr();
+    return rar_grad_norm(handle(h), &a, stream_of(t.device));
+}
+
+// (handle, tensors) -> (norm, norms)
+PyObject *grad_norm(PyObject *, PyObject *const *args, Py_ssize_t nargs) {
+    return call(nargs, 2, [&]() -> PyObject * {
+        const Tensors t("a tensor", list("tensors", args[1]));
+        const auto type = at::TensorOptions().dtype(at::kFloat).device(t.device);
+        Tensor norm = at::empty({}, type), norms = at::empty({(int64_t)t.at.size()}, type);
+        const int rc = norm_of(args[0], t, norm, norms);
+        return rc ? PyLong_FromLong(rc) : tuple({norm, norms});
+    });
+}
+
+// (handle, tensors, max_norm, norm or None, out or None, eps) -> (norm,)
+PyObject *grad_clip(PyObject *, PyObject *const *args, Py_ssize_t nargs) {
+    return call(nargs, 6, [&]() -> PyObject * {
+        const auto tensors = list("tensors", args[1]);
+        std::vector<const Tensor *> outs;
+        if (args[4] != Py_None) outs = list("out", args[4]);
+        const Tensors plain("a tensor", tensors), t = outs.empty() ? plain : Tensors("a tensor", tensors, &outs);
+        const double max_norm = PyFloat_AsDouble(args[2]), eps = PyFloat_AsDouble(args[5]);
+        if (PyErr_Occurred()) return nullptr;
+        rar_grad_clip_args a{};
+        std::vector<rar_tensor> to;
+        if (!outs.empty()) {
+            to = Tensors("an output", outs, &tensors).at;
+            a.out = to.data();
+        }
+        a.tensors = t.at.data();
+        a.n = t.at.size();
+        a.max_norm = (float)max_norm;
+        a.eps = (float)eps;
+        Tensor norm;
+        if (args[3] != Py_None) {
+            norm = tensor("norm", args[3]);
+            if (norm.numel() != 1 || norm.scalar_type() != at::kFloat || norm.device() != t.device)
+                refuse("norm must be one float32 value on " + t.device.str());
+        } else {
+            norm = at::empty({}, at::TensorOptions().dtype(at::kFloat).device(t.device));
+        }
+        a.norm = (const float *)norm.data_ptr();
+        // (what the second call would refuse is refused before the first one runs)
+        if (!(a.max_norm >= 0.0f) || a.max_norm > 3.402823466e38f) refuse("max_norm must be finite and not negative");
+        if (!(a.eps >= 0.0f) || a.eps > 3.402823466e38f) refuse("eps must be finite and not negative");
+        if (args[3] == Py_None)
+            if (const int rc = norm_of(args[0], plain, norm, Tensor())) return PyLong_FromLong(rc);
+        const int rc = rar_grad_clip(handle(args[0]), &a, stream_of(t.device));
+        return rc ? PyLong_FromLong(rc) : tuple({norm});
+    });
+}
+
 #define RAR_FAST(name) {#name, (PyCFunction)(void (*)(void))name, METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {RAR_FAST(add_rmsnorm), RAR_FAST(add_rmsnorm_grad), RAR_FAST(vocab_xent), RAR_FAST(embedding),
-                         RAR_FAST(embedding_grad), {nullptr, nullptr, 0, nullptr}};
+                         RAR_FAST(embedding_grad), RAR_FAST(vocab_logprobs), RAR_FAST(vocab_logprobs_grad), RAR_FAST(grad_norm),
+                         RAR_FAST(grad_clip), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_torch_ops", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -1,0 +1,514 @@
+// vocab_logprobs.cu -- log probabilities of given tokens, entropy and the most likely
+// alternatives over a vocabulary in p pieces, from the hidden states
+// (rar_vocab_logprobs), and their gradients (rar_vocab_logprobs_grad).
+//
+//   z = hidden W^T,  l = scale z,  m = max z,  S = sum exp(scale (z - m)),  U = sum exp(scale (z - m)) (z - m)
+//   lse = scale m + log S,  logprob = scale (z[target] - m) - log S,  entropy = log S - scale U / S
+//
+// (in this form nothing large cancels: S is at least 1 and U at most 0).  The gradient
+// for z, from those of the log probability, a, and of the entropy, b:
+//
+//   G = scale (a onehot(target) - p (a + b (log p + entropy))),  p = exp(l - lse)
+//   dhidden = G W,  dweights = G^T hidden
+//
+// which takes lse and the entropy as the forward pass gave them, so that the logits are
+// made once: 6 tokens x vocab x dim operations in all.
+#include "vocab_tiles.cuh"
+
+namespace rar {
+
+// Values in the order of their logits, equal ones from the lowest token on: the larger key first.
+// 0 is no value; NaN and -inf have none.
+__device__ __forceinline__ unsigned long long top_key(float z, uint32_t token) {
+    const uint32_t b = __float_as_uint(z + 0.0f);  // (no -0)
+    return (unsigned long long)(b & 0x80000000u ? ~b : b | 0x80000000u) << 32 | (uint32_t)~token;
+}
+__device__ __forceinline__ float top_value(unsigned long long key) {
+    const uint32_t b = (uint32_t)(key >> 32);
+    return __uint_as_float(b & 0x80000000u ? b ^ 0x80000000u : ~b);
+}
+__device__ __forceinline__ uint32_t top_token(unsigned long long key) { return ~(uint32_t)key; }
+
+// The largest keys seen by a warp, one a lane in falling order; `least` is the one at `top`.
+struct TopList {
+    unsigned long long key = 0, least = 0;
+    // takes the lanes' keys; 0 where a lane has none
+    __device__ __forceinline__ void add(unsigned long long x, int top) {
+        const int lane = threadIdx.x % 32;
+        for (unsigned more = __ballot_sync(0xFFFFFFFFu, x > least); more; more &= more - 1) {
+            const unsigned long long y = __shfl_sync(0xFFFFFFFFu, x, __ffs(more) - 1);
+            if (y <= least) continue;
+            const int at = __popc(__ballot_sync(0xFFFFFFFFu, key > y));
+            const unsigned long long before = __shfl_up_sync(0xFFFFFFFFu, key, 1);
+            key = lane < at ? key : lane == at ? y : before;
+            least = __shfl_sync(0xFFFFFFFFu, key, top - 1);
+        }
+    }
+    // takes another list: of two falling runs, one turned round, the larger ones of each
+    // place are the 32 largest of all, rising and falling once (Batcher's merge)
+    __device__ __forceinline__ void merge(unsigned long long other) {
+        const int lane = threadIdx.x % 32;
+        const unsigned long long x = __shfl_sync(0xFFFFFFFFu, other, 31 - lane);
+        key = key > x ? key : x;
+#pragma unroll
+        for (int d = 16; d; d /= 2) {
+            const unsigned long long y = __shfl_xor_sync(0xFFFFFFFFu, key, d);
+            key = ((lane & d) == 0) == (key > y) ? key : y;
+        }
+    }
+};
+
+// exp(scale x) for k = scale log2(e); good to (2 + |scale x|) 2^-23 (see exp_of).
+__device__ __forceinline__ float exp_scaled(float x, float k) {
+    float r;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x * k));
+    return r;
+}
+
+// max, S and U of some logits, S and U relative to the maximum.
+struct LogitSums {
+    float max = -INFINITY, s = 0.0f, u = 0.0f;
+    // moves the maximum up to `top`
+    __device__ __forceinline__ void raise(float top, float k) {
+        const float d = fmaxf(max - top, -1e30f), f = exp_scaled(d, k);  // (from -inf: s and u are 0)
+        u = f * fmaf(d, s, u);
+        s *= f;
+        max = top;
+    }
+    // z[n], of which those that are not there are -inf
+    template <int N>
+    __device__ __forceinline__ void add(const float (&z)[N], float k) {
+        float top = max;
+#pragma unroll
+        for (int i = 0; i < N; i++) top = fmaxf(top, z[i]);
+        if (top > max) raise(top, k);
+        const float ref = top == -INFINITY ? 0.0f : top;  // nothing but -inf, or NaN, which s then shows
+#pragma unroll
+        for (int i = 0; i < N; i++) {
+            const float d = z[i] - ref, e = exp_scaled(d, k);
+            s += e;
+            u = fmaf(e, fmaxf(d, -1e30f), u);  // (-inf: 0 to be added)
+        }
+    }
+    __device__ __forceinline__ void join(float om, float os, float ou, float k) {
+        if (os == 0.0f) return;  // nothing there
+        LogitSums o{om, os, ou};
+        const float top = fmaxf(max, om);
+        if (top != -INFINITY) {
+            raise(top, k);
+            o.raise(top, k);
+        }
+        s += o.s;
+        u += o.u;
+    }
+    // over the lanes, in an order that gives every lane the same bits
+    __device__ __forceinline__ void join_lanes(int lanes, float k) {
+        const int lane = threadIdx.x % 32;
+        for (int d = 1; d < lanes; d *= 2) {
+            const float om = __shfl_xor_sync(0xFFFFFFFFu, max, d), os = __shfl_xor_sync(0xFFFFFFFFu, s, d), ou = __shfl_xor_sync(0xFFFFFFFFu, u, d);
+            if (lane & d) {
+                LogitSums o{om, os, ou};
+                o.join(max, s, u, k);
+                *this = o;
+            } else {
+                join(om, os, ou, k);
+            }
+        }
+    }
+};
+
+// Results of tokens [0, tokens).
+struct LogprobOut {
+    long long tokens, vocab;
+    float scale;
+    int top;
+    const void *targets;
+    int index_bytes;
+    float *logprob, *entropy, *lse;
+    float *top_logprob;
+    long long *top_token;
+};
+// Those of one token, by a warp with the same sums in every lane.
+__device__ __forceinline__ void write_token(const LogprobOut &o, long long t, const LogitSums &sums, float z_target, unsigned long long key) {
+    const int lane = threadIdx.x % 32;
+    const float log_s = logf(sums.s);
+    if (lane == 0) {
+        const long long y = load_index(o.targets, o.index_bytes, t);
+        if (o.logprob) o.logprob[t] = y >= 0 && y < o.vocab ? fmaf(o.scale, z_target - sums.max, -log_s) : 0.0f;
+        if (o.entropy) o.entropy[t] = log_s - o.scale * __fdiv_rn(sums.u, sums.s);
+        if (o.lse) o.lse[t] = fmaf(o.scale, sums.max, log_s);
+    }
+    if (lane < o.top) {
+        o.top_token[t * o.top + lane] = key ? (long long)top_token(key) : -1ll;
+        o.top_logprob[t * o.top + lane] = key ? fmaf(o.scale, top_value(key) - sums.max, -log_s) : -INFINITY;
+    }
+}
+
+struct SelectArgs {
+    LogprobOut out;
+    const float *logits;  // [tokens][pitch], 16-byte aligned rows
+    long long pitch;
+};
+
+constexpr int kSelectWarps = 8, kSelectCluster = 8;
+
+// Everything about a token from its logits: a cluster of CTAs a token, each with a range of the
+// vocabulary, whose warps keep sums and a list of their own.
+__global__ void __launch_bounds__(32 * kSelectWarps) logprob_select_kernel(const __grid_constant__ SelectArgs a) {
+    __shared__ unsigned long long lists[kSelectWarps][32];
+    __shared__ float3 sums[kSelectWarps];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, top = a.out.top;
+    const uint32_t rank = cluster_rank(), ctas = gridDim.x;
+    const long long t = blockIdx.y;
+    const float k = a.out.scale * 1.4426950408889634f;
+    pdl_wait();
+    pdl_launch_dependents();
+    const float *row = a.logits + t * a.pitch;
+    const uint32_t vocab = (uint32_t)a.out.vocab, vecs = (vocab + 3) / 4;
+    const uint32_t v0 = (uint32_t)((unsigned long long)vecs * rank / ctas), v1 = (uint32_t)((unsigned long long)vecs * (rank + 1) / ctas);
+    LogitSums own;
+    TopList list;
+    for (uint32_t v = v0 + warp * 32; v < v1; v += 32 * kSelectWarps) {
+        const bool has = v + lane < v1;
+        float4 q = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        if (has) q = __ldcg(reinterpret_cast<const float4 *>(row) + v + lane);
+        const uint32_t first = (v + lane) * 4;
+        float z[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int e = 0; e < 4; e++)
+            if (first + e >= vocab) z[e] = -INFINITY;
+        own.add(z, k);
+        if (top) {
+            const float least = list.least ? top_value(list.least) : -INFINITY;
+            // (NaN is below everything here)
+            if (__any_sync(0xFFFFFFFFu, fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])) >= least))
+#pragma unroll
+                for (int e = 0; e < 4; e++) list.add(z[e] > -INFINITY ? top_key(z[e], first + e) : 0ull, top);
+        }
+    }
+    own.join_lanes(32, k);
+    lists[warp][lane] = list.key;
+    if (lane == 0) sums[warp] = make_float3(own.max, own.s, own.u);
+    // the CTA's, and then the cluster's, in warp 0 of its first CTA
+    auto join = [&](int n) {
+        for (int d = 1; d < n; d *= 2) {
+            __syncthreads();
+            if (top && warp % (2 * d) == 0 && warp + d < n) {
+                list.merge(lists[warp + d][lane]);
+                lists[warp][lane] = list.key;
+            }
+        }
+        __syncthreads();
+        if (warp == 0) {
+            own = LogitSums();
+            if (lane < n) own.join(sums[lane].x, sums[lane].y, sums[lane].z, k);
+            own.join_lanes(32, k);
+        }
+    };
+    join(kSelectWarps);
+    if (ctas > 1) {
+        if (warp == 0 && lane == 0) sums[0] = make_float3(own.max, own.s, own.u);
+        cluster_sync_all();
+        list.key = 0;
+        float3 other = make_float3(-INFINITY, 0.0f, 0.0f);
+        if (rank == 0 && warp < (int)ctas) {
+            const uint32_t at = peer_addr(smem_u32(&lists[0][lane]), (uint32_t)warp), st = peer_addr(smem_u32(&sums[0]), (uint32_t)warp);
+            asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(list.key) : "r"(at) : "memory");
+            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(other.x) : "r"(st) : "memory");
+            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(other.y) : "r"(st + 4) : "memory");
+            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(other.z) : "r"(st + 8) : "memory");
+        }
+        cluster_sync_all();  // all of it is read: the others may end, and this one may write
+        if (rank) return;
+        lists[warp][lane] = list.key;
+        if (lane == 0) sums[warp] = other;
+        join((int)ctas);
+    }
+    if (warp == 0) {
+        const long long y = load_index(a.out.targets, a.out.index_bytes, t);
+        write_token(a.out, t, own, y >= 0 && y < a.out.vocab ? __ldcg(row + y) : 0.0f, list.key);
+    }
+}
+
+// Of each token: its weights in G (none where its target is left out), the largest bound on an
+// entry of its row of G, and its hidden state, cleared where it has no part in the gradients
+// (0 x NaN is not 0 in dweights' sum).  A warp a token.
+constexpr int kPrepareTokens = 8;
+__global__ void __launch_bounds__(32 * kPrepareTokens) logprob_prepare_kernel(const __grid_constant__ VocabArgs a) {
+    pdl_wait();
+    pdl_launch_dependents();
+    const int lane = threadIdx.x % 32;
+    const long long t = (long long)blockIdx.x * kPrepareTokens + threadIdx.x / 32;
+    if (t >= a.tokens) return;
+    const long long y = load_index(a.targets, a.index_bytes, t);
+    const bool counts = y >= 0 && y < a.vocab;
+    const float da = counts && a.dlogprob ? a.dlogprob[t] : 0.0f, db = counts && a.dentropy ? a.dentropy[t] : 0.0f;
+    const bool used = da != 0.0f || db != 0.0f;
+    if (lane == 0) {
+        a.row_weight[t] = da;
+        a.row_entropy[t] = db;
+        // |G| <= |a| + |b| max(p |log p|, p entropy)
+        const float most = fabsf(da) + (db != 0.0f ? fabsf(db) * fmaxf(1.0f, fabsf(a.entropy_in[t])) : 0.0f);
+        if (isfinite(most)) atomicMax(a.w_max, __float_as_uint(most));
+    }
+    const int vecs = (int)(a.dim / 8);
+    const uint4 *from = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.hidden) + t * a.hidden_stride);
+    uint4 *to = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.hidden_used) + t * a.dim);
+    for (int i0 = lane; i0 < vecs; i0 += 32 * 4) {
+        uint4 q[4];  // loads in flight together
+#pragma unroll
+        for (int u = 0; u < 4; u++) q[u] = used ? __ldg(from + min(i0 + u * 32, vecs - 1)) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int u = 0; u < 4; u++)
+            if (i0 + u * 32 < vecs) to[i0 + u * 32] = q[u];
+    }
+}
+
+namespace {
+
+constexpr size_t kLogitBytes = (size_t)256 << 20;  // of logits in the workspace, at most
+
+size_t plan(void *base, size_t tokens, size_t vocab, int p, VocabArgs *k) {
+    WorkspacePlan w(base);
+    plan_blocks(vocab, p, k);
+    k->logits_pitch = (long long)((vocab + 3) / 4 * 4);
+    // tokens of a pass over the pieces
+    size_t chunk = std::min(tokens, std::max<size_t>(kLogitBytes / (4 * (size_t)k->logits_pitch), kTile));
+    if (chunk < tokens) chunk = chunk / kTile * kTile;
+    k->window = (int)chunk;
+    k->logits = w.take<float>(chunk * (size_t)k->logits_pitch);
+    return w.used;
+}
+size_t plan_gradients(void *base, size_t tokens, size_t dim, size_t vocab, int p, VocabArgs *k) {
+    WorkspacePlan w(base);
+    plan_blocks(vocab, p, k);
+    k->w_max = w.take<unsigned>(1);
+    k->row_weight = w.take<float>(tokens);
+    k->row_entropy = w.take<float>(tokens);
+    plan_grad(w, tokens, dim, k);
+    return w.used;
+}
+
+// What both calls have: sizes, hidden states, pieces, targets.
+template <typename Args>
+int check_inputs(OpCheck &c, const Args *a) {
+    if (!a) return c.bad("args is NULL");
+    int rc = c.dtype(a->dtype, false);
+    if (rc != RAR_OK) return rc;
+    if (a->p < 1 || a->p > kInlineP) return c.bad("p must be in [1, 64]");
+    if (a->dim < 1 || a->vocab < 1) return c.bad("dim and vocab must be at least 1");
+    if (a->dim % 8) return c.bad("dim must be a multiple of 8");
+    if (a->index_bytes != 4 && a->index_bytes != 8) return c.bad("index_bytes must be 4 or 8");
+    if (!(a->logit_scale > 0.0f && a->logit_scale <= 3.402823466e38f)) return c.bad("logit_scale must be positive and finite");
+    if (!sizes_ok(a->tokens, a->dim, a->vocab, a->p)) return c.bad("the sizes are too large");
+    MatrixSpan s;
+    if ((rc = c.matrix("hidden", a->hidden, a->tokens, a->dim, a->hidden_stride, 2, 16, &s)) != RAR_OK) return rc;
+    c.input(s);
+    if (!a->weights) return c.bad("weights is NULL");
+    for (int r = 0; r < a->p; r++) {
+        const size_t rows = a->vocab / a->p + ((size_t)r < a->vocab % a->p ? 1 : 0);
+        if ((rc = c.matrix("a weight piece", a->weights[r], rows, a->dim, a->weight_stride, 2, 16, &s)) != RAR_OK) return rc;
+        c.input(s);
+    }
+    const size_t ib = (size_t)a->index_bytes;
+    if ((rc = c.matrix("targets", a->targets, 1, a->tokens, 0, ib, ib, &s)) != RAR_OK) return rc;
+    c.input(s);
+    return RAR_OK;
+}
+template <typename Args>
+void set_inputs(rar_ctx *h, const Args *a, VocabArgs *k) {
+    for (int r = 0; r < a->p; r++) k->w.inl[r] = const_cast<void *>(a->weights[r]);
+    k->p = a->p;
+    k->tokens = (long long)a->tokens;
+    k->dim = (long long)a->dim;
+    k->vocab = (long long)a->vocab;
+    k->hidden_stride = (long long)(a->hidden_stride ? a->hidden_stride : a->dim);
+    k->weight_stride = (long long)(a->weight_stride ? a->weight_stride : a->dim);
+    k->hidden = a->hidden;
+    k->targets = a->targets;
+    k->index_bytes = a->index_bytes;
+    k->scale = a->logit_scale;
+    k->limits = {h->status, op_timeout_ns(h), op_muted_rank(h)};
+}
+struct Vec { const char *name; const void *ptr; size_t n, eb; };
+
+cudaError_t launch_select(const rar_ctx *h, const SelectArgs &s, cudaStream_t stream) {
+    // CTAs a token: until there are two an SM, but at least 1024 logits each
+    unsigned ctas = 1;
+    while (ctas < kSelectCluster && s.out.tokens * ctas < 2 * h->sm_count && s.out.vocab / (2 * ctas) >= 1024) ctas *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(32 * kSelectWarps);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = ctas;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    // (a grid's y has 16 bits)
+    for (long long t0 = 0; t0 < s.out.tokens; t0 += 65535) {
+        SelectArgs part = s;
+        part.out.tokens = std::min<long long>(s.out.tokens - t0, 65535);
+        part.logits += t0 * s.pitch;
+        part.out.targets = static_cast<const char *>(s.out.targets) + t0 * s.out.index_bytes;
+        for (float **p : {&part.out.logprob, &part.out.entropy, &part.out.lse})
+            if (*p) *p += t0;
+        if (s.out.top) part.out.top_logprob += t0 * s.out.top, part.out.top_token += t0 * s.out.top;
+        cfg.gridDim = dim3(ctas, (unsigned)part.out.tokens);
+        const cudaError_t e = cudaLaunchKernelEx(&cfg, logprob_select_kernel, part);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+int vocab_logprobs(rar_ctx *h, const rar_vocab_logprobs_args *a, cudaStream_t stream) {
+    OpCheck c(h, "rar_vocab_logprobs");
+    int rc = check_inputs(c, a);
+    if (rc != RAR_OK) return rc;
+    if (a->top < 0 || a->top > RAR_LOGPROBS_MAX_TOP || (size_t)a->top > a->vocab) return c.bad("top must be in [0, RAR_LOGPROBS_MAX_TOP] and at most vocab");
+    MatrixSpan s;
+    const size_t n = a->tokens, listed = n * (size_t)a->top;
+    for (const Vec &v : {Vec{"logprob", a->logprob, n, 4}, Vec{"entropy", a->entropy, n, 4}, Vec{"lse", a->lse, n, 4}})
+        if (v.ptr) {
+            if ((rc = c.matrix(v.name, v.ptr, 1, v.n, 0, v.eb, v.eb, &s)) != RAR_OK) return rc;
+            c.output(s);
+        }
+    for (const Vec &v : {Vec{"top_logprob", a->top_logprob, listed, 4}, Vec{"top_token", a->top_token, listed, 8}}) {  // (top 0: nothing)
+        if ((rc = c.matrix(v.name, v.ptr, 1, v.n, 0, v.eb, v.eb, &s)) != RAR_OK) return rc;
+        c.output(s);
+    }
+    VocabArgs k{};
+    const size_t need = plan(nullptr, a->tokens, a->vocab, a->p, &k);
+    if ((rc = c.workspace(a->workspace, a->workspace_bytes, need)) != RAR_OK) return rc;
+    if ((rc = c.overlaps([](const MatrixSpan &, const MatrixSpan &) { return false; })) != RAR_OK) return rc;
+    if (a->tokens == 0) return RAR_OK;
+
+    DeviceGuard dg(h->device);
+    if (dg.err != cudaSuccess) return cuda_fail(h, dg.err, "selecting the device");
+    plan(a->workspace, a->tokens, a->vocab, a->p, &k);
+    set_inputs(h, a, &k);
+    note_op_call(h, a->p, stream);
+
+    CallMaps m;
+    if (!make_maps(a->dtype, k, &m)) return fail(h, RAR_ECUDA, "rar_vocab_logprobs: the driver refused a tensor map");
+    auto run = [&](auto dt) {
+        constexpr int DT = decltype(dt)::value;
+        cudaError_t e = cudaSuccess;
+        const long long chunk = k.window;
+        for (long long t0 = 0; t0 < (long long)n && e == cudaSuccess; t0 += chunk) {
+            VocabArgs part = k;
+            part.tokens = std::min((long long)n - t0, chunk);
+            part.hidden = static_cast<const uint16_t *>(k.hidden) + t0 * k.hidden_stride;
+            part.targets = static_cast<const char *>(k.targets) + t0 * k.index_bytes;
+            if (!make_map(&m.logits.one, a->dtype, part.hidden, part.tokens, k.dim, k.hidden_stride, 128)) return cudaErrorInvalidValue;
+            e = k.dim > 64 * kStepsPerSum ? launch_tiles<TILES_LOGITS_SUMS, DT>(h, part, m.logits, 0, k.n_blocks, stream)
+                                          : launch_tiles<TILES_LOGITS, DT>(h, part, m.logits, 0, k.n_blocks, stream);
+            SelectArgs s{};
+            auto at = [&](float *v) { return v ? v + t0 : nullptr; };
+            s.out = {part.tokens, k.vocab, k.scale, a->top, part.targets, k.index_bytes, at(a->logprob), at(a->entropy), at(a->lse), nullptr, nullptr};
+            if (a->top) s.out.top_logprob = a->top_logprob + t0 * a->top, s.out.top_token = a->top_token + t0 * a->top;
+            s.logits = k.logits;
+            s.pitch = k.logits_pitch;
+            if (e == cudaSuccess) e = launch_select(h, s, stream);
+        }
+        return e;
+    };
+    const cudaError_t ce = a->dtype == RAR_BFLOAT16 ? run(IntC<DT_BF16>{}) : run(IntC<DT_F16>{});
+    return ce == cudaSuccess ? RAR_OK : cuda_fail(h, ce, "launching the log probabilities");
+}
+
+int vocab_logprobs_grad(rar_ctx *h, const rar_vocab_logprobs_grad_args *a, cudaStream_t stream) {
+    OpCheck c(h, "rar_vocab_logprobs_grad");
+    int rc = check_inputs(c, a);
+    if (rc != RAR_OK) return rc;
+    MatrixSpan s;
+    const size_t n = a->tokens;
+    if (n && !a->dlogprob && !a->dentropy) return c.bad("dlogprob and dentropy are NULL");
+    const Vec ins[] = {{"lse", a->lse, n, 1}, {"dlogprob", a->dlogprob, n, a->dlogprob != nullptr}, {"dentropy", a->dentropy, n, a->dentropy != nullptr},
+                       {"entropy", a->entropy, n, a->dentropy != nullptr}};
+    for (const Vec &v : ins)
+        if (v.eb) {  // (needed)
+            if ((rc = c.matrix(v.name, v.ptr, 1, v.n, 0, 4, 4, &s)) != RAR_OK) return rc;
+            c.input(s);
+        }
+    if (!a->dhidden && !a->dweights) return c.bad("dhidden and dweights are NULL");
+    if (a->dhidden) {
+        if ((rc = c.matrix("dhidden", a->dhidden, n, a->dim, a->dhidden_stride, 2, 16, &s)) != RAR_OK) return rc;
+        c.output(s);
+    }
+    for (int r = 0; r < a->p && a->dweights; r++) {
+        const size_t rows = a->vocab / a->p + ((size_t)r < a->vocab % a->p ? 1 : 0);
+        if ((rc = c.matrix("a dweight piece", a->dweights[r], rows, a->dim, a->dweight_stride, 2, 16, &s)) != RAR_OK) return rc;
+        c.output(s);
+    }
+    VocabArgs k{};
+    const size_t need = plan_gradients(nullptr, n, a->dim, a->vocab, a->p, &k);
+    if ((rc = c.workspace(a->workspace, a->workspace_bytes, need)) != RAR_OK) return rc;
+    if ((rc = c.overlaps([](const MatrixSpan &, const MatrixSpan &) { return false; })) != RAR_OK) return rc;
+    if (n == 0 && !a->dweights) return RAR_OK;
+
+    DeviceGuard dg(h->device);
+    if (dg.err != cudaSuccess) return cuda_fail(h, dg.err, "selecting the device");
+    plan_gradients(a->workspace, n, a->dim, a->vocab, a->p, &k);
+    set_inputs(h, a, &k);
+    for (int r = 0; r < a->p; r++) k.dw.inl[r] = a->dweights ? a->dweights[r] : nullptr;
+    k.dhidden_stride = (long long)(a->dhidden_stride ? a->dhidden_stride : a->dim);
+    k.dweight_stride = (long long)(a->dweight_stride ? a->dweight_stride : a->dim);
+    k.dhidden = a->dhidden;
+    k.want_dw = a->dweights != nullptr;
+    k.lse_in = a->lse;
+    k.entropy_in = a->entropy;
+    k.dlogprob = a->dlogprob;
+    k.dentropy = a->dentropy;
+    note_op_call(h, a->p, stream);
+
+    CallMaps m;
+    if (k.tokens && !make_maps(a->dtype, k, &m)) return fail(h, RAR_ECUDA, "rar_vocab_logprobs_grad: the driver refused a tensor map");
+    auto run = [&](auto dt) {
+        constexpr int DT = decltype(dt)::value;
+        if (!k.tokens) return clear_dweights(k, stream);
+        cudaError_t e = cudaMemsetAsync(k.w_max, 0, sizeof(*k.w_max), stream);
+        if (e == cudaSuccess)
+            e = launch_pdl(logprob_prepare_kernel, dim3((unsigned)((k.tokens + kPrepareTokens - 1) / kPrepareTokens)), dim3(32 * kPrepareTokens), 0, stream, k);
+        if (e != cudaSuccess) return e;
+        return k.dim > 64 * kStepsPerSum ? launch_gradients<TILES_LOGPROB_G_SUMS, DT>(h, k, m, stream) : launch_gradients<TILES_LOGPROB_G, DT>(h, k, m, stream);
+    };
+    const cudaError_t ce = a->dtype == RAR_BFLOAT16 ? run(IntC<DT_BF16>{}) : run(IntC<DT_F16>{});
+    return ce == cudaSuccess ? RAR_OK : cuda_fail(h, ce, "launching the log probabilities' gradients");
+}
+
+}  // namespace
+}  // namespace rar
+
+extern "C" {
+
+size_t rar_vocab_logprobs_workspace(size_t tokens, size_t dim, size_t vocab, int p, int top) {
+    if (!rar::sizes_ok(tokens, dim, vocab, p) || top < 0 || top > RAR_LOGPROBS_MAX_TOP) return 0;
+    rar::VocabArgs k{};
+    return rar::plan(nullptr, tokens, vocab, p, &k);
+}
+
+int rar_vocab_logprobs(rar_handle h, const rar_vocab_logprobs_args *a, void *stream) {
+    return rar::guarded(h, [&] {
+        if (!h) return rar::fail(nullptr, RAR_EINVAL, "handle is NULL");
+        return rar::vocab_logprobs(h, a, (cudaStream_t)stream);
+    });
+}
+
+size_t rar_vocab_logprobs_grad_workspace(size_t tokens, size_t dim, size_t vocab, int p) {
+    if (!rar::sizes_ok(tokens, dim, vocab, p)) return 0;
+    rar::VocabArgs k{};
+    return rar::plan_gradients(nullptr, tokens, dim, vocab, p, &k);
+}
+
+int rar_vocab_logprobs_grad(rar_handle h, const rar_vocab_logprobs_grad_args *a, void *stream) {
+    return rar::guarded(h, [&] {
+        if (!h) return rar::fail(nullptr, RAR_EINVAL, "handle is NULL");
+        return rar::vocab_logprobs_grad(h, a, (cudaStream_t)stream);
+    });
+}
+
+}  // extern "C"
