@@ -13,21 +13,11 @@
 //
 // which takes lse and the entropy as the forward pass gave them, so that the logits are
 // made once: 6 tokens x vocab x dim operations in all.
+#include <cmath>
+
 #include "vocab_tiles.cuh"
 
 namespace rar {
-
-// Values in the order of their logits, equal ones from the lowest token on: the larger key first.
-// 0 is no value; NaN and -inf have none.
-__device__ __forceinline__ unsigned long long top_key(float z, uint32_t token) {
-    const uint32_t b = __float_as_uint(z + 0.0f);  // (no -0)
-    return (unsigned long long)(b & 0x80000000u ? ~b : b | 0x80000000u) << 32 | (uint32_t)~token;
-}
-__device__ __forceinline__ float top_value(unsigned long long key) {
-    const uint32_t b = (uint32_t)(key >> 32);
-    return __uint_as_float(b & 0x80000000u ? b ^ 0x80000000u : ~b);
-}
-__device__ __forceinline__ uint32_t top_token(unsigned long long key) { return ~(uint32_t)key; }
 
 // The largest keys seen by a warp, one a lane in falling order; `least` is the one at `top`.
 struct TopList {
@@ -58,68 +48,9 @@ struct TopList {
     }
 };
 
-// exp(scale x) for k = scale log2(e); good to (2 + |scale x|) 2^-23 (see exp_of).
-__device__ __forceinline__ float exp_scaled(float x, float k) {
-    float r;
-    asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x * k));
-    return r;
-}
-
-// max, S and U of some logits, S and U relative to the maximum.
-struct LogitSums {
-    float max = -INFINITY, s = 0.0f, u = 0.0f;
-    // moves the maximum up to `top`
-    __device__ __forceinline__ void raise(float top, float k) {
-        const float d = fmaxf(max - top, -1e30f), f = exp_scaled(d, k);  // (from -inf: s and u are 0)
-        u = f * fmaf(d, s, u);
-        s *= f;
-        max = top;
-    }
-    // z[n], of which those that are not there are -inf
-    template <int N>
-    __device__ __forceinline__ void add(const float (&z)[N], float k) {
-        float top = max;
-#pragma unroll
-        for (int i = 0; i < N; i++) top = fmaxf(top, z[i]);
-        if (top > max) raise(top, k);
-        const float ref = top == -INFINITY ? 0.0f : top;  // nothing but -inf, or NaN, which s then shows
-#pragma unroll
-        for (int i = 0; i < N; i++) {
-            const float d = z[i] - ref, e = exp_scaled(d, k);
-            s += e;
-            u = fmaf(e, fmaxf(d, -1e30f), u);  // (-inf: 0 to be added)
-        }
-    }
-    __device__ __forceinline__ void join(float om, float os, float ou, float k) {
-        if (os == 0.0f) return;  // nothing there
-        LogitSums o{om, os, ou};
-        const float top = fmaxf(max, om);
-        if (top != -INFINITY) {
-            raise(top, k);
-            o.raise(top, k);
-        }
-        s += o.s;
-        u += o.u;
-    }
-    // over the lanes, in an order that gives every lane the same bits
-    __device__ __forceinline__ void join_lanes(int lanes, float k) {
-        const int lane = threadIdx.x % 32;
-        for (int d = 1; d < lanes; d *= 2) {
-            const float om = __shfl_xor_sync(0xFFFFFFFFu, max, d), os = __shfl_xor_sync(0xFFFFFFFFu, s, d), ou = __shfl_xor_sync(0xFFFFFFFFu, u, d);
-            if (lane & d) {
-                LogitSums o{om, os, ou};
-                o.join(max, s, u, k);
-                *this = o;
-            } else {
-                join(om, os, ou, k);
-            }
-        }
-    }
-};
-
-// Results of tokens [0, tokens).
+// Where a call's results go.
 struct LogprobOut {
-    long long tokens, vocab;
+    long long vocab;
     float scale;
     int top;
     const void *targets;
@@ -144,90 +75,38 @@ __device__ __forceinline__ void write_token(const LogprobOut &o, long long t, co
     }
 }
 
-struct SelectArgs {
-    LogprobOut out;
-    const float *logits;  // [tokens][pitch], 16-byte aligned rows
-    long long pitch;
-};
-
-constexpr int kSelectWarps = 8, kSelectCluster = 8;
-
-// Everything about a token from its logits: a cluster of CTAs a token, each with a range of the
-// vocabulary, whose warps keep sums and a list of their own.
-__global__ void __launch_bounds__(32 * kSelectWarps) logprob_select_kernel(const __grid_constant__ SelectArgs a) {
-    __shared__ unsigned long long lists[kSelectWarps][32];
-    __shared__ float3 sums[kSelectWarps];
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, top = a.out.top;
-    const uint32_t rank = cluster_rank(), ctas = gridDim.x;
-    const long long t = blockIdx.y;
-    const float k = a.out.scale * 1.4426950408889634f;
+// Results from the pairs' sums and alternatives, a warp a token.
+constexpr int kJoinTokens = 4;
+__global__ void __launch_bounds__(32 * kJoinTokens) logprob_join_kernel(const __grid_constant__ VocabArgs a, const __grid_constant__ LogprobOut o) {
     pdl_wait();
     pdl_launch_dependents();
-    const float *row = a.logits + t * a.pitch;
-    const uint32_t vocab = (uint32_t)a.out.vocab, vecs = (vocab + 3) / 4;
-    const uint32_t v0 = (uint32_t)((unsigned long long)vecs * rank / ctas), v1 = (uint32_t)((unsigned long long)vecs * (rank + 1) / ctas);
+    const int lane = threadIdx.x % 32;
+    const long long t = (long long)blockIdx.x * kJoinTokens + threadIdx.x / 32;
+    if (t >= a.tokens) return;
+    const float k = a.scale * 1.4426950408889634f;
+    const int tb = tiles_of(a.tokens), r0 = (int)(t / kTile) / a.width * a.width;
+    const int lists = 2 * min(pairs_a_row(a.pairs, min(a.width, tb - r0)), a.n_blocks);
+    const long long y = load_index(o.targets, o.index_bytes, t);
+    const float z = y >= 0 && y < a.vocab ? a.z_target[t] : 0.0f;
     LogitSums own;
-    TopList list;
-    for (uint32_t v = v0 + warp * 32; v < v1; v += 32 * kSelectWarps) {
-        const bool has = v + lane < v1;
-        float4 q = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-        if (has) q = __ldcg(reinterpret_cast<const float4 *>(row) + v + lane);
-        const uint32_t first = (v + lane) * 4;
-        float z[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-        for (int e = 0; e < 4; e++)
-            if (first + e >= vocab) z[e] = -INFINITY;
-        own.add(z, k);
-        if (top) {
-            const float least = list.least ? top_value(list.least) : -INFINITY;
-            // (NaN is below everything here)
-            if (__any_sync(0xFFFFFFFFu, fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])) >= least))
-#pragma unroll
-                for (int e = 0; e < 4; e++) list.add(z[e] > -INFINITY ? top_key(z[e], first + e) : 0ull, top);
-        }
+    for (int i = lane; i < lists; i += 32) {
+        const float4 q = __ldcg(a.sums + (long long)i * a.tokens + t);
+        own.join(q.x, q.y, q.z, k);
     }
     own.join_lanes(32, k);
-    lists[warp][lane] = list.key;
-    if (lane == 0) sums[warp] = make_float3(own.max, own.s, own.u);
-    // the CTA's, and then the cluster's, in warp 0 of its first CTA
-    auto join = [&](int n) {
-        for (int d = 1; d < n; d *= 2) {
-            __syncthreads();
-            if (top && warp % (2 * d) == 0 && warp + d < n) {
-                list.merge(lists[warp + d][lane]);
-                lists[warp][lane] = list.key;
-            }
+    TopList list;
+    const int n = lists * a.top;
+    for (int i0 = 0; i0 < n; i0 += 32 * 4) {
+        unsigned long long x[4];  // loads in flight together
+#pragma unroll
+        for (int u = 0; u < 4; u++) {
+            const int i = i0 + u * 32 + lane;
+            x[u] = i < n ? __ldcg(a.lists + (long long)i * a.tokens + t) : 0ull;
         }
-        __syncthreads();
-        if (warp == 0) {
-            own = LogitSums();
-            if (lane < n) own.join(sums[lane].x, sums[lane].y, sums[lane].z, k);
-            own.join_lanes(32, k);
-        }
-    };
-    join(kSelectWarps);
-    if (ctas > 1) {
-        if (warp == 0 && lane == 0) sums[0] = make_float3(own.max, own.s, own.u);
-        cluster_sync_all();
-        list.key = 0;
-        float3 other = make_float3(-INFINITY, 0.0f, 0.0f);
-        if (rank == 0 && warp < (int)ctas) {
-            const uint32_t at = peer_addr(smem_u32(&lists[0][lane]), (uint32_t)warp), st = peer_addr(smem_u32(&sums[0]), (uint32_t)warp);
-            asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(list.key) : "r"(at) : "memory");
-            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(other.x) : "r"(st) : "memory");
-            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(other.y) : "r"(st + 4) : "memory");
-            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(other.z) : "r"(st + 8) : "memory");
-        }
-        cluster_sync_all();  // all of it is read: the others may end, and this one may write
-        if (rank) return;
-        lists[warp][lane] = list.key;
-        if (lane == 0) sums[warp] = other;
-        join((int)ctas);
+#pragma unroll
+        for (int u = 0; u < 4; u++) list.add(x[u], a.top);
     }
-    if (warp == 0) {
-        const long long y = load_index(a.out.targets, a.out.index_bytes, t);
-        write_token(a.out, t, own, y >= 0 && y < a.out.vocab ? __ldcg(row + y) : 0.0f, list.key);
-    }
+    write_token(o, t, own, z, list.key);
 }
 
 // Of each token: its weights in G (none where its target is left out), the largest bound on an
@@ -266,17 +145,39 @@ __global__ void __launch_bounds__(32 * kPrepareTokens) logprob_prepare_kernel(co
 
 namespace {
 
-constexpr size_t kLogitBytes = (size_t)256 << 20;  // of logits in the workspace, at most
+// Tokens of a pass over the pieces: bounds the workspace.
+constexpr size_t kPassTokens = 16384;
 
-size_t plan(void *base, size_t tokens, size_t vocab, int p, VocabArgs *k) {
+// Rows of tiles that are worked on at a time: those that keep the pairs busiest, the more
+// the better (each group of rows reads all pieces once).  In the last round of a single group
+// a block too few costs as much as one; over several groups that evens out.
+int choose_width(int tb, int nb, int pairs) {
+    int best = 1;
+    double least = 0.0;
+    for (int w = 1; w <= std::min(tb, 8); w++) {
+        const int groups = tb / w, rest = tb % w;
+        double rounds = groups * (double)nb / pairs_a_row(pairs, w) + (rest ? (double)nb / pairs_a_row(pairs, rest) : 0.0);
+        if (groups + (rest != 0) == 1) rounds = std::ceil(rounds);
+        if (w == 1 || rounds <= least) best = w, least = rounds;
+    }
+    return best;
+}
+
+size_t plan(void *base, size_t tokens, size_t vocab, int p, int top, VocabArgs *k) {
     WorkspacePlan w(base);
     plan_blocks(vocab, p, k);
-    k->logits_pitch = (long long)((vocab + 3) / 4 * 4);
-    // tokens of a pass over the pieces
-    size_t chunk = std::min(tokens, std::max<size_t>(kLogitBytes / (4 * (size_t)k->logits_pitch), kTile));
-    if (chunk < tokens) chunk = chunk / kTile * kTile;
-    k->window = (int)chunk;
-    k->logits = w.take<float>(chunk * (size_t)k->logits_pitch);
+    const size_t pass = std::min(tokens, kPassTokens);
+    k->window = (int)pass;
+    if (tokens) {
+        // (a last pass of fewer tokens has a width of its own, and up to all pairs on a row)
+        const int tb = tiles_of((long long)pass), width = choose_width(tb, k->n_blocks, (int)kPairs), rest = tb % width;
+        const bool even = tokens % pass == 0;
+        const int share = even ? pairs_a_row((int)kPairs, rest ? rest : width) : (int)kPairs;
+        const size_t lists = 2 * (size_t)std::min(std::max(share, pairs_a_row((int)kPairs, width)), k->n_blocks);
+        k->z_target = w.take<float>(pass);
+        k->sums = w.take<float4>(lists * pass);
+        k->lists = w.take<unsigned long long>(lists * pass * (size_t)top);
+    }
     return w.used;
 }
 size_t plan_gradients(void *base, size_t tokens, size_t dim, size_t vocab, int p, VocabArgs *k) {
@@ -332,38 +233,6 @@ void set_inputs(rar_ctx *h, const Args *a, VocabArgs *k) {
 }
 struct Vec { const char *name; const void *ptr; size_t n, eb; };
 
-cudaError_t launch_select(const rar_ctx *h, const SelectArgs &s, cudaStream_t stream) {
-    // CTAs a token: until there are two an SM, but at least 1024 logits each
-    unsigned ctas = 1;
-    while (ctas < kSelectCluster && s.out.tokens * ctas < 2 * h->sm_count && s.out.vocab / (2 * ctas) >= 1024) ctas *= 2;
-    cudaLaunchConfig_t cfg = {};
-    cfg.blockDim = dim3(32 * kSelectWarps);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = ctas;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    // (a grid's y has 16 bits)
-    for (long long t0 = 0; t0 < s.out.tokens; t0 += 65535) {
-        SelectArgs part = s;
-        part.out.tokens = std::min<long long>(s.out.tokens - t0, 65535);
-        part.logits += t0 * s.pitch;
-        part.out.targets = static_cast<const char *>(s.out.targets) + t0 * s.out.index_bytes;
-        for (float **p : {&part.out.logprob, &part.out.entropy, &part.out.lse})
-            if (*p) *p += t0;
-        if (s.out.top) part.out.top_logprob += t0 * s.out.top, part.out.top_token += t0 * s.out.top;
-        cfg.gridDim = dim3(ctas, (unsigned)part.out.tokens);
-        const cudaError_t e = cudaLaunchKernelEx(&cfg, logprob_select_kernel, part);
-        if (e != cudaSuccess) return e;
-    }
-    return cudaSuccess;
-}
-
 int vocab_logprobs(rar_ctx *h, const rar_vocab_logprobs_args *a, cudaStream_t stream) {
     OpCheck c(h, "rar_vocab_logprobs");
     int rc = check_inputs(c, a);
@@ -381,14 +250,14 @@ int vocab_logprobs(rar_ctx *h, const rar_vocab_logprobs_args *a, cudaStream_t st
         c.output(s);
     }
     VocabArgs k{};
-    const size_t need = plan(nullptr, a->tokens, a->vocab, a->p, &k);
+    const size_t need = plan(nullptr, a->tokens, a->vocab, a->p, a->top, &k);
     if ((rc = c.workspace(a->workspace, a->workspace_bytes, need)) != RAR_OK) return rc;
     if ((rc = c.overlaps([](const MatrixSpan &, const MatrixSpan &) { return false; })) != RAR_OK) return rc;
     if (a->tokens == 0) return RAR_OK;
 
     DeviceGuard dg(h->device);
     if (dg.err != cudaSuccess) return cuda_fail(h, dg.err, "selecting the device");
-    plan(a->workspace, a->tokens, a->vocab, a->p, &k);
+    plan(a->workspace, a->tokens, a->vocab, a->p, a->top, &k);
     set_inputs(h, a, &k);
     note_op_call(h, a->p, stream);
 
@@ -397,22 +266,24 @@ int vocab_logprobs(rar_ctx *h, const rar_vocab_logprobs_args *a, cudaStream_t st
     auto run = [&](auto dt) {
         constexpr int DT = decltype(dt)::value;
         cudaError_t e = cudaSuccess;
-        const long long chunk = k.window;
-        for (long long t0 = 0; t0 < (long long)n && e == cudaSuccess; t0 += chunk) {
+        for (long long t0 = 0; t0 < (long long)n && e == cudaSuccess; t0 += k.window) {
             VocabArgs part = k;
-            part.tokens = std::min((long long)n - t0, chunk);
+            part.tokens = std::min((long long)n - t0, (long long)k.window);
             part.hidden = static_cast<const uint16_t *>(k.hidden) + t0 * k.hidden_stride;
             part.targets = static_cast<const char *>(k.targets) + t0 * k.index_bytes;
-            if (!make_map(&m.logits.one, a->dtype, part.hidden, part.tokens, k.dim, k.hidden_stride, 128)) return cudaErrorInvalidValue;
-            e = k.dim > 64 * kStepsPerSum ? launch_tiles<TILES_LOGITS_SUMS, DT>(h, part, m.logits, 0, k.n_blocks, stream)
-                                          : launch_tiles<TILES_LOGITS, DT>(h, part, m.logits, 0, k.n_blocks, stream);
-            SelectArgs s{};
+            part.top = a->top;
+            part.stages = stages_beside(a->top);
+            const int tb = tiles_of(part.tokens);
+            part.width = choose_width(tb, k.n_blocks, (int)kPairs);
+            part.pairs = std::min(std::min(h->sm_count / 2, (int)kPairs), std::min(tb, part.width) * k.n_blocks);
+            if (t0 && !make_map(&m.logits.one, a->dtype, part.hidden, part.tokens, k.dim, k.hidden_stride, 128)) return cudaErrorInvalidValue;
+            e = k.dim > 64 * kStepsPerSum ? launch_tiles<TILES_LOGPROB_SUMS, DT>(h, part, m.logits, 0, k.n_blocks, stream)
+                                          : launch_tiles<TILES_LOGPROB, DT>(h, part, m.logits, 0, k.n_blocks, stream);
             auto at = [&](float *v) { return v ? v + t0 : nullptr; };
-            s.out = {part.tokens, k.vocab, k.scale, a->top, part.targets, k.index_bytes, at(a->logprob), at(a->entropy), at(a->lse), nullptr, nullptr};
-            if (a->top) s.out.top_logprob = a->top_logprob + t0 * a->top, s.out.top_token = a->top_token + t0 * a->top;
-            s.logits = k.logits;
-            s.pitch = k.logits_pitch;
-            if (e == cudaSuccess) e = launch_select(h, s, stream);
+            LogprobOut o{k.vocab, k.scale, a->top, part.targets, k.index_bytes, at(a->logprob), at(a->entropy), at(a->lse), nullptr, nullptr};
+            if (a->top) o.top_logprob = a->top_logprob + t0 * a->top, o.top_token = a->top_token + t0 * a->top;
+            if (e == cudaSuccess)
+                e = launch_pdl(logprob_join_kernel, dim3((unsigned)((part.tokens + kJoinTokens - 1) / kJoinTokens)), dim3(32 * kJoinTokens), 0, stream, part, o);
         }
         return e;
     };
@@ -488,7 +359,7 @@ extern "C" {
 size_t rar_vocab_logprobs_workspace(size_t tokens, size_t dim, size_t vocab, int p, int top) {
     if (!rar::sizes_ok(tokens, dim, vocab, p) || top < 0 || top > RAR_LOGPROBS_MAX_TOP) return 0;
     rar::VocabArgs k{};
-    return rar::plan(nullptr, tokens, vocab, p, &k);
+    return rar::plan(nullptr, tokens, vocab, p, top, &k);
 }
 
 int rar_vocab_logprobs(rar_handle h, const rar_vocab_logprobs_args *a, void *stream) {

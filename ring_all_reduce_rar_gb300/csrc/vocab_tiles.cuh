@@ -48,8 +48,13 @@ struct VocabArgs {
     int window;           // blocks of a window
     int splits;           // of dhidden's sum over a window
     bool direct;          // one split: the last window writes dhidden itself
-    float *logits;        // [tokens][logits_pitch]
-    long long logits_pitch;
+    // log probabilities: sums and alternatives of each row of tiles' pairs, by half a block's columns
+    int width;                    // rows of tiles that are worked on at a time
+    int pairs;                    // of the launch
+    int stages;                   // of the ring
+    int top;
+    float4 *sums;                 // [2 slots][tokens]: max, S, U (see LogitSums)
+    unsigned long long *lists;    // [2 slots][top][tokens]: keys, in no order
     WaitLimits limits;
 };
 
@@ -109,17 +114,19 @@ __device__ __forceinline__ float g_undo(const VocabArgs &a) {
 }
 
 // What a tile is: statistics of logits (for the cross entropy), G of the cross entropy, the
-// products with G, logits as they are, G of log probabilities.  (_SUMS: see kStepsPerSum)
+// products with G, sums and alternatives of logits (for log probabilities), G of log
+// probabilities.  (_SUMS: see kStepsPerSum)
 enum TileMode {
     TILES_STATS, TILES_G, TILES_DHIDDEN, TILES_DWEIGHT, TILES_STATS_SUMS, TILES_G_SUMS,
-    TILES_LOGITS, TILES_LOGITS_SUMS, TILES_LOGPROB_G, TILES_LOGPROB_G_SUMS
+    TILES_LOGPROB, TILES_LOGPROB_SUMS, TILES_LOGPROB_G, TILES_LOGPROB_G_SUMS
 };
 template <int MODE>
 struct Mode {
-    static constexpr bool sums = MODE == TILES_STATS_SUMS || MODE == TILES_G_SUMS || MODE == TILES_LOGITS_SUMS || MODE == TILES_LOGPROB_G_SUMS;
+    static constexpr bool sums = MODE == TILES_STATS_SUMS || MODE == TILES_G_SUMS || MODE == TILES_LOGPROB_SUMS || MODE == TILES_LOGPROB_G_SUMS;
     static constexpr bool stats = MODE == TILES_STATS || MODE == TILES_STATS_SUMS;
-    static constexpr bool plain = MODE == TILES_LOGITS || MODE == TILES_LOGITS_SUMS, logprob = MODE == TILES_LOGPROB_G || MODE == TILES_LOGPROB_G_SUMS;
-    static constexpr bool g = MODE == TILES_G || MODE == TILES_G_SUMS || logprob, logits = stats || g || plain;
+    // a pair stays with one row of tiles while it walks the vocabulary, and keeps sums and alternatives meanwhile
+    static constexpr bool resident = MODE == TILES_LOGPROB || MODE == TILES_LOGPROB_SUMS, logprob = MODE == TILES_LOGPROB_G || MODE == TILES_LOGPROB_G_SUMS;
+    static constexpr bool g = MODE == TILES_G || MODE == TILES_G_SUMS || logprob, logits = stats || g || resident;
     // whether a row of the operand is a row of K (MN-major); rows of a box; boxes of a stage
     static constexpr bool a_mn = MODE == TILES_DWEIGHT, b_mn = MODE == TILES_DHIDDEN || MODE == TILES_DWEIGHT;
     static constexpr int a_box = a_mn ? 64 : 128, b_box = b_mn ? 64 : 128;
@@ -134,6 +141,8 @@ struct TileItem {
     int block;   // block of the window (not TILES_DHIDDEN)
     int split;
     int k0, k1;  // TILES_DHIDDEN: blocks of the window; else steps of 64
+    int slot;          // resident: the pair's place among those of its row of tiles
+    bool begins, ends; // resident: its first tile of this row, its last
 };
 
 __host__ __device__ inline int tiles_of(long long n) { return (int)((n + kTile - 1) / kTile); }
@@ -177,6 +186,39 @@ template <int MODE>
 __host__ __device__ inline int tile_items(const VocabArgs &a, int nb) {
     const int tb = tiles_of(a.tokens), db = tiles_of(a.dim);
     return MODE == TILES_DHIDDEN ? tb * db * a.splits : MODE == TILES_DWEIGHT ? nb * db : tb * nb;
+}
+
+// Pairs that work on each of `w` rows of tiles at a time.
+__host__ __device__ inline int pairs_a_row(int pairs, int w) { return pairs / w; }
+// Calls f for the tiles of this pair until it returns false.
+template <int MODE, typename F>
+__device__ __forceinline__ void tile_walk(const VocabArgs &a, int b0, int nb, F &&f) {
+    const int pairs = gridDim.x / 2, first = blockIdx.x / 2;
+    if constexpr (!Mode<MODE>::resident) {
+        const int items = tile_items<MODE>(a, nb);
+        for (int i = first; i < items; i += pairs)
+            if (!f(tile_item<MODE>(a, b0, nb, i))) return;
+    } else {
+        const int tb = tiles_of(a.tokens);
+        TileItem o{};
+        o.k1 = (int)((a.dim + 63) / 64);
+        int turn = 0;
+        for (int r0 = 0; r0 < tb; r0 += a.width) {
+            const int w = min(a.width, tb - r0), share = pairs_a_row(pairs, w), slot = first / w;
+            if (slot >= share) continue;
+            o.row = (r0 + first % w) * kTile;
+            o.slot = slot + turn < share ? slot + turn : slot + turn - share;
+            o.begins = true;
+            for (int b = o.slot; b < nb; b += share) {
+                o.block = b;
+                o.n = round32(block_of(a, b0 + b).rows);
+                o.ends = b + share >= nb;
+                if (!f(o)) return;
+                o.begins = false;
+            }
+            turn = (turn + nb) % share;  // the blocks that are left over go to other pairs the next time
+        }
+    }
 }
 
 // Calls f for every step of 64 along K: f(step within the block or the
@@ -225,6 +267,120 @@ __device__ __forceinline__ uint4 narrow8_scaled(const float *v, float scale) {
 // and its time.  Products whose results are rounded to 16 bits do without.
 constexpr int kStepsPerSum = 16;
 
+// Values in the order of their logits, equal ones from the lowest token on: the larger key first.
+// 0 is no value; NaN and -inf have none.
+__device__ __forceinline__ unsigned long long top_key(float z, uint32_t token) {
+    const uint32_t b = __float_as_uint(z + 0.0f);  // (no -0)
+    return (unsigned long long)(b & 0x80000000u ? ~b : b | 0x80000000u) << 32 | (uint32_t)~token;
+}
+__device__ __forceinline__ float top_value(unsigned long long key) {
+    const uint32_t b = (uint32_t)(key >> 32);
+    return __uint_as_float(b & 0x80000000u ? b ^ 0x80000000u : ~b);
+}
+__device__ __forceinline__ uint32_t top_token(unsigned long long key) { return ~(uint32_t)key; }
+
+// exp(scale x) for k = scale log2(e); good to (2 + |scale x|) 2^-23 (see exp_of).
+__device__ __forceinline__ float exp_scaled(float x, float k) {
+    float r;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x * k));
+    return r;
+}
+
+// max, S and U of some logits, S and U relative to the maximum.
+struct LogitSums {
+    float max = -INFINITY, s = 0.0f, u = 0.0f;
+    // moves the maximum up to `top`
+    __device__ __forceinline__ void raise(float top, float k) {
+        const float d = fmaxf(max - top, -1e30f), f = exp_scaled(d, k);  // (from -inf: s and u are 0)
+        u = f * fmaf(d, s, u);
+        s *= f;
+        max = top;
+    }
+    // z[n], of which those that are not there are -inf
+    template <int N>
+    __device__ __forceinline__ void add(const float (&z)[N], float k) {
+        float top = max;
+#pragma unroll
+        for (int i = 0; i < N; i++) top = fmaxf(top, z[i]);
+        if (top > max) raise(top, k);
+        const float ref = top == -INFINITY ? 0.0f : top;  // nothing but -inf, or NaN, which s then shows
+#pragma unroll
+        for (int i = 0; i < N; i++) {
+            const float d = z[i] - ref, e = exp_scaled(d, k);
+            s += e;
+            u = fmaf(e, fmaxf(d, -1e30f), u);  // (-inf: 0 to be added)
+        }
+    }
+    __device__ __forceinline__ void join(float om, float os, float ou, float k) {
+        if (os == 0.0f) return;  // nothing there
+        LogitSums o{om, os, ou};
+        const float top = fmaxf(max, om);
+        if (top != -INFINITY) {
+            raise(top, k);
+            o.raise(top, k);
+        }
+        s += o.s;
+        u += o.u;
+    }
+    // over the lanes, in an order that gives every lane the same bits
+    __device__ __forceinline__ void join_lanes(int lanes, float k) {
+        const int lane = threadIdx.x % 32;
+        for (int d = 1; d < lanes; d *= 2) {
+            const float om = __shfl_xor_sync(0xFFFFFFFFu, max, d), os = __shfl_xor_sync(0xFFFFFFFFu, s, d), ou = __shfl_xor_sync(0xFFFFFFFFu, u, d);
+            if (lane & d) {
+                LogitSums o{om, os, ou};
+                o.join(max, s, u, k);
+                *this = o;
+            } else {
+                join(om, os, ou, k);
+            }
+        }
+    }
+};
+
+// The `most` largest keys that a thread has seen, in shared memory: place i of thread t at
+// [i][t], so that a warp's accesses meet no bank twice.  Columns are looked at 16 at a time: each
+// thread first notes those that may belong into its list, then all threads insert theirs
+// side by side, so that a step of a warp serves all of its rows (column by column, with a step
+// for each column that any of 32 rows wants, there would be several times as many).
+struct TileTop {
+    static constexpr int kNoted = 16, kRow = 32 * kTcEpilogueWarps;
+    unsigned long long *list, *noted;
+    int most, held = 0, worst = 0;      // `worst`: where the least of a full list lies
+    unsigned long long least = 0;       // 0 until the list is full
+    __device__ __forceinline__ TileTop(unsigned long long *at, int top) : list(at + kNoted * kRow), noted(at), most(top) {}
+    __device__ __forceinline__ void clear() { held = 0, worst = 0, least = 0; }
+    __device__ __forceinline__ unsigned long long get(int i) const { return i < held ? list[i * kRow] : 0ull; }
+    __device__ __forceinline__ void add(const float (&v)[32], bool live, uint32_t first) {
+#pragma unroll
+        for (int c0 = 0; c0 < 32; c0 += kNoted) {
+            const float bar = least ? top_value(least) : -INFINITY;
+            float best = v[c0];
+#pragma unroll
+            for (int c = 1; c < kNoted; c++) best = fmaxf(best, v[c0 + c]);
+            // (a later token with the same logit comes after)
+            if (!__any_sync(0xFFFFFFFFu, live && best > bar)) continue;
+            int n = 0;
+#pragma unroll
+            for (int c = 0; c < kNoted; c++)
+                if (live && v[c0 + c] > bar) noted[n++ * kRow] = top_key(v[c0 + c], first + c0 + c);
+            const int steps = __reduce_max_sync(0xFFFFFFFFu, n);
+#pragma unroll 1
+            for (int i = 0; i < steps; i++) {
+                const unsigned long long x = i < n ? noted[i * kRow] : 0ull;
+                if (x <= least) continue;
+                list[(held < most ? held++ : worst) * kRow] = x;
+                if (held < most) continue;
+                least = ~0ull;
+                for (int k = 0; k < most; k++) {
+                    const unsigned long long y = list[k * kRow];
+                    if (y < least) least = y, worst = k;
+                }
+            }
+        }
+    }
+};
+
 // What an epilogue thread keeps of a tile: one row of it.
 struct TileRow {
     int row;          // of tokens (or of the block, TILES_DWEIGHT)
@@ -236,6 +392,7 @@ struct TileRow {
     float w_target;
     bool used;        // the token has a part in the gradients
     float max, sum;   // logits for the statistics
+    int first;        // the vocabulary's row of the half's first column
     char *out;        // where the row's half begins
     float *part;      // TILES_DHIDDEN: the sums so far
 };
@@ -265,9 +422,8 @@ __device__ __forceinline__ TileRow tile_row(const VocabArgs &a, int b0, const Ti
         r.target = y >= 0 && y < r.cols ? (int)y : -1;
         r.max = -INFINITY;
         r.sum = 0.0f;
-        if constexpr (Mode<MODE>::plain) {
-            r.out = reinterpret_cast<char *>(a.logits + row * a.logits_pitch + b.first + half);
-        } else if constexpr (Mode<MODE>::logprob) {
+        r.first = b.first + half;
+        if constexpr (Mode<MODE>::logprob) {
             const int e = g_exponent<DT>(a);
             const float unit = g_unit(a);
             const float da = r.live ? ldexpf(a.row_weight[row] / unit, e) : 0.0f, db = r.live ? ldexpf(a.row_entropy[row] / unit, e) : 0.0f;
@@ -285,6 +441,22 @@ __device__ __forceinline__ TileRow tile_row(const VocabArgs &a, int b0, const Ti
     return r;
 }
 
+// Columns beyond the block's last.
+__device__ __forceinline__ void mask_columns(float (&v)[32], int cols) {
+    if (cols >= 32) return;
+#pragma unroll
+    for (int c = 0; c < 32; c++) v[c] = c < cols ? v[c] : -INFINITY;
+}
+__device__ __forceinline__ void keep_target(const VocabArgs &a, const TileRow &r, int c0, const float (&v)[32]) {
+    const int y = r.target - c0;
+    if (y < 0 || y >= 32) return;
+    float z = 0.0f;
+#pragma unroll
+    for (int c = 0; c < 32; c++)  // (in this form v stays in registers)
+        asm("{\n\t.reg .pred P;\n\tsetp.eq.s32 P, %1, %2;\n\tselp.f32 %0, %3, %0, P;\n\t}" : "+f"(z) : "r"(y), "r"(c), "f"(v[c]));
+    a.z_target[r.row] = z;
+}
+
 // Columns c0 .. c0 + 31 of the row's half.
 template <int MODE, int DT>
 __device__ __forceinline__ void tile_columns(const VocabArgs &a, TileRow &r, int c0, float undo, bool first, bool direct, float (&v)[32]) {
@@ -292,18 +464,8 @@ __device__ __forceinline__ void tile_columns(const VocabArgs &a, TileRow &r, int
     const int cols = r.cols - c0;
     if constexpr (Mode<MODE>::stats) {
         if (cols <= 0) return;
-        if (cols < 32) {
-#pragma unroll
-            for (int c = 0; c < 32; c++) v[c] = c < cols ? v[c] : -INFINITY;
-        }
-        const int y = r.target - c0;
-        if (y >= 0 && y < 32) {
-            float z = 0.0f;
-#pragma unroll
-            for (int c = 0; c < 32; c++)  // (in this form v stays in registers)
-                asm("{\n\t.reg .pred P;\n\tsetp.eq.s32 P, %1, %2;\n\tselp.f32 %0, %3, %0, P;\n\t}" : "+f"(z) : "r"(y), "r"(c), "f"(v[c]));
-            a.z_target[r.row] = z;
-        }
+        mask_columns(v, cols);
+        keep_target(a, r, c0, v);
         float m = r.max;
 #pragma unroll
         for (int c = 0; c < 32; c++) m = fmaxf(m, v[c]);
@@ -314,11 +476,6 @@ __device__ __forceinline__ void tile_columns(const VocabArgs &a, TileRow &r, int
         for (int c = 0; c < 32; c++) s += exp_of(v[c] - ref);
         r.max = m;
         r.sum = s;
-    } else if constexpr (Mode<MODE>::plain) {
-        float *out = reinterpret_cast<float *>(r.out) + c0;
-#pragma unroll
-        for (int c = 0; c < 32; c++)
-            if (c < cols) out[c] = v[c];
     } else if constexpr (Mode<MODE>::g) {
         const int y = r.target - c0;
 #pragma unroll
@@ -392,7 +549,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(152)
     pdl_wait();
     pdl_launch_dependents();
     if (Mode<MODE>::stats && blockIdx.x == 0 && threadIdx.x == 0) *a.w_max = 0u;
-    const int items = tile_items<MODE>(a, nb), pairs = gridDim.x / 2, first = blockIdx.x / 2;
+    const uint32_t ring = Mode<MODE>::resident ? (uint32_t)a.stages : kTcStages;
     constexpr bool a_mn = Mode<MODE>::a_mn, b_mn = Mode<MODE>::b_mn;
     constexpr int kABoxes = Mode<MODE>::a_boxes, kLoaders = kABoxes + Mode<MODE>::b_boxes;
     if (warp == kTcEpilogueWarps && lane < kLoaders) {
@@ -402,8 +559,8 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(152)
         const int part = is_a ? lane * Mode<MODE>::a_box : (lane - kABoxes) * Mode<MODE>::b_box;  // rows (columns) into the operand
         unsigned step = 0;
         uint32_t st = 0, phase = 0;
-        for (int i = first; i < items && !__any_sync(kLanes, *(volatile int *)&sh.failed); i += pairs) {
-            const TileItem it = tile_item<MODE>(a, b0, nb, i);
+        tile_walk<MODE>(a, b0, nb, [&](const TileItem &it) {
+            if (__any_sync(kLanes, *(volatile int *)&sh.failed)) return false;
             tile_steps<MODE>(a, b0, it, [&](int s, int k, const BlockOf &b) {
                 // (a new barrier's preceding phase counts as complete: the first turn does not wait)
                 if (!__all_sync(kLanes, tc_wait(&sh, a.limits, &sh.empty[st], phase ^ 1, 0))) return false;
@@ -422,25 +579,25 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(152)
                 else x = s * 64, y = is_a ? row : b.row + col;
                 if (!is_a || a_rows((int)rank)) tc_load_box(map, to, bar, x, y);
                 step++;
-                if (++st == kTcStages) st = 0, phase ^= 1;
+                if (++st == ring) st = 0, phase ^= 1;
                 return true;
             });
-        }
+            return true;
+        });
         // neither CTA may leave while the pair's loads, products or arrivals are under way,
         // nor give its tensor memory back, even after a wait that ran out: products in flight
         // belong to the last stages, whose `empty` they arrive at in both CTAs
-        for (unsigned k = step > kTcStages ? step - kTcStages : 0; k < step && lane == 0; k++) {
-            const int st = (int)(k % kTcStages);
-            if (rank == 0 && !mbar_drain(&sh.full[st], (k / kTcStages) & 1)) break;
-            if (!mbar_drain(&sh.empty[st], (k / kTcStages) & 1)) break;
+        for (unsigned k = step > ring ? step - ring : 0; k < step && lane == 0; k++) {
+            const int st = (int)(k % ring);
+            if (rank == 0 && !mbar_drain(&sh.full[st], (k / ring) & 1)) break;
+            if (!mbar_drain(&sh.empty[st], (k / ring) & 1)) break;
         }
     } else if (warp == kTcEpilogueWarps + 1 && lane == 0 && rank == 0) {
         const uint64_t operand_a = tc_operand(stages, a_mn ? 8192 : 16, 1024), operand_b = tc_operand(stages + 16384, b_mn ? 8192 : 16, 1024);
         // the next stage and its phase; accumulators begun.  (This thread issues a step of 64
         // every 512 cycles or so: what it computes between two steps is time lost.)
         uint32_t st = 0, phase = 0, sums = 0;
-        for (int i = first; i < items; i += pairs) {
-            const TileItem it = tile_item<MODE>(a, b0, nb, i);
+        tile_walk<MODE>(a, b0, nb, [&](const TileItem &it) {
             const uint32_t idesc = tc_instruction(DT == DT_BF16, a_mn, b_mn, (uint32_t)it.n);
             uint32_t d = 0;
             int left = 0;  // steps that the present accumulator takes yet
@@ -465,13 +622,13 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(152)
                     more = true;
                 }
                 tc_commit(&sh.empty[st]);
-                if (++st == kTcStages) st = 0, phase ^= 1;
+                if (++st == ring) st = 0, phase ^= 1;
                 left--;
                 return true;
             });
-            if (!ok) break;
-            tc_commit(&sh.acc_full[(sums - 1) & 1]);
-        }
+            if (ok) tc_commit(&sh.acc_full[(sums - 1) & 1]);
+            return ok;
+        });
     } else if (warp < kTcEpilogueWarps) {
         const int quarter = warp % 4;
         const float undo = MODE == TILES_DHIDDEN || MODE == TILES_DWEIGHT ? g_undo<DT>(a) : 1.0f;
@@ -488,9 +645,10 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(152)
             if (lane == 0) tc_arrive_cluster(peer_addr(smem_u32(&sh.acc_empty[sums & 1]), 0));
             sums++;
         };
-        bool ok = true;
-        for (int i = first; i < items; i += pairs) {
-            const TileItem it = tile_item<MODE>(a, b0, nb, i);
+        [[maybe_unused]] LogitSums own;
+        [[maybe_unused]] TileTop top(reinterpret_cast<unsigned long long *>(dyn + (stages - smem_u32(dyn)) + ring * kTcStageBytes) + threadIdx.x, a.top);
+        tile_walk<MODE>(a, b0, nb, [&](const TileItem &it) {
+            bool ok = true;
             const int half = warp / 4 * 128, row = it.row + (int)rank * 128 + quarter * 32 + lane;
             TileRow r = tile_row<MODE, DT>(a, b0, it, row, half);
             auto at = [&](int c) { return sh.tmem + ((uint32_t)quarter << 21) + (sums & 1) * kTile + half + c; };
@@ -512,7 +670,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(152)
                     }
                     release();
                 }
-                if (!ok || !(ok = ready())) break;
+                if (!ok || !ready()) return false;
 #pragma unroll
                 for (int q = 0; q < 128; q += 8) {
                     float v[8];
@@ -523,20 +681,37 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(152)
                     tc_write8(at(q), v);
                 }
                 tc_write_wait();
-            } else if (!(ok = ready())) {
-                break;
+            } else if (!ready()) {
+                return false;
             }
+            if constexpr (Mode<MODE>::resident)
+                if (it.begins) own = LogitSums(), top.clear();
 #pragma unroll 1
             for (int c0 = 0; c0 < 128; c0 += 32) {
                 float v[32];
                 tc_read32(at(c0), v);
                 tc_read_wait();
-                tile_columns<MODE, DT>(a, r, c0, undo, first_window, direct, v);
+                if constexpr (Mode<MODE>::resident) {
+                    if (r.cols - c0 <= 0) break;  // (the same for the whole warp)
+                    mask_columns(v, r.cols - c0);
+                    keep_target(a, r, c0, v);
+                    own.add(v, a.scale * 1.4426950408889634f);
+                    if (a.top) top.add(v, r.live, (uint32_t)(r.first + c0));
+                } else {
+                    tile_columns<MODE, DT>(a, r, c0, undo, first_window, direct, v);
+                }
             }
             release();
             if constexpr (Mode<MODE>::stats)
                 if (r.live) a.stats[(2ll * (b0 + it.block) + half / 128) * a.tokens + row] = make_float2(r.max, r.sum);
-        }
+            if constexpr (Mode<MODE>::resident)
+                if (it.ends && r.live) {
+                    const long long list = 2ll * it.slot + half / 128;
+                    a.sums[list * a.tokens + row] = make_float4(own.max, own.s, own.u, 0.0f);
+                    for (int i = 0; i < a.top; i++) a.lists[(list * a.top + i) * a.tokens + row] = top.get(i);
+                }
+            return true;
+        });
     }
     __syncwarp();
     tc_end(&sh);
@@ -602,13 +777,21 @@ bool make_map(CUtensorMap *m, int dtype, const void *ptr, long long rows, long l
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Shared memory of the alternatives' lists.
+constexpr int list_bytes(int top) { return top ? (top + TileTop::kNoted) * TileTop::kRow * 8 : 0; }
+constexpr int kMaxTileSmem = 4 * kTcStageBytes + 1024 + list_bytes(RAR_LOGPROBS_MAX_TOP);
+static_assert(kMaxTileSmem <= 226 * 1024, "the lists leave four stages");
+// Stages that fit beside them.
+constexpr int stages_beside(int top) { return std::min(kTcStages, (kMaxTileSmem - 1024 - list_bytes(top)) / kTcStageBytes); }
+
 template <int MODE, int DT>
 cudaError_t launch_tiles(const rar_ctx *h, const VocabArgs &k, const VocabMaps &maps, int b0, int nb, cudaStream_t stream) {
     auto kern = vocab_tile_kernel<MODE, DT>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcSmem);
+    const int pairs = Mode<MODE>::resident ? k.pairs : std::min(tile_items<MODE>(k, nb), h->sm_count / 2);
+    const int smem = Mode<MODE>::resident ? k.stages * kTcStageBytes + 1024 + list_bytes(k.top) : kTcSmem;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Mode<MODE>::resident ? kMaxTileSmem : kTcSmem);
     if (e != cudaSuccess) return e;
-    const int pairs = std::min(tile_items<MODE>(k, nb), h->sm_count / 2);
-    return launch_pdl(kern, dim3((unsigned)(2 * pairs)), dim3(kTcThreads), kTcSmem, stream, k, maps, b0, nb);
+    return launch_pdl(kern, dim3((unsigned)(2 * pairs)), dim3(kTcThreads), (size_t)smem, stream, k, maps, b0, nb);
 }
 
 void plan_blocks(size_t vocab, int p, VocabArgs *k) {

@@ -534,7 +534,7 @@ def test_refusals(h):  # noqa: F811
         assert e.value.code == code
     # through the C call: a short workspace, an output that lies on an input, alternatives without a place
     lib, stream = rar.load_library(), torch.cuda.current_stream().cuda_stream
-    need = lib.rar_vocab_logprobs_workspace(4, 64, 4, 1, 2)
+    need = lib.rar_vocab_logprobs_workspace(4, 64, 4, 1, 0)
     ws, out = torch.empty(need, dtype=torch.uint8, device="cuda"), torch.empty(8, device="cuda")
     wp = (ctypes.c_void_p * 1)(half.data_ptr())
 
