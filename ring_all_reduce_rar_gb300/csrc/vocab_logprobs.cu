@@ -25,7 +25,13 @@ struct TopList {
     // takes the lanes' keys; 0 where a lane has none
     __device__ __forceinline__ void add(unsigned long long x, int top) {
         const int lane = threadIdx.x % 32;
-        for (unsigned more = __ballot_sync(0xFFFFFFFFu, x > least); more; more &= more - 1) {
+        unsigned more = __ballot_sync(0xFFFFFFFFu, x > least);
+        if (__popc(more) > 6) {  // sorted and merged, 20 steps: as much as inserting six
+            merge(sorted(x));
+            least = __shfl_sync(0xFFFFFFFFu, key, top - 1);
+            return;
+        }
+        for (; more; more &= more - 1) {
             const unsigned long long y = __shfl_sync(0xFFFFFFFFu, x, __ffs(more) - 1);
             if (y <= least) continue;
             const int at = __popc(__ballot_sync(0xFFFFFFFFu, key > y));
@@ -35,16 +41,26 @@ struct TopList {
         }
     }
     // takes another list: of two falling runs, one turned round, the larger ones of each
-    // place are the 32 largest of all, rising and falling once (Batcher's merge)
+    // place are the 32 largest of all, in a bitonic order
     __device__ __forceinline__ void merge(unsigned long long other) {
+        const unsigned long long x = __shfl_sync(0xFFFFFFFFu, other, 31 - threadIdx.x % 32);
+        key = fall(key > x ? key : x, 32);
+    }
+    // runs of n keys in a bitonic order, into falling order (rising ones where lane & n)
+    __device__ static __forceinline__ unsigned long long fall(unsigned long long x, int n) {
         const int lane = threadIdx.x % 32;
-        const unsigned long long x = __shfl_sync(0xFFFFFFFFu, other, 31 - lane);
-        key = key > x ? key : x;
-#pragma unroll
-        for (int d = 16; d; d /= 2) {
-            const unsigned long long y = __shfl_xor_sync(0xFFFFFFFFu, key, d);
-            key = ((lane & d) == 0) == (key > y) ? key : y;
+        for (int d = n / 2; d; d /= 2) {
+            const unsigned long long y = __shfl_xor_sync(0xFFFFFFFFu, x, d);
+            const bool first = ((lane & d) == 0) == ((lane & n) == 0);
+            x = first == (x > y) ? x : y;
         }
+        return x;
+    }
+    // in falling order (Batcher's bitonic sort)
+    __device__ static __forceinline__ unsigned long long sorted(unsigned long long x) {
+#pragma unroll
+        for (int n = 2; n <= 32; n *= 2) x = fall(x, n);
+        return x;
     }
 };
 
@@ -75,37 +91,52 @@ __device__ __forceinline__ void write_token(const LogprobOut &o, long long t, co
     }
 }
 
-// Results from the pairs' sums and alternatives, a warp a token.
-constexpr int kJoinTokens = 4;
-__global__ void __launch_bounds__(32 * kJoinTokens) logprob_join_kernel(const __grid_constant__ VocabArgs a, const __grid_constant__ LogprobOut o) {
+// Results from the pairs' sums and alternatives.  SHARED: by a CTA of warps a token, for few tokens
+// (which have the longer lists), else by a warp a token.
+constexpr int kJoinWarps = 4;
+template <bool SHARED>
+__global__ void __launch_bounds__(32 * kJoinWarps) logprob_join_kernel(const __grid_constant__ VocabArgs a, const __grid_constant__ LogprobOut o) {
+    constexpr int kWarps = SHARED ? kJoinWarps : 1;
+    __shared__ unsigned long long found[kJoinWarps][32];
     pdl_wait();
     pdl_launch_dependents();
-    const int lane = threadIdx.x % 32;
-    const long long t = (long long)blockIdx.x * kJoinTokens + threadIdx.x / 32;
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, part = SHARED ? warp : 0;
+    const long long t = SHARED ? (long long)blockIdx.x : (long long)blockIdx.x * kJoinWarps + warp;
     if (t >= a.tokens) return;
     const float k = a.scale * 1.4426950408889634f;
     const int tb = tiles_of(a.tokens), r0 = (int)(t / kTile) / a.width * a.width;
     const int lists = 2 * min(pairs_a_row(a.pairs, min(a.width, tb - r0)), a.n_blocks);
-    const long long y = load_index(o.targets, o.index_bytes, t);
-    const float z = y >= 0 && y < a.vocab ? a.z_target[t] : 0.0f;
     LogitSums own;
-    for (int i = lane; i < lists; i += 32) {
-        const float4 q = __ldcg(a.sums + (long long)i * a.tokens + t);
-        own.join(q.x, q.y, q.z, k);
+    float z = 0.0f;
+    if (part == 0) {
+        const long long y = load_index(o.targets, o.index_bytes, t);
+        z = y >= 0 && y < a.vocab ? a.z_target[t] : 0.0f;
+        for (int i = lane; i < lists; i += 32) {
+            const float4 q = __ldcg(a.sums + (long long)i * a.tokens + t);
+            own.join(q.x, q.y, q.z, k);
+        }
     }
-    own.join_lanes(32, k);
     TopList list;
     const int n = lists * a.top;
-    for (int i0 = 0; i0 < n; i0 += 32 * 4) {
-        unsigned long long x[4];  // loads in flight together
+    for (int i0 = part * 32; i0 < n; i0 += 32 * kWarps * 8) {
+        unsigned long long x[8];  // loads in flight together
 #pragma unroll
-        for (int u = 0; u < 4; u++) {
-            const int i = i0 + u * 32 + lane;
+        for (int u = 0; u < 8; u++) {
+            const int i = i0 + u * 32 * kWarps + lane;
             x[u] = i < n ? __ldcg(a.lists + (long long)i * a.tokens + t) : 0ull;
         }
 #pragma unroll
-        for (int u = 0; u < 4; u++) list.add(x[u], a.top);
+        for (int u = 0; u < 8; u++)
+            if (i0 + u * 32 * kWarps < n) list.add(x[u], a.top);
     }
+    if (SHARED && a.top) {
+        found[warp][lane] = list.key;
+        __syncthreads();
+        if (warp == 0)
+            for (int w = 1; w < kWarps; w++) list.merge(found[w][lane]);
+    }
+    if (part) return;
+    own.join_lanes(32, k);
     write_token(o, t, own, z, list.key);
 }
 
@@ -145,6 +176,9 @@ __global__ void __launch_bounds__(32 * kPrepareTokens) logprob_prepare_kernel(co
 
 namespace {
 
+// Tokens for which a CTA joins a token's lists: 256 tokens of one row of tiles have up to 152 lists, 2048
+// of 8 rows 38.
+constexpr long long kSharedJoin = 1024;
 // Tokens of a pass over the pieces: bounds the workspace.
 constexpr size_t kPassTokens = 16384;
 
@@ -283,7 +317,9 @@ int vocab_logprobs(rar_ctx *h, const rar_vocab_logprobs_args *a, cudaStream_t st
             LogprobOut o{k.vocab, k.scale, a->top, part.targets, k.index_bytes, at(a->logprob), at(a->entropy), at(a->lse), nullptr, nullptr};
             if (a->top) o.top_logprob = a->top_logprob + t0 * a->top, o.top_token = a->top_token + t0 * a->top;
             if (e == cudaSuccess)
-                e = launch_pdl(logprob_join_kernel, dim3((unsigned)((part.tokens + kJoinTokens - 1) / kJoinTokens)), dim3(32 * kJoinTokens), 0, stream, part, o);
+                e = part.tokens <= kSharedJoin
+                        ? launch_pdl(logprob_join_kernel<true>, dim3((unsigned)part.tokens), dim3(32 * kJoinWarps), 0, stream, part, o)
+                        : launch_pdl(logprob_join_kernel<false>, dim3((unsigned)((part.tokens + kJoinWarps - 1) / kJoinWarps)), dim3(32 * kJoinWarps), 0, stream, part, o);
         }
         return e;
     };

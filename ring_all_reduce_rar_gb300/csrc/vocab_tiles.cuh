@@ -338,46 +338,116 @@ struct LogitSums {
     }
 };
 
-// The `most` largest keys that a thread has seen, in shared memory: place i of thread t at
-// [i][t], so that a warp's accesses meet no bank twice.  Columns are looked at 16 at a time: each
-// thread first notes those that may belong into its list, then all threads insert theirs
-// side by side, so that a step of a warp serves all of its rows (column by column, with a step
-// for each column that any of 32 rows wants, there would be several times as many).
-struct TileTop {
-    static constexpr int kNoted = 16, kRow = 32 * kTcEpilogueWarps;
-    unsigned long long *list, *noted;
-    int most, held = 0, worst = 0;      // `worst`: where the least of a full list lies
-    unsigned long long least = 0;       // 0 until the list is full
-    __device__ __forceinline__ TileTop(unsigned long long *at, int top) : list(at + kNoted * kRow), noted(at), most(top) {}
-    __device__ __forceinline__ void clear() { held = 0, worst = 0, least = 0; }
-    __device__ __forceinline__ unsigned long long get(int i) const { return i < held ? list[i * kRow] : 0ull; }
-    __device__ __forceinline__ void add(const float (&v)[32], bool live, uint32_t first) {
+// Bounds of the k-th largest of a row's columns: the least of the maxima of k groups of them.
+struct GroupMaxima {
+    float most = -INFINITY, least4 = INFINITY, least8 = INFINITY, least16 = INFINITY;  // of all, of groups of 4, 8, 16
+    __device__ __forceinline__ void add(const float (&v)[32]) {
+        float m4[8];
 #pragma unroll
-        for (int c0 = 0; c0 < 32; c0 += kNoted) {
-            const float bar = least ? top_value(least) : -INFINITY;
-            float best = v[c0];
-#pragma unroll
-            for (int c = 1; c < kNoted; c++) best = fmaxf(best, v[c0 + c]);
-            // (a later token with the same logit comes after)
-            if (!__any_sync(0xFFFFFFFFu, live && best > bar)) continue;
-            int n = 0;
-#pragma unroll
-            for (int c = 0; c < kNoted; c++)
-                if (live && v[c0 + c] > bar) noted[n++ * kRow] = top_key(v[c0 + c], first + c0 + c);
-            const int steps = __reduce_max_sync(0xFFFFFFFFu, n);
-#pragma unroll 1
-            for (int i = 0; i < steps; i++) {
-                const unsigned long long x = i < n ? noted[i * kRow] : 0ull;
-                if (x <= least) continue;
-                list[(held < most ? held++ : worst) * kRow] = x;
-                if (held < most) continue;
-                least = ~0ull;
-                for (int k = 0; k < most; k++) {
-                    const unsigned long long y = list[k * kRow];
-                    if (y < least) least = y, worst = k;
-                }
-            }
+        for (int i = 0; i < 8; i++) {
+            m4[i] = fmaxf(fmaxf(v[4 * i], v[4 * i + 1]), fmaxf(v[4 * i + 2], v[4 * i + 3]));
+            least4 = fminf(least4, m4[i]);
         }
+#pragma unroll
+        for (int i = 0; i < 8; i += 4) {
+            const float a = fmaxf(m4[i], m4[i + 1]), b = fmaxf(m4[i + 2], m4[i + 3]), c = fmaxf(a, b);
+            least8 = fminf(least8, fminf(a, b));
+            least16 = fminf(least16, c);
+            most = fmaxf(most, c);
+        }
+    }
+    // a logit below this is not among the `top` largest of 128
+    __device__ __forceinline__ float bound(int top) const { return top == 1 ? most : top <= 8 ? least16 : top <= 16 ? least8 : least4; }
+};
+
+// The `top` largest keys that a thread has seen, in shared memory: place i of thread t at
+// [i][t], so that a warp's accesses meet no bank twice.  Each thread first notes the columns
+// that may belong into its list; when one has noted many, and at the end of a tile, all insert theirs
+// side by side, so that a step of a warp serves all of its rows (column by column, with a step for each
+// column that any of 32 rows wants, there would be several times as many).  A new key takes
+// the place of the least one; which is the least then is known from the 8 places around and the other
+// groups' least, in registers.
+struct TileTop {
+    static constexpr int kNoted = 24, kRow = 32 * kTcEpilogueWarps, kGroups = RAR_LOGPROBS_MAX_TOP / 8;
+    static constexpr int kNotedBytes = kNoted * kRow * 5;
+    uint32_t noted, column, list;       // shared-memory addresses: logits and columns noted, keys
+    uint32_t next;                      // where the next logit is noted
+    unsigned long long group[kGroups];  // least keys of 8 places each
+    unsigned long long least;           // of all: 0 until the list is full
+    uint32_t at;                        // its place, in bits 0 to 7; that of group g in bits 8 + 3 g and on
+    __device__ __forceinline__ TileTop(uint32_t addr)
+        : noted(addr + threadIdx.x * 4), column(addr + kNoted * kRow * 4 + threadIdx.x), list(addr + kNotedBytes + threadIdx.x * 8), next(noted) {}
+    static __device__ __forceinline__ unsigned long long load(uint32_t addr) {
+        unsigned long long x;
+        asm volatile("ld.shared.u64 %0, [%1];" : "=l"(x) : "r"(addr));
+        return x;
+    }
+    static __device__ __forceinline__ void store(uint32_t addr, unsigned long long x) { asm volatile("st.shared.u64 [%0], %1;" ::"r"(addr), "l"(x) : "memory"); }
+    // places beyond `top` hold what is never the least
+    __device__ __forceinline__ void clear(int top) {
+        const int places = (top + 7) / 8 * 8;
+        for (int i = 0; i < places; i++) store(list + i * kRow * 8, i < top ? 0ull : ~0ull);
+#pragma unroll
+        for (int g = 0; g < kGroups; g++) group[g] = g * 8 < top ? 0ull : ~0ull;
+        least = 0;
+        at = 0;
+    }
+    __device__ __forceinline__ unsigned long long get(int i) const { return load(list + i * kRow * 8); }
+    __device__ __forceinline__ void insert(unsigned long long x) {
+        if (x <= least) return;
+        const uint32_t place = at & 0xFFu, g = place / 8;
+        store(list + place * kRow * 8, x);
+        unsigned long long y[8];
+#pragma unroll
+        for (int i = 0; i < 8; i++) y[i] = load(list + (g * 8 + i) * kRow * 8);
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            w[i] = y[2 * i + 1] < y[2 * i] ? 2 * i + 1 : 2 * i;
+            y[i] = y[2 * i + 1] < y[2 * i] ? y[2 * i + 1] : y[2 * i];
+        }
+        w[0] = y[1] < y[0] ? w[1] : w[0], y[0] = y[1] < y[0] ? y[1] : y[0];
+        w[2] = y[3] < y[2] ? w[3] : w[2], y[2] = y[3] < y[2] ? y[3] : y[2];
+        w[0] = y[2] < y[0] ? w[2] : w[0], y[0] = y[2] < y[0] ? y[2] : y[0];
+        at = (at & ~(7u << (8 + 3 * g)) & ~0xFFu) | w[0] << (8 + 3 * g);
+        uint32_t worst = 0;
+#pragma unroll
+        for (int i = 0; i < kGroups; i++) {
+            group[i] = g == i ? y[0] : group[i];
+            if (i == 0 || group[i] < least) least = group[i], worst = i;
+        }
+        at |= worst * 8 + (at >> (8 + 3 * worst) & 7u);
+    }
+    // what has to be passed to get into the list
+    __device__ __forceinline__ float bar() const { return least ? top_value(least) : -INFINITY; }
+    // columns c0 .. c0 + 31 of a row whose first is `first`, of which those up to `bound` are not wanted (infinity: none is)
+    __device__ __forceinline__ void add(const float (&v)[32], float bound, int c0, uint32_t first) {
+#pragma unroll
+        for (int h = 0; h < 32; h += 16) {
+            const float over = fmaxf(bar(), bound);
+            uint32_t where = column + (next - noted) / 4;
+#pragma unroll
+            for (int c = h; c < h + 16; c++)
+                asm volatile("{\n\t.reg .pred P;\n\tsetp.gt.f32 P, %2, %3;\n\t@P st.shared.f32 [%0], %2;\n\t@P st.shared.u8 [%1], %6;\n\t"
+                             "@P add.u32 %0, %0, %4;\n\t@P add.u32 %1, %1, %5;\n\t}"
+                             : "+r"(next), "+r"(where)
+                             : "f"(v[c]), "f"(over), "n"(kRow * 4), "n"(kRow), "r"(c0 + c)
+                             : "memory");
+            if (__any_sync(0xFFFFFFFFu, next > noted + (kNoted - 16) * kRow * 4)) insert_noted(first);
+        }
+    }
+    __device__ __forceinline__ void insert_noted(uint32_t first) {
+        const int n = (int)(next - noted) / (kRow * 4), steps = __reduce_max_sync(0xFFFFFFFFu, n);
+#pragma unroll 1
+        for (int i = 0; i < steps; i++)
+            if (i < n) {
+                float x;
+                uint32_t c;
+                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(noted + i * kRow * 4));
+                asm volatile("ld.shared.u8 %0, [%1];" : "=r"(c) : "r"(column + i * kRow));
+                insert(top_key(x, first + c));
+            }
+        next = noted;
     }
 };
 
@@ -646,7 +716,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(152)
             sums++;
         };
         [[maybe_unused]] LogitSums own;
-        [[maybe_unused]] TileTop top(reinterpret_cast<unsigned long long *>(dyn + (stages - smem_u32(dyn)) + ring * kTcStageBytes) + threadIdx.x, a.top);
+        [[maybe_unused]] TileTop top(stages + ring * kTcStageBytes);
         tile_walk<MODE>(a, b0, nb, [&](const TileItem &it) {
             bool ok = true;
             const int half = warp / 4 * 128, row = it.row + (int)rank * 128 + quarter * 32 + lane;
@@ -685,7 +755,11 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(152)
                 return false;
             }
             if constexpr (Mode<MODE>::resident)
-                if (it.begins) own = LogitSums(), top.clear();
+                if (it.begins) {
+                    own = LogitSums();
+                    if (a.top) top.clear(a.top);
+                }
+            [[maybe_unused]] GroupMaxima groups;
 #pragma unroll 1
             for (int c0 = 0; c0 < 128; c0 += 32) {
                 float v[32];
@@ -696,9 +770,26 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(152)
                     mask_columns(v, r.cols - c0);
                     keep_target(a, r, c0, v);
                     own.add(v, a.scale * 1.4426950408889634f);
-                    if (a.top) top.add(v, r.live, (uint32_t)(r.first + c0));
+                    if (a.top) groups.add(v);
                 } else {
                     tile_columns<MODE, DT>(a, r, c0, undo, first_window, direct, v);
+                }
+            }
+            if constexpr (Mode<MODE>::resident) {
+                // a second look, where a row of the warp has a column for its list
+                if (a.top && __any_sync(0xFFFFFFFFu, r.live && groups.most > top.bar())) {
+                    // (a bound that is itself a logit counts; columns beyond the block's last bound nothing)
+                    const float bound = !r.live ? INFINITY : r.cols < 128 ? -INFINITY : nextafterf(groups.bound(a.top), -INFINITY);
+#pragma unroll 1
+                    for (int c0 = 0; c0 < 128; c0 += 32) {
+                        if (r.cols - c0 <= 0) break;
+                        float v[32];
+                        tc_read32(at(c0), v);
+                        tc_read_wait();
+                        mask_columns(v, r.cols - c0);
+                        top.add(v, bound, c0, (uint32_t)r.first);
+                    }
+                    top.insert_noted((uint32_t)r.first);
                 }
             }
             release();
@@ -778,18 +869,17 @@ bool make_map(CUtensorMap *m, int dtype, const void *ptr, long long rows, long l
 }
 
 // Shared memory of the alternatives' lists.
-constexpr int list_bytes(int top) { return top ? (top + TileTop::kNoted) * TileTop::kRow * 8 : 0; }
-constexpr int kMaxTileSmem = 4 * kTcStageBytes + 1024 + list_bytes(RAR_LOGPROBS_MAX_TOP);
-static_assert(kMaxTileSmem <= 226 * 1024, "the lists leave four stages");
-// Stages that fit beside them.
-constexpr int stages_beside(int top) { return std::min(kTcStages, (kMaxTileSmem - 1024 - list_bytes(top)) / kTcStageBytes); }
+constexpr int list_bytes(int top) { return top ? (top + 7) / 8 * 8 * TileTop::kRow * 8 + TileTop::kNotedBytes : 0; }
+// Stages that fit beside them (2048 tokens by 50021 x 2048 fp16 take the same time with 4 to 7).
+constexpr int stages_beside(int top) { return (kTcSmem - 1024 - list_bytes(top)) / kTcStageBytes; }
+static_assert(stages_beside(RAR_LOGPROBS_MAX_TOP) >= 4 && stages_beside(0) == kTcStages, "the lists leave four stages");
 
 template <int MODE, int DT>
 cudaError_t launch_tiles(const rar_ctx *h, const VocabArgs &k, const VocabMaps &maps, int b0, int nb, cudaStream_t stream) {
     auto kern = vocab_tile_kernel<MODE, DT>;
     const int pairs = Mode<MODE>::resident ? k.pairs : std::min(tile_items<MODE>(k, nb), h->sm_count / 2);
     const int smem = Mode<MODE>::resident ? k.stages * kTcStageBytes + 1024 + list_bytes(k.top) : kTcSmem;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Mode<MODE>::resident ? kMaxTileSmem : kTcSmem);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcSmem);
     if (e != cudaSuccess) return e;
     return launch_pdl(kern, dim3((unsigned)(2 * pairs)), dim3(kTcThreads), (size_t)smem, stream, k, maps, b0, nb);
 }
