@@ -15,7 +15,7 @@
 // made once: 6 tokens x vocab x dim operations in all.
 #include <cmath>
 
-#include "vocab_tiles.cuh"
+#include "vocab_stream.cuh"
 
 namespace rar {
 
@@ -88,6 +88,92 @@ __device__ __forceinline__ void write_token(const LogprobOut &o, long long t, co
     if (lane < o.top) {
         o.top_token[t * o.top + lane] = key ? (long long)top_token(key) : -1ll;
         o.top_logprob[t * o.top + lane] = key ? fmaf(o.scale, top_value(key) - sums.max, -log_s) : -INFINITY;
+    }
+}
+
+struct SelectArgs {
+    LogprobOut out;
+    const float *logits;  // [tokens][pitch], 16-byte aligned rows
+    long long pitch;
+};
+
+constexpr int kSelectWarps = 8, kSelectCluster = 8;
+
+// Everything about a token from its logits, for few tokens: a cluster of CTAs a token, each with a range
+// of the vocabulary, whose warps keep sums and a list of their own.
+__global__ void __launch_bounds__(32 * kSelectWarps) logprob_select_kernel(const __grid_constant__ SelectArgs a) {
+    __shared__ unsigned long long lists[kSelectWarps][32];
+    __shared__ float3 sums[kSelectWarps];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, top = a.out.top;
+    const uint32_t rank = cluster_rank(), ctas = gridDim.x;
+    const long long t = blockIdx.y;
+    const float k = a.out.scale * 1.4426950408889634f;
+    pdl_wait();
+    pdl_launch_dependents();
+    const float *row = a.logits + t * a.pitch;
+    const uint32_t vocab = (uint32_t)a.out.vocab, vecs = (vocab + 3) / 4;
+    const uint32_t v0 = (uint32_t)((unsigned long long)vecs * rank / ctas), v1 = (uint32_t)((unsigned long long)vecs * (rank + 1) / ctas);
+    LogitSums own;
+    TopList list;
+    for (uint32_t v = v0 + warp * 32; v < v1; v += 32 * kSelectWarps) {
+        const bool has = v + lane < v1;
+        float4 q = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        if (has) q = __ldcg(reinterpret_cast<const float4 *>(row) + v + lane);
+        const uint32_t first = (v + lane) * 4;
+        float z[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int e = 0; e < 4; e++)
+            if (first + e >= vocab) z[e] = -INFINITY;
+        own.add(z, k);
+        if (top) {
+            const float least = list.least ? top_value(list.least) : -INFINITY;
+            // (NaN is below everything here)
+            if (__any_sync(0xFFFFFFFFu, fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])) >= least))
+#pragma unroll
+                for (int e = 0; e < 4; e++) list.add(z[e] > -INFINITY ? top_key(z[e], first + e) : 0ull, top);
+        }
+    }
+    own.join_lanes(32, k);
+    lists[warp][lane] = list.key;
+    if (lane == 0) sums[warp] = make_float3(own.max, own.s, own.u);
+    // the CTA's, and then the cluster's, in warp 0 of its first CTA
+    auto join = [&](int n) {
+        for (int d = 1; d < n; d *= 2) {
+            __syncthreads();
+            if (top && warp % (2 * d) == 0 && warp + d < n) {
+                list.merge(lists[warp + d][lane]);
+                lists[warp][lane] = list.key;
+            }
+        }
+        __syncthreads();
+        if (warp == 0) {
+            own = LogitSums();
+            if (lane < n) own.join(sums[lane].x, sums[lane].y, sums[lane].z, k);
+            own.join_lanes(32, k);
+        }
+    };
+    join(kSelectWarps);
+    if (ctas > 1) {
+        if (warp == 0 && lane == 0) sums[0] = make_float3(own.max, own.s, own.u);
+        cluster_sync_all();
+        list.key = 0;
+        float3 other = make_float3(-INFINITY, 0.0f, 0.0f);
+        if (rank == 0 && warp < (int)ctas) {
+            const uint32_t at = peer_addr(smem_u32(&lists[0][lane]), (uint32_t)warp), st = peer_addr(smem_u32(&sums[0]), (uint32_t)warp);
+            asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(list.key) : "r"(at) : "memory");
+            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(other.x) : "r"(st) : "memory");
+            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(other.y) : "r"(st + 4) : "memory");
+            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(other.z) : "r"(st + 8) : "memory");
+        }
+        cluster_sync_all();  // all of it is read: the others may end, and this one may write
+        if (rank) return;
+        lists[warp][lane] = list.key;
+        if (lane == 0) sums[warp] = other;
+        join((int)ctas);
+    }
+    if (warp == 0) {
+        const long long y = load_index(a.out.targets, a.out.index_bytes, t);
+        write_token(a.out, t, own, y >= 0 && y < a.out.vocab ? __ldcg(row + y) : 0.0f, list.key);
     }
 }
 
@@ -197,9 +283,14 @@ int choose_width(int tb, int nb, int pairs) {
     return best;
 }
 
-size_t plan(void *base, size_t tokens, size_t vocab, int p, int top, VocabArgs *k) {
+size_t plan(void *base, size_t tokens, size_t dim, size_t vocab, int p, int top, VocabArgs *k, float **logits) {
     WorkspacePlan w(base);
     plan_blocks(vocab, p, k);
+    *logits = nullptr;
+    if (stream_fits(tokens, dim)) {
+        *logits = w.take<float>(tokens * stream_pitch(vocab));
+        return w.used;
+    }
     const size_t pass = std::min(tokens, kPassTokens);
     k->window = (int)pass;
     if (tokens) {
@@ -267,6 +358,26 @@ void set_inputs(rar_ctx *h, const Args *a, VocabArgs *k) {
 }
 struct Vec { const char *name; const void *ptr; size_t n, eb; };
 
+cudaError_t launch_select(const rar_ctx *h, const SelectArgs &s, int tokens, cudaStream_t stream) {
+    // CTAs a token: until there are two an SM, but at least 1024 logits each
+    unsigned ctas = 1;
+    while (ctas < kSelectCluster && tokens * (int)ctas < 2 * h->sm_count && s.out.vocab / (2 * ctas) >= 1024) ctas *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas, (unsigned)tokens);
+    cfg.blockDim = dim3(32 * kSelectWarps);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = ctas;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, logprob_select_kernel, s);
+}
+
 int vocab_logprobs(rar_ctx *h, const rar_vocab_logprobs_args *a, cudaStream_t stream) {
     OpCheck c(h, "rar_vocab_logprobs");
     int rc = check_inputs(c, a);
@@ -284,17 +395,31 @@ int vocab_logprobs(rar_ctx *h, const rar_vocab_logprobs_args *a, cudaStream_t st
         c.output(s);
     }
     VocabArgs k{};
-    const size_t need = plan(nullptr, a->tokens, a->vocab, a->p, a->top, &k);
+    float *logits;
+    const size_t need = plan(nullptr, a->tokens, a->dim, a->vocab, a->p, a->top, &k, &logits);
     if ((rc = c.workspace(a->workspace, a->workspace_bytes, need)) != RAR_OK) return rc;
     if ((rc = c.overlaps([](const MatrixSpan &, const MatrixSpan &) { return false; })) != RAR_OK) return rc;
     if (a->tokens == 0) return RAR_OK;
 
     DeviceGuard dg(h->device);
     if (dg.err != cudaSuccess) return cuda_fail(h, dg.err, "selecting the device");
-    plan(a->workspace, a->tokens, a->vocab, a->p, a->top, &k);
+    plan(a->workspace, a->tokens, a->dim, a->vocab, a->p, a->top, &k, &logits);
     set_inputs(h, a, &k);
     note_op_call(h, a->p, stream);
 
+    if (stream_fits(n, a->dim)) {
+        StreamArgs st{};
+        VocabMaps maps;
+        stream_shape(&st, (int)n, k.dim, k.base, k.extra, k.p, h->sm_count);
+        st.logits = logits;
+        st.pitch = (long long)stream_pitch(a->vocab);
+        st.limits = k.limits;
+        if (!stream_maps(a->dtype, k, st, &maps)) return fail(h, RAR_ECUDA, "rar_vocab_logprobs: the driver refused a tensor map");
+        const SelectArgs sel{{k.vocab, k.scale, a->top, k.targets, k.index_bytes, a->logprob, a->entropy, a->lse, a->top_logprob, a->top_token}, logits, st.pitch};
+        cudaError_t e = a->dtype == RAR_BFLOAT16 ? launch_stream<DT_BF16>(h, st, maps, stream) : launch_stream<DT_F16>(h, st, maps, stream);
+        if (e == cudaSuccess) e = launch_select(h, sel, (int)n, stream);
+        return e == cudaSuccess ? RAR_OK : cuda_fail(h, e, "launching the log probabilities");
+    }
     CallMaps m;
     if (!make_maps(a->dtype, k, &m)) return fail(h, RAR_ECUDA, "rar_vocab_logprobs: the driver refused a tensor map");
     auto run = [&](auto dt) {
@@ -395,7 +520,8 @@ extern "C" {
 size_t rar_vocab_logprobs_workspace(size_t tokens, size_t dim, size_t vocab, int p, int top) {
     if (!rar::sizes_ok(tokens, dim, vocab, p) || top < 0 || top > RAR_LOGPROBS_MAX_TOP) return 0;
     rar::VocabArgs k{};
-    return rar::plan(nullptr, tokens, vocab, p, top, &k);
+    float *logits;
+    return rar::plan(nullptr, tokens, dim, vocab, p, top, &k, &logits);
 }
 
 int rar_vocab_logprobs(rar_handle h, const rar_vocab_logprobs_args *a, void *stream) {
