@@ -20,49 +20,54 @@
 namespace rar {
 
 // The largest keys seen by a warp, one a lane in falling order; `least` is the one at `top`.
+// (Short code, and called, not repeated: these kernels run for a few microseconds, in which
+// instructions that are fetched for the first time show.)
 struct TopList {
     unsigned long long key = 0, least = 0;
-    // takes the lanes' keys; 0 where a lane has none
-    __device__ __forceinline__ void add(unsigned long long x, int top) {
-        const int lane = threadIdx.x % 32;
-        unsigned more = __ballot_sync(0xFFFFFFFFu, x > least);
-        if (__popc(more) > 6) {  // sorted and merged, 20 steps: as much as inserting six
-            merge(sorted(x));
-            least = __shfl_sync(0xFFFFFFFFu, key, top - 1);
-            return;
-        }
-        for (; more; more &= more - 1) {
-            const unsigned long long y = __shfl_sync(0xFFFFFFFFu, x, __ffs(more) - 1);
-            if (y <= least) continue;
-            const int at = __popc(__ballot_sync(0xFFFFFFFFu, key > y));
-            const unsigned long long before = __shfl_up_sync(0xFFFFFFFFu, key, 1);
-            key = lane < at ? key : lane == at ? y : before;
-            least = __shfl_sync(0xFFFFFFFFu, key, top - 1);
-        }
-    }
-    // takes another list: of two falling runs, one turned round, the larger ones of each
-    // place are the 32 largest of all, in a bitonic order
-    __device__ __forceinline__ void merge(unsigned long long other) {
-        const unsigned long long x = __shfl_sync(0xFFFFFFFFu, other, 31 - threadIdx.x % 32);
-        key = fall(key > x ? key : x, 32);
-    }
-    // runs of n keys in a bitonic order, into falling order (rising ones where lane & n)
-    __device__ static __forceinline__ unsigned long long fall(unsigned long long x, int n) {
-        const int lane = threadIdx.x % 32;
-        for (int d = n / 2; d; d /= 2) {
-            const unsigned long long y = __shfl_xor_sync(0xFFFFFFFFu, x, d);
-            const bool first = ((lane & d) == 0) == ((lane & n) == 0);
-            x = first == (x > y) ? x : y;
-        }
-        return x;
-    }
-    // in falling order (Batcher's bitonic sort)
-    __device__ static __forceinline__ unsigned long long sorted(unsigned long long x) {
-#pragma unroll
-        for (int n = 2; n <= 32; n *= 2) x = fall(x, n);
-        return x;
-    }
 };
+// runs of n keys in a bitonic order, into falling order (rising ones where lane & n)
+__device__ __forceinline__ unsigned long long top_fall(unsigned long long x, int n) {
+    const int lane = threadIdx.x % 32;
+#pragma unroll 1
+    for (int d = n / 2; d; d /= 2) {
+        const unsigned long long y = __shfl_xor_sync(0xFFFFFFFFu, x, d);
+        const bool first = ((lane & d) == 0) == ((lane & n) == 0);
+        x = first == (x > y) ? x : y;
+    }
+    return x;
+}
+// in falling order (Batcher's bitonic sort)
+__device__ __noinline__ unsigned long long top_sorted(unsigned long long x) {
+#pragma unroll 1
+    for (int n = 2; n <= 32; n *= 2) x = top_fall(x, n);
+    return x;
+}
+// The 32 largest of two lists: of two falling runs, one turned round, the larger ones of each
+// place, which are in a bitonic order.
+__device__ __noinline__ unsigned long long top_merged(unsigned long long key, unsigned long long other) {
+    const unsigned long long x = __shfl_sync(0xFFFFFFFFu, other, 31 - threadIdx.x % 32);
+    return top_fall(key > x ? key : x, 32);
+}
+// takes the lanes' keys; 0 where a lane has none
+__device__ __noinline__ TopList top_add(TopList list, unsigned long long x, int top) {
+    const int lane = threadIdx.x % 32;
+    unsigned more = __ballot_sync(0xFFFFFFFFu, x > list.least);
+    if (__popc(more) > 6) {  // sorted and merged, 20 steps: as much as inserting six
+        list.key = top_merged(list.key, top_sorted(x));
+        list.least = __shfl_sync(0xFFFFFFFFu, list.key, top - 1);
+        return list;
+    }
+#pragma unroll 1
+    for (; more; more &= more - 1) {
+        const unsigned long long y = __shfl_sync(0xFFFFFFFFu, x, __ffs(more) - 1);
+        if (y <= list.least) continue;
+        const int at = __popc(__ballot_sync(0xFFFFFFFFu, list.key > y));
+        const unsigned long long before = __shfl_up_sync(0xFFFFFFFFu, list.key, 1);
+        list.key = lane < at ? list.key : lane == at ? y : before;
+        list.least = __shfl_sync(0xFFFFFFFFu, list.key, top - 1);
+    }
+    return list;
+}
 
 // Where a call's results go.
 struct LogprobOut {
@@ -97,12 +102,12 @@ struct SelectArgs {
     long long pitch;
 };
 
-constexpr int kSelectWarps = 8, kSelectCluster = 8;
+constexpr int kSelectWarps = 8, kSelectCluster = 8, kSelectAhead = 4;
 
 // Everything about a token from its logits, for few tokens: a cluster of CTAs a token, each with a range
 // of the vocabulary, whose warps keep sums and a list of their own.
 __global__ void __launch_bounds__(32 * kSelectWarps) logprob_select_kernel(const __grid_constant__ SelectArgs a) {
-    __shared__ unsigned long long lists[kSelectWarps][32];
+    __shared__ unsigned long long lists[kSelectWarps][32], noted[kSelectWarps][32 * 4 * kSelectAhead];
     __shared__ float3 sums[kSelectWarps];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, top = a.out.top;
     const uint32_t rank = cluster_rank(), ctas = gridDim.x;
@@ -115,23 +120,41 @@ __global__ void __launch_bounds__(32 * kSelectWarps) logprob_select_kernel(const
     const uint32_t v0 = (uint32_t)((unsigned long long)vecs * rank / ctas), v1 = (uint32_t)((unsigned long long)vecs * (rank + 1) / ctas);
     LogitSums own;
     TopList list;
-    for (uint32_t v = v0 + warp * 32; v < v1; v += 32 * kSelectWarps) {
-        const bool has = v + lane < v1;
-        float4 q = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-        if (has) q = __ldcg(reinterpret_cast<const float4 *>(row) + v + lane);
-        const uint32_t first = (v + lane) * 4;
-        float z[4] = {q.x, q.y, q.z, q.w};
+    for (uint32_t v = v0 + warp * 32; v < v1; v += 32 * kSelectWarps * kSelectAhead) {
+        float z[4 * kSelectAhead];
+        const uint32_t at = v + lane;
 #pragma unroll
-        for (int e = 0; e < 4; e++)
-            if (first + e >= vocab) z[e] = -INFINITY;
-        own.add(z, k);
-        if (top) {
-            const float least = list.least ? top_value(list.least) : -INFINITY;
-            // (NaN is below everything here)
-            if (__any_sync(0xFFFFFFFFu, fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])) >= least))
-#pragma unroll
-                for (int e = 0; e < 4; e++) list.add(z[e] > -INFINITY ? top_key(z[e], first + e) : 0ull, top);
+        for (int u = 0; u < kSelectAhead; u++) {  // loads in flight together
+            float4 q = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+            if (at + u * 32 * kSelectWarps < v1) q = __ldcg(reinterpret_cast<const float4 *>(row) + at + u * 32 * kSelectWarps);
+            z[4 * u] = q.x, z[4 * u + 1] = q.y, z[4 * u + 2] = q.z, z[4 * u + 3] = q.w;
         }
+        auto token = [&](int i) { return (at + (i / 4) * 32 * kSelectWarps) * 4 + i % 4; };
+#pragma unroll
+        for (int i = 0; i < 4 * kSelectAhead; i++)
+            if (token(i) >= vocab) z[i] = -INFINITY;  // (behind the row's last)
+        own.add(z, k);
+        if (!top) continue;
+        // each lane's best: as many of the logits as there are lanes above one of these are not below it
+        float best = z[0];
+#pragma unroll
+        for (int i = 1; i < 4 * kSelectAhead; i++) best = fmaxf(best, z[i]);
+        const float full = list.least ? top_value(list.least) : -INFINITY;
+        if (!__any_sync(0xFFFFFFFFu, best >= full)) continue;
+        const unsigned long long kth = __shfl_sync(0xFFFFFFFFu, top_sorted(best > -INFINITY ? top_key(best, 0) : 0ull), top - 1);
+        const float bar = fmaxf(full, kth ? top_value(kth) : -INFINITY);
+        int n = 0;  // noted so far
+#pragma unroll
+        for (int i = 0; i < 4 * kSelectAhead; i++) {
+            const bool wanted = z[i] >= bar && z[i] > -INFINITY;
+            const unsigned who = __ballot_sync(0xFFFFFFFFu, wanted);
+            if (wanted) noted[warp][n + __popc(who & ((1u << lane) - 1))] = top_key(z[i], token(i));
+            n += __popc(who);
+        }
+        __syncwarp();
+#pragma unroll 1
+        for (int i = lane; i < n + lane; i += 32) list = top_add(list, i < n ? noted[warp][i] : 0ull, top);
+        __syncwarp();
     }
     own.join_lanes(32, k);
     lists[warp][lane] = list.key;
@@ -141,7 +164,7 @@ __global__ void __launch_bounds__(32 * kSelectWarps) logprob_select_kernel(const
         for (int d = 1; d < n; d *= 2) {
             __syncthreads();
             if (top && warp % (2 * d) == 0 && warp + d < n) {
-                list.merge(lists[warp + d][lane]);
+                list.key = top_merged(list.key, lists[warp + d][lane]);
                 lists[warp][lane] = list.key;
             }
         }
@@ -213,13 +236,13 @@ __global__ void __launch_bounds__(32 * kJoinWarps) logprob_join_kernel(const __g
         }
 #pragma unroll
         for (int u = 0; u < 8; u++)
-            if (i0 + u * 32 * kWarps < n) list.add(x[u], a.top);
+            if (i0 + u * 32 * kWarps < n) list = top_add(list, x[u], a.top);
     }
     if (SHARED && a.top) {
         found[warp][lane] = list.key;
         __syncthreads();
         if (warp == 0)
-            for (int w = 1; w < kWarps; w++) list.merge(found[w][lane]);
+            for (int w = 1; w < kWarps; w++) list.key = top_merged(list.key, found[w][lane]);
     }
     if (part) return;
     own.join_lanes(32, k);

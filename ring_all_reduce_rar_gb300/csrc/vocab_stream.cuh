@@ -6,8 +6,8 @@
 // vocabulary rows, as many in each as give all CTAs the same share; a stage of its
 // ring holds 64 columns of dim of all the pass's rows, one box, and of the hidden states, so
 // that these are read once a pass.  A sum of 1024 of dim has accumulators of its own (see
-// kStepsPerSum in vocab_tiles.cuh), which are added in registers at the end; a second set of
-// accumulators takes the next pass meanwhile.
+// kStepsPerSum in vocab_tiles.cuh), which are added in registers at the end; where tensor memory has
+// room for a second set of them, that takes the next pass meanwhile.
 #pragma once
 
 #include "vocab_tiles.cuh"
@@ -23,13 +23,14 @@ struct StreamArgs {
     int steps;             // of 64 along dim
     int sums;              // accumulators of a tile
     int tiles;             // of 128 rows in a pass, 1 or 2
+    int sets;              // of accumulators, 1 or 2
     int stages, stage_bytes;
     float *logits;         // [tokens][pitch], by index in the vocabulary
     long long pitch;
     WaitLimits limits;
 };
 
-constexpr int kStreamMaxTokens = 64, kStreamMaxStages = 12, kStreamEpilogueWarps = 8;
+constexpr int kStreamMaxTokens = 128, kStreamMaxStages = 12, kStreamEpilogueWarps = 8;
 constexpr int kStreamThreads = 32 * (kStreamEpilogueWarps + 2);
 constexpr int kStreamSmem = 225 * 1024;
 
@@ -137,9 +138,10 @@ __global__ void __launch_bounds__(kStreamThreads, 1) vocab_stream_kernel(const _
         unsigned turn = 0;
         bool ok = true;
         for (int i = blockIdx.x; i < a.passes && ok; i += gridDim.x, turn++) {
-            if (turn >= 2 && !wait(&sh.acc_empty[turn & 1], (turn / 2 - 1) & 1, 2)) break;
+            const unsigned set = turn % a.sets, use = turn / a.sets;
+            if (use && !wait(&sh.acc_empty[set], (use - 1) & 1, 2)) break;
             tc_fence_after();
-            const uint32_t acc = sh.tmem + (turn & 1) * 256;
+            const uint32_t acc = sh.tmem + set * 256;
             for (int s = 0; s < a.steps; s++) {
                 if (!(ok = wait(&sh.full[st], phase, 3))) break;
                 tc_fence_after();
@@ -152,16 +154,17 @@ __global__ void __launch_bounds__(kStreamThreads, 1) vocab_stream_kernel(const _
                 stream_commit(&sh.empty[st]);
                 if (++st == a.stages) st = 0, phase ^= 1;
             }
-            if (ok) stream_commit(&sh.acc_full[turn & 1]);
+            if (ok) stream_commit(&sh.acc_full[set]);
         }
     } else if (warp < kStreamEpilogueWarps) {
         const int quarter = warp % 4, tile = warp / 4, row = tile * 128 + quarter * 32 + lane;
         unsigned turn = 0;
         for (int i = blockIdx.x; i < a.passes; i += gridDim.x, turn++) {
             const PassOf b = pass_of(a, i);
-            if (!__all_sync(0xFFFFFFFFu, wait(&sh.acc_full[turn & 1], (turn / 2) & 1, 4))) break;
+            const unsigned set = turn % a.sets, use = turn / a.sets;
+            if (!__all_sync(0xFFFFFFFFu, wait(&sh.acc_full[set], use & 1, 4))) break;
             tc_fence_after();
-            const uint32_t acc = sh.tmem + ((uint32_t)quarter << 21) + (turn & 1) * 256 + tile * a.sums * a.columns;
+            const uint32_t acc = sh.tmem + ((uint32_t)quarter << 21) + set * 256 + tile * a.sums * a.columns;
             if (tile < a.tiles)
                 for (int c0 = 0; c0 < a.tokens; c0 += 8) {
                     float z[8] = {};
@@ -179,7 +182,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) vocab_stream_kernel(const _
                 }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.acc_empty[turn & 1]);
+            if (lane == 0) mbar_arrive(&sh.acc_empty[set]);
         }
     }
     __syncwarp();
@@ -191,10 +194,11 @@ __global__ void __launch_bounds__(kStreamThreads, 1) vocab_stream_kernel(const _
 
 namespace {
 
-// Whether a call is one of these: the accumulators of a tile have room in half the tensor memory.
+// Whether a call is one of these: the accumulators of two tiles fit into the tensor memory, or those of
+// one for up to 64 tokens.
 bool stream_fits(size_t tokens, size_t dim) {
     const size_t columns = (tokens + 15) / 16 * 16, sums = (dim + 64 * kStepsPerSum - 1) / (64 * kStepsPerSum);
-    return tokens >= 1 && tokens <= kStreamMaxTokens && columns * sums <= 256;
+    return tokens >= 1 && tokens <= kStreamMaxTokens && columns * sums <= (tokens <= 64 ? 512 : 256);
 }
 
 size_t stream_pitch(size_t vocab) { return (vocab + 3) / 4 * 4; }
@@ -208,7 +212,7 @@ void stream_shape(StreamArgs *s, int tokens, long long dim, int base, int extra,
     s->steps = (int)((dim + 63) / 64);
     s->sums = (s->steps + kStepsPerSum - 1) / kStepsPerSum;
     // rows of a pass: the fewest for the CTA that has most of them (and, for equal ones, the fewest passes)
-    const int most = 2 * s->sums * s->columns <= 256 ? 256 : 128;
+    const int tile = s->sums * s->columns, most = 2 * tile <= 512 ? 256 : 128;
     long long least = 0;
     for (int rows = most; rows >= 8; rows -= 8) {
         const int big = (base + 1 + rows - 1) / rows, small = (base + rows - 1) / rows;
@@ -221,6 +225,7 @@ void stream_shape(StreamArgs *s, int tokens, long long dim, int base, int extra,
         s->passes = (int)passes;
     }
     s->tiles = s->rows > 128 ? 2 : 1;
+    s->sets = s->tiles * tile <= 256 ? 2 : 1;
     s->stage_bytes = s->columns * 128 + (s->rows * 128 + 1023) / 1024 * 1024;
     // (a product reads 128 rows of a tile, whatever lies behind the pass's last)
     const int behind = s->tiles * 16384 - (s->stage_bytes - s->columns * 128);

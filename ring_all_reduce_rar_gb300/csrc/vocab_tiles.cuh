@@ -325,6 +325,7 @@ struct LogitSums {
     // over the lanes, in an order that gives every lane the same bits
     __device__ __forceinline__ void join_lanes(int lanes, float k) {
         const int lane = threadIdx.x % 32;
+#pragma unroll 1
         for (int d = 1; d < lanes; d *= 2) {
             const float om = __shfl_xor_sync(0xFFFFFFFFu, max, d), os = __shfl_xor_sync(0xFFFFFFFFu, s, d), ou = __shfl_xor_sync(0xFFFFFFFFu, u, d);
             if (lane & d) {
