@@ -19,13 +19,13 @@ struct GradEntry {
     const void *data;
     void *out;
     long long n, cols, stride, out_stride;
-    unsigned first;  // its first chunk
     short dtype, out_dtype;
 };
 // The tensors of a launch travel in the kernel's parameters.
 template <int N>
 struct GradTable {
     GradEntry entry[N];
+    unsigned start[N + 1];  // a tensor's first chunk (apart from the rest: it is what is searched); its end
     int n;
     unsigned first, chunks;  // of this launch
     long long chunk;         // elements of a chunk
@@ -42,11 +42,11 @@ constexpr int kGradThreads = 256;
 
 // The tensor that a chunk belongs to (tensors without elements have none).
 template <int N>
-__device__ __forceinline__ int entry_of(const GradTable<N> &a, unsigned chunk) {
+__device__ __forceinline__ int tensor_of(const GradTable<N> &a, unsigned chunk) {
     int lo = 0, hi = a.n - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) / 2;
-        if (a.entry[mid].first <= chunk) lo = mid;
+        if (a.start[mid] <= chunk) lo = mid;
         else hi = mid - 1;
     }
     return lo;
@@ -158,42 +158,52 @@ __global__ void __launch_bounds__(kGradThreads) grad_norm_kernel(const __grid_co
     pdl_wait();
     pdl_launch_dependents();
     const unsigned chunk = a.first + blockIdx.x;
-    const GradEntry &t = a.entry[entry_of(a, chunk)];
-    const long long e0 = (long long)(chunk - t.first) * a.chunk, e1 = min(e0 + a.chunk, t.n);
+    const int i = tensor_of(a, chunk);
+    const GradEntry &t = a.entry[i];
+    const long long e0 = (long long)(chunk - a.start[i]) * a.chunk, e1 = min(e0 + a.chunk, t.n);
     const double s = t.dtype == DT_F32 ? chunk_sum<DT_F32>(t, e0, e1) : t.dtype == DT_BF16 ? chunk_sum<DT_BF16>(t, e0, e1) : chunk_sum<DT_F16>(t, e0, e1);
     if (threadIdx.x == 0) a.sums[chunk] = s;
 }
 
-__device__ __forceinline__ double warp_sum_double(double v) {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+// Sum over groups of n lanes, in each of them.
+__device__ __forceinline__ double lanes_sum(double v, int n) {
+    for (int o = n / 2; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
     return v;
 }
 
-// The chunks' sums by tensor, a warp a tensor, and the tensors'.
+// The chunks' sums by tensor, and the tensors': one CTA, a group of lanes a tensor, so that the latency of
+// a tensor's few loads is not paid for one after the other.
 template <int N>
 __global__ void __launch_bounds__(1024) grad_norm_join_kernel(const __grid_constant__ GradTable<N> a) {
     __shared__ double tensor[N];
+    __shared__ unsigned start[N + 1];
+    for (int i = threadIdx.x; i <= a.n; i += 1024) start[i] = a.start[i];
+    __syncthreads();
     pdl_wait();
     pdl_launch_dependents();
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    for (int i = warp; i < a.n; i += 32) {
-        const unsigned lo = a.entry[i].first, hi = i + 1 < a.n ? a.entry[i + 1].first : a.first + a.chunks;
+    int lanes = 32;
+    while (lanes > 4 && a.n * lanes > 1024) lanes /= 2;
+    const int sub = threadIdx.x % lanes;
+    for (int i0 = 0; i0 < a.n; i0 += 1024 / lanes) {
+        const int i = i0 + threadIdx.x / lanes;
         double s = 0.0;
+        if (i < a.n) {
+            const unsigned hi = start[i + 1];
 #pragma unroll 8
-        for (unsigned c = lo + lane; c < hi; c += 32) s += __ldcg(a.sums + c);
-        s = warp_sum_double(s);
-        if (lane == 0) {
+            for (unsigned c = start[i] + sub; c < hi; c += lanes) s += __ldcg(a.sums + c);
+        }
+        s = lanes_sum(s, lanes);
+        if (i < a.n && sub == 0) {
             tensor[i] = s;
             if (a.norms) a.norms[i] = (float)sqrt(s);
         }
     }
     __syncthreads();
-    if (warp) return;
+    if (threadIdx.x >= 32) return;
     double s = 0.0;
-    for (int i = lane; i < a.n; i += 32) s += tensor[i];
-    s = warp_sum_double(s);
-    if (lane) return;
+    for (int i = threadIdx.x; i < a.n; i += 32) s += tensor[i];
+    s = lanes_sum(s, 32);
+    if (threadIdx.x) return;
     if (!a.begins) s += *a.total;
     if (!a.ends) *a.total = s;
     else if (a.norm) *a.norm = (float)sqrt(s);
@@ -230,9 +240,10 @@ __global__ void __launch_bounds__(kGradThreads) grad_clip_kernel(const __grid_co
     const float d = *a.clip_norm + a.eps;
     const float f = d <= a.max_norm ? 1.0f : __fdiv_rn(a.max_norm, d);  // (a NaN is passed on)
     const unsigned chunk = a.first + a.chunks - 1 - blockIdx.x;
-    const GradEntry &t = a.entry[entry_of(a, chunk)];
+    const int i = tensor_of(a, chunk);
+    const GradEntry &t = a.entry[i];
     if (f == 1.0f && t.out == t.data) return;
-    const long long e0 = (long long)(chunk - t.first) * a.chunk, e1 = min(e0 + a.chunk, t.n);
+    const long long e0 = (long long)(chunk - a.start[i]) * a.chunk, e1 = min(e0 + a.chunk, t.n);
     if (t.dtype == DT_F32) scale_chunk<DT_F32, DT_F32>(t, e0, e1, f);
     else if (t.dtype == DT_BF16) t.out_dtype == DT_F32 ? scale_chunk<DT_BF16, DT_F32>(t, e0, e1, f) : scale_chunk<DT_BF16, DT_BF16>(t, e0, e1, f);
     else t.out_dtype == DT_F32 ? scale_chunk<DT_F16, DT_F32>(t, e0, e1, f) : scale_chunk<DT_F16, DT_F16>(t, e0, e1, f);
@@ -242,12 +253,16 @@ namespace {
 
 size_t elements(const rar_tensor &t) { return t.rows * t.cols; }
 
-// Elements of a chunk: a power of two, so many that the join has few sums to add (one CTA, 16 a
-// thread), so few that small sets use all SMs.
-size_t chunk_elements(const rar_tensor *tensors, size_t n) {
-    size_t total = 0, chunk = 4096;
+// Elements of a chunk: a power of two, 8192 or more (at 4096, 10 M fp16 elements took 24 us to clip, 17 at
+// 8192), so that there are at most `most` chunks, and one more a tensor.  For the norm 4096, whose sums one CTA
+// joins: 1.07 G elements bf16 take 296 us with 512 to 4096 of them, 310 with up to 16384, 334 with 65536;
+// 157 M float32 99 us with up to 4096, 102 and 191.  Clipping has nothing to join: the 1.07 G into 32 bits took
+// 1716 us with up to 512, 1473 with 2048, 1424 with 16384, 1400 with 65536, with the norm before it.
+constexpr size_t kLeastChunk = 8192, kNormChunks = 4096, kClipChunks = 65536;
+size_t chunk_elements(const rar_tensor *tensors, size_t n, size_t most) {
+    size_t total = 0, chunk = kLeastChunk;
     for (size_t i = 0; i < n; i++) total += elements(tensors[i]);
-    while (total / chunk > 16384) chunk *= 2;
+    while (total / chunk > most) chunk *= 2;
     return chunk;
 }
 size_t count_chunks(const rar_tensor *tensors, size_t n, size_t chunk) {
@@ -258,7 +273,7 @@ size_t count_chunks(const rar_tensor *tensors, size_t n, size_t chunk) {
 size_t plan(void *base, const rar_tensor *tensors, size_t n, double **sums, double **total) {
     WorkspacePlan w(base);
     *total = w.take<double>(1);
-    *sums = w.take<double>(count_chunks(tensors, n, chunk_elements(tensors, n)));
+    *sums = w.take<double>(count_chunks(tensors, n, chunk_elements(tensors, n, kNormChunks)));
     return w.used;
 }
 
@@ -313,11 +328,12 @@ cudaError_t for_tables(const rar_tensor *tensors, const rar_tensor *out, size_t 
             g.cols = one ? g.n : (long long)t.cols;
             g.stride = one ? g.n : (long long)(t.stride ? t.stride : t.cols);
             g.out_stride = one ? g.n : (long long)(o.stride ? o.stride : o.cols);
-            g.first = chunks;
+            a.start[i] = chunks;
             g.dtype = (short)t.dtype;
             g.out_dtype = (short)o.dtype;
             chunks += (unsigned)((elements(t) + chunk - 1) / chunk);
         }
+        a.start[a.n] = chunks;
         a.chunks = chunks - a.first;
         a.chunk = (long long)chunk;
         a.begins = i0 == 0;
@@ -354,7 +370,7 @@ int grad_norm(rar_ctx *h, const rar_grad_norm_args *a, cudaStream_t stream) {
     note_op_call(h, 1, stream);
     auto run = [&](auto most) {
         constexpr int N = decltype(most)::value;
-        return for_tables<N>(a->tensors, nullptr, a->n, chunk_elements(a->tensors, a->n), [&](GradTable<N> &t, size_t i0) {
+        return for_tables<N>(a->tensors, nullptr, a->n, chunk_elements(a->tensors, a->n, kNormChunks), [&](GradTable<N> &t, size_t i0) {
             t.sums = sums;
             t.total = total;
             t.norm = a->norm;
@@ -394,7 +410,7 @@ int grad_clip(rar_ctx *h, const rar_grad_clip_args *a, cudaStream_t stream) {
     note_op_call(h, 1, stream);
     auto run = [&](auto most) {
         constexpr int N = decltype(most)::value;
-        return for_tables<N>(a->tensors, a->out, a->n, chunk_elements(a->tensors, a->n), [&](GradTable<N> &t, size_t) {
+        return for_tables<N>(a->tensors, a->out, a->n, chunk_elements(a->tensors, a->n, kClipChunks), [&](GradTable<N> &t, size_t) {
             t.clip_norm = a->norm;
             t.max_norm = a->max_norm;
             t.eps = a->eps;

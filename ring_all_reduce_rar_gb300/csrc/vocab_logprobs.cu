@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(32 * kPrepareTokens) logprob_prepare_kernel(co
     pdl_launch_dependents();
     const int lane = threadIdx.x % 32;
     const long long t = (long long)blockIdx.x * kPrepareTokens + threadIdx.x / 32;
-    if (t >= a.tokens) return;
+    if (t >= (a.pair ? a.pair : a.tokens)) return;
     const long long y = load_index(a.targets, a.index_bytes, t);
     const bool counts = y >= 0 && y < a.vocab;
     const float da = counts && a.dlogprob ? a.dlogprob[t] : 0.0f, db = counts && a.dentropy ? a.dentropy[t] : 0.0f;
@@ -279,7 +279,10 @@ __global__ void __launch_bounds__(32 * kPrepareTokens) logprob_prepare_kernel(co
         for (int u = 0; u < 4; u++) q[u] = used ? __ldg(from + min(i0 + u * 32, vecs - 1)) : make_uint4(0, 0, 0, 0);
 #pragma unroll
         for (int u = 0; u < 4; u++)
-            if (i0 + u * 32 < vecs) to[i0 + u * 32] = q[u];
+            if (i0 + u * 32 < vecs) {
+                to[i0 + u * 32] = q[u];
+                if (a.pair) to[a.pair * vecs + i0 + u * 32] = q[u];
+            }
     }
 }
 
@@ -328,13 +331,18 @@ size_t plan(void *base, size_t tokens, size_t dim, size_t vocab, int p, int top,
     }
     return w.used;
 }
+// Up to so many tokens G is held as two 16-bit rows a token, the second what rounding left of the first, and the
+// products take both.  A gradient of few tokens is a sum of few products, in which G's rounding shows as much as the
+// gradient's own or, where one entry decides it, up to 2.6 times as much; over many tokens it adds 1.4 times.
+constexpr size_t kPairedTokens = 512;
 size_t plan_gradients(void *base, size_t tokens, size_t dim, size_t vocab, int p, VocabArgs *k) {
     WorkspacePlan w(base);
     plan_blocks(vocab, p, k);
     k->w_max = w.take<unsigned>(1);
     k->row_weight = w.take<float>(tokens);
     k->row_entropy = w.take<float>(tokens);
-    plan_grad(w, tokens, dim, k);
+    k->pair = tokens <= kPairedTokens ? (long long)tokens : 0;
+    plan_grad(w, k->pair ? 2 * tokens : tokens, dim, k);
     return w.used;
 }
 
@@ -520,14 +528,19 @@ int vocab_logprobs_grad(rar_ctx *h, const rar_vocab_logprobs_grad_args *a, cudaS
     k.dentropy = a->dentropy;
     note_op_call(h, a->p, stream);
 
+    // the products' rows are those of G, and of the hidden states that have a part in it
+    if (k.pair) k.tokens = 2 * k.pair;
+    VocabArgs rows = k;
+    rows.hidden = k.hidden_used;
+    rows.hidden_stride = k.dim;
     CallMaps m;
-    if (k.tokens && !make_maps(a->dtype, k, &m)) return fail(h, RAR_ECUDA, "rar_vocab_logprobs_grad: the driver refused a tensor map");
+    if (k.tokens && !make_maps(a->dtype, rows, &m)) return fail(h, RAR_ECUDA, "rar_vocab_logprobs_grad: the driver refused a tensor map");
     auto run = [&](auto dt) {
         constexpr int DT = decltype(dt)::value;
         if (!k.tokens) return clear_dweights(k, stream);
         cudaError_t e = cudaMemsetAsync(k.w_max, 0, sizeof(*k.w_max), stream);
         if (e == cudaSuccess)
-            e = launch_pdl(logprob_prepare_kernel, dim3((unsigned)((k.tokens + kPrepareTokens - 1) / kPrepareTokens)), dim3(32 * kPrepareTokens), 0, stream, k);
+            e = launch_pdl(logprob_prepare_kernel, dim3((unsigned)((n + kPrepareTokens - 1) / kPrepareTokens)), dim3(32 * kPrepareTokens), 0, stream, k);
         if (e != cudaSuccess) return e;
         return k.dim > 64 * kStepsPerSum ? launch_gradients<TILES_LOGPROB_G_SUMS, DT>(h, k, m, stream) : launch_gradients<TILES_LOGPROB_G, DT>(h, k, m, stream);
     };

@@ -47,6 +47,7 @@ struct VocabArgs {
     float *dh_part;       // [splits][tokens][dim]
     int window;           // blocks of a window
     int splits;           // of dhidden's sum over a window
+    long long pair;       // not 0: row t + pair of G is what rounding left of row t, for rows of `pair` tokens
     bool direct;          // one split: the last window writes dhidden itself
     // log probabilities: sums and alternatives of each row of tiles' pairs, by half a block's columns
     int width;                    // rows of tiles that are worked on at a time
@@ -106,6 +107,16 @@ __device__ __forceinline__ int g_exponent(const VocabArgs &a) {
 __device__ __forceinline__ float g_unit(const VocabArgs &a) {
     const float m = __uint_as_float(*a.w_max);
     return m > 0.0f ? ldexpf(m, -ilogbf(m)) : 1.0f;
+}
+// Both, of a token's weights.  (The power of two is a normal number, so the product is rounded as
+// ldexp's result.)
+struct GScale {
+    float unit, power;
+    __device__ __forceinline__ float scaled(float w) const { return w / unit * power; }
+};
+template <int DT>
+__device__ __forceinline__ GScale g_scale(const VocabArgs &a) {
+    return {g_unit(a), ldexpf(1.0f, g_exponent<DT>(a))};
 }
 // What undoes both, and brings in the logits' scale.
 template <int DT>
@@ -462,6 +473,7 @@ struct TileRow {
     float w_log;      // G of log probabilities: p (w + w_log log p) + w_target at the target
     float w_target;
     bool used;        // the token has a part in the gradients
+    bool rest;        // what rounding leaves of another row of G (see VocabArgs::pair)
     float max, sum;   // logits for the statistics
     int first;        // the vocabulary's row of the half's first column
     char *out;        // where the row's half begins
@@ -469,7 +481,7 @@ struct TileRow {
 };
 
 template <int MODE, int DT>
-__device__ __forceinline__ TileRow tile_row(const VocabArgs &a, int b0, const TileItem &it, int row, int half) {
+__device__ __forceinline__ TileRow tile_row(const VocabArgs &a, const GScale &g, int b0, const TileItem &it, int row, int half) {
     TileRow r;
     r.row = row;
     r.out = nullptr;
@@ -488,6 +500,9 @@ __device__ __forceinline__ TileRow tile_row(const VocabArgs &a, int b0, const Ti
     } else {
         const BlockOf b = block_of(a, b0 + it.block);
         r.live = row < a.tokens;
+        r.rest = false;
+        if constexpr (Mode<MODE>::logprob)
+            if (a.pair && row >= a.pair) r.rest = true, row -= (int)a.pair;
         r.cols = b.rows - half;
         const long long y = r.live ? load_index(a.targets, a.index_bytes, row) - b.first - half : -1;
         r.target = y >= 0 && y < r.cols ? (int)y : -1;
@@ -495,19 +510,17 @@ __device__ __forceinline__ TileRow tile_row(const VocabArgs &a, int b0, const Ti
         r.sum = 0.0f;
         r.first = b.first + half;
         if constexpr (Mode<MODE>::logprob) {
-            const int e = g_exponent<DT>(a);
-            const float unit = g_unit(a);
-            const float da = r.live ? ldexpf(a.row_weight[row] / unit, e) : 0.0f, db = r.live ? ldexpf(a.row_entropy[row] / unit, e) : 0.0f;
+            const float da = r.live ? g.scaled(a.row_weight[row]) : 0.0f, db = r.live ? g.scaled(a.row_entropy[row]) : 0.0f;
             r.used = da != 0.0f || db != 0.0f;
             r.w = -da - (db != 0.0f ? db * a.entropy_in[row] : 0.0f);
             r.w_log = -db;
             r.w_target = da;
             r.lse = r.used ? a.lse_in[row] : 0.0f;
         } else if constexpr (Mode<MODE>::g) {
-            r.w = r.live ? ldexpf(a.row_weight[row] / g_unit(a), g_exponent<DT>(a)) : 0.0f;
+            r.w = r.live ? g.scaled(a.row_weight[row]) : 0.0f;
             r.lse = r.live ? a.lse_ws[row] : 0.0f;
         }
-        if constexpr (Mode<MODE>::g) r.out = static_cast<char *>(a.g) + (((long long)row * a.window + it.block) * kBlock + half) * 2;
+        if constexpr (Mode<MODE>::g) r.out = static_cast<char *>(a.g) + (((long long)r.row * a.window + it.block) * kBlock + half) * 2;
     }
     return r;
 }
@@ -559,6 +572,10 @@ __device__ __forceinline__ void tile_columns(const VocabArgs &a, TileRow &r, int
                 v[c] = c < cols && r.w != 0.0f ? p * r.w : 0.0f;
             }
         }
+        if constexpr (Mode<MODE>::logprob)
+            if (r.rest)
+#pragma unroll
+                for (int c = 0; c < 32; c++) v[c] -= widen<DT>(narrow<DT>(v[c]));
 #pragma unroll
         for (int c = 0; c < 32; c += 16) {
             const uint4 x = narrow8<DT>(v + c), y4 = narrow8<DT>(v + c + 8);
@@ -703,6 +720,8 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(152)
     } else if (warp < kTcEpilogueWarps) {
         const int quarter = warp % 4;
         const float undo = MODE == TILES_DHIDDEN || MODE == TILES_DWEIGHT ? g_undo<DT>(a) : 1.0f;
+        GScale g;
+        if constexpr (Mode<MODE>::g) g = g_scale<DT>(a);
         const bool first_window = b0 == 0, direct = a.direct && b0 + nb == a.n_blocks;
         unsigned sums = 0;  // accumulators read
         auto ready = [&] {
@@ -721,7 +740,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(152)
         tile_walk<MODE>(a, b0, nb, [&](const TileItem &it) {
             bool ok = true;
             const int half = warp / 4 * 128, row = it.row + (int)rank * 128 + quarter * 32 + lane;
-            TileRow r = tile_row<MODE, DT>(a, b0, it, row, half);
+            TileRow r = tile_row<MODE, DT>(a, g, b0, it, row, half);
             auto at = [&](int c) { return sh.tmem + ((uint32_t)quarter << 21) + (sums & 1) * kTile + half + c; };
             if (Mode<MODE>::sums) {
                 // all sums but the last into registers, and these onto the last
@@ -809,25 +828,28 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(152)
     tc_end(&sh);
 }
 
-// dhidden from the splits' sums.
+// dhidden from the splits' sums, and the paired rows'.
 template <int DT>
 __global__ void __launch_bounds__(256) vocab_dhidden_join_kernel(const __grid_constant__ VocabArgs a) {
     pdl_wait();
     pdl_launch_dependents();
     const float undo = g_undo<DT>(a);
-    const long long vecs = a.dim / 8, n = a.tokens * vecs;
+    const long long vecs = a.dim / 8, n = (a.pair ? a.pair : a.tokens) * vecs, pitch = a.tokens * a.dim, half = a.pair * a.dim;
+    const int parts = a.pair ? 2 * a.splits : a.splits;  // (those of a pair one after the other)
     for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (long long)gridDim.x * blockDim.x) {
         const long long t = n < 0x7FFFFFFF ? (long long)((uint32_t)i / (uint32_t)vecs) : i / vecs, d = (i - t * vecs) * 8;
         const float *part = a.dh_part + t * a.dim + d;
-        const long long pitch = a.tokens * a.dim;
         float v[8] = {};
-        for (int k0 = 0; k0 < a.splits; k0 += 4) {
+        for (int k0 = 0; k0 < parts; k0 += 4) {
             uint32_t q[4][8];  // loads in flight together
 #pragma unroll
-            for (int k = 0; k < 4; k++) load_32b(part + min(k0 + k, a.splits - 1) * pitch, q[k]);
+            for (int k = 0; k < 4; k++) {
+                const int j = min(k0 + k, parts - 1);
+                load_32b(part + (a.pair ? (j / 2) * pitch + (j % 2) * half : j * pitch), q[k]);
+            }
 #pragma unroll
             for (int k = 0; k < 4; k++)
-                if (k0 + k < a.splits)
+                if (k0 + k < parts)
 #pragma unroll
                     for (int e = 0; e < 8; e++) v[e] += __uint_as_float(q[k][e]);
         }
@@ -893,7 +915,7 @@ void plan_blocks(size_t vocab, int p, VocabArgs *k) {
     k->n_blocks = k->extra * k->nb_big + (p - k->extra) * k->nb_small;
 }
 
-// The gradients' share of a workspace: G for a window of blocks, and dhidden's sums.
+// The gradients' share of a workspace: G for a window of blocks, and dhidden's sums.  tokens: rows of G.
 void plan_grad(WorkspacePlan &w, size_t tokens, size_t dim, VocabArgs *k) {
     const size_t n_blocks = (size_t)k->n_blocks;
     k->hidden_used = w.take<uint16_t>(tokens * dim);
@@ -906,8 +928,8 @@ void plan_grad(WorkspacePlan &w, size_t tokens, size_t dim, VocabArgs *k) {
     const size_t tiles = ((tokens + kTile - 1) / kTile) * ((dim + kTile - 1) / kTile);
     const size_t splits = std::min(std::max<size_t>(2 * kPairs / std::max<size_t>(tiles, 1), 1), window);
     k->splits = (int)splits;
-    k->direct = splits == 1;
-    k->dh_part = w.take<float>(window < n_blocks || splits > 1 ? splits * tokens * dim : 0);
+    k->direct = splits == 1 && !k->pair;
+    k->dh_part = w.take<float>(window < n_blocks || !k->direct ? splits * tokens * dim : 0);
 }
 
 // The maps of a call: of the logits' products, dhidden's and dweights'.
@@ -954,8 +976,8 @@ cudaError_t launch_gradients(const rar_ctx *h, const VocabArgs &k, const CallMap
         }
         if (e == cudaSuccess && k.want_dw) e = launch_tiles<TILES_DWEIGHT, DT>(h, k, m.dw, b0, nb, stream);
     }
-    if (e == cudaSuccess && k.dhidden && k.splits > 1) {
-        const long long n = k.tokens * (k.dim / 8);
+    if (e == cudaSuccess && k.dhidden && !k.direct) {
+        const long long n = (k.pair ? k.pair : k.tokens) * (k.dim / 8);
         const unsigned grid = (unsigned)std::min<long long>((n + 255) / 256, h->sm_count * 8);
         e = launch_pdl(vocab_dhidden_join_kernel<DT>, dim3(grid), dim3(256), 0, stream, k);
     }
