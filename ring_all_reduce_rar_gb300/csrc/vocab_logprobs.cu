@@ -68,6 +68,22 @@ __device__ __noinline__ TopList top_add(TopList list, unsigned long long x, int 
     }
     return list;
 }
+// The lanes' largest of several keys each, in falling order: as many keys as there are lanes above one of
+// these are not below it.  What is below the one at `top` is not among the `top` largest.
+__device__ __forceinline__ unsigned long long top_bound(const TopList &list, unsigned long long best, int top) {
+    return list.least ? list.least : __shfl_sync(0xFFFFFFFFu, top_sorted(best), top - 1);
+}
+// takes the keys noted in shared memory
+__device__ __noinline__ TopList top_add_noted(TopList list, const unsigned long long *noted, int n, int top) {
+    __syncwarp();
+#pragma unroll 1
+    for (int i0 = 0; i0 < n; i0 += 32) {
+        const int i = i0 + threadIdx.x % 32;
+        list = top_add(list, i < n ? noted[i] : 0ull, top);
+    }
+    __syncwarp();
+    return list;
+}
 
 // Where a call's results go.
 struct LogprobOut {
@@ -102,12 +118,15 @@ struct SelectArgs {
     long long pitch;
 };
 
-constexpr int kSelectWarps = 8, kSelectCluster = 8, kSelectAhead = 4;
+// Warps of a CTA, CTAs of a token, 16-byte loads that a lane has in flight.  A round of these loads costs a
+// sort whatever it brings, so rounds are long: a whole call for 16 tokens by 65536 x 4096 bf16 with 5
+// alternatives takes 101 us, 107 with 8 warps of 4 loads; 64 by 32768 x 2048 56 us with either.
+constexpr int kSelectWarps = 4, kSelectCluster = 8, kSelectAhead = 16, kSelectNoted = 256;
 
 // Everything about a token from its logits, for few tokens: a cluster of CTAs a token, each with a range
 // of the vocabulary, whose warps keep sums and a list of their own.
 __global__ void __launch_bounds__(32 * kSelectWarps) logprob_select_kernel(const __grid_constant__ SelectArgs a) {
-    __shared__ unsigned long long lists[kSelectWarps][32], noted[kSelectWarps][32 * 4 * kSelectAhead];
+    __shared__ unsigned long long lists[kSelectWarps][32], noted[kSelectWarps][kSelectNoted];
     __shared__ float3 sums[kSelectWarps];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, top = a.out.top;
     const uint32_t rank = cluster_rank(), ctas = gridDim.x;
@@ -135,14 +154,13 @@ __global__ void __launch_bounds__(32 * kSelectWarps) logprob_select_kernel(const
             if (token(i) >= vocab) z[i] = -INFINITY;  // (behind the row's last)
         own.add(z, k);
         if (!top) continue;
-        // each lane's best: as many of the logits as there are lanes above one of these are not below it
         float best = z[0];
 #pragma unroll
         for (int i = 1; i < 4 * kSelectAhead; i++) best = fmaxf(best, z[i]);
         const float full = list.least ? top_value(list.least) : -INFINITY;
         if (!__any_sync(0xFFFFFFFFu, best >= full)) continue;
-        const unsigned long long kth = __shfl_sync(0xFFFFFFFFu, top_sorted(best > -INFINITY ? top_key(best, 0) : 0ull), top - 1);
-        const float bar = fmaxf(full, kth ? top_value(kth) : -INFINITY);
+        const unsigned long long bound = top_bound(list, best > -INFINITY ? top_key(best, 0) : 0ull, top);
+        const float bar = bound ? top_value(bound) : -INFINITY;
         int n = 0;  // noted so far
 #pragma unroll
         for (int i = 0; i < 4 * kSelectAhead; i++) {
@@ -150,11 +168,12 @@ __global__ void __launch_bounds__(32 * kSelectWarps) logprob_select_kernel(const
             const unsigned who = __ballot_sync(0xFFFFFFFFu, wanted);
             if (wanted) noted[warp][n + __popc(who & ((1u << lane) - 1))] = top_key(z[i], token(i));
             n += __popc(who);
+            if (i % 4 == 3 && n > kSelectNoted - 4 * 32) {  // (seldom: far fewer are above the bar, unless they rise along the row)
+                list = top_add_noted(list, noted[warp], n, top);
+                n = 0;
+            }
         }
-        __syncwarp();
-#pragma unroll 1
-        for (int i = lane; i < n + lane; i += 32) list = top_add(list, i < n ? noted[warp][i] : 0ull, top);
-        __syncwarp();
+        list = top_add_noted(list, noted[warp], n, top);
     }
     own.join_lanes(32, k);
     lists[warp][lane] = list.key;
@@ -180,19 +199,23 @@ __global__ void __launch_bounds__(32 * kSelectWarps) logprob_select_kernel(const
         if (warp == 0 && lane == 0) sums[0] = make_float3(own.max, own.s, own.u);
         cluster_sync_all();
         list.key = 0;
-        float3 other = make_float3(-INFINITY, 0.0f, 0.0f);
-        if (rank == 0 && warp < (int)ctas) {
-            const uint32_t at = peer_addr(smem_u32(&lists[0][lane]), (uint32_t)warp), st = peer_addr(smem_u32(&sums[0]), (uint32_t)warp);
-            asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(list.key) : "r"(at) : "memory");
-            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(other.x) : "r"(st) : "memory");
-            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(other.y) : "r"(st + 4) : "memory");
-            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(other.z) : "r"(st + 8) : "memory");
+        own = LogitSums();
+        for (int c = warp; c < (int)ctas && rank == 0; c += kSelectWarps) {
+            const uint32_t at = peer_addr(smem_u32(&lists[0][lane]), (uint32_t)c), st = peer_addr(smem_u32(&sums[0]), (uint32_t)c);
+            unsigned long long x;
+            float m, e, u;
+            asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(x) : "r"(at) : "memory");
+            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(m) : "r"(st) : "memory");
+            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(e) : "r"(st + 4) : "memory");
+            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(u) : "r"(st + 8) : "memory");
+            list.key = c == warp ? x : top_merged(list.key, x);
+            own.join(m, e, u, k);
         }
         cluster_sync_all();  // all of it is read: the others may end, and this one may write
         if (rank) return;
         lists[warp][lane] = list.key;
-        if (lane == 0) sums[warp] = other;
-        join((int)ctas);
+        if (lane == 0) sums[warp] = make_float3(own.max, own.s, own.u);
+        join(min((int)ctas, kSelectWarps));
     }
     if (warp == 0) {
         const long long y = load_index(a.out.targets, a.out.index_bytes, t);
@@ -202,11 +225,11 @@ __global__ void __launch_bounds__(32 * kSelectWarps) logprob_select_kernel(const
 
 // Results from the pairs' sums and alternatives.  SHARED: by a CTA of warps a token, for few tokens
 // (which have the longer lists), else by a warp a token.
-constexpr int kJoinWarps = 4;
+constexpr int kJoinWarps = 4, kJoinAhead = 10;
 template <bool SHARED>
 __global__ void __launch_bounds__(32 * kJoinWarps) logprob_join_kernel(const __grid_constant__ VocabArgs a, const __grid_constant__ LogprobOut o) {
     constexpr int kWarps = SHARED ? kJoinWarps : 1;
-    __shared__ unsigned long long found[kJoinWarps][32];
+    __shared__ unsigned long long found[kJoinWarps][32], noted[kJoinWarps][32 * kJoinAhead];
     pdl_wait();
     pdl_launch_dependents();
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, part = SHARED ? warp : 0;
@@ -227,16 +250,26 @@ __global__ void __launch_bounds__(32 * kJoinWarps) logprob_join_kernel(const __g
     }
     TopList list;
     const int n = lists * a.top;
-    for (int i0 = part * 32; i0 < n; i0 += 32 * kWarps * 8) {
-        unsigned long long x[8];  // loads in flight together
+    for (int i0 = part * 32; i0 < n; i0 += 32 * kWarps * kJoinAhead) {
+        unsigned long long x[kJoinAhead], best = 0;
 #pragma unroll
-        for (int u = 0; u < 8; u++) {
+        for (int u = 0; u < kJoinAhead; u++) {  // loads in flight together
             const int i = i0 + u * 32 * kWarps + lane;
             x[u] = i < n ? __ldcg(a.lists + (long long)i * a.tokens + t) : 0ull;
         }
 #pragma unroll
-        for (int u = 0; u < 8; u++)
-            if (i0 + u * 32 * kWarps < n) list = top_add(list, x[u], a.top);
+        for (int u = 0; u < kJoinAhead; u++) best = x[u] > best ? x[u] : best;
+        if (!__any_sync(0xFFFFFFFFu, best > list.least)) continue;
+        const unsigned long long bound = top_bound(list, best, a.top);
+        int m = 0;  // noted so far
+#pragma unroll
+        for (int u = 0; u < kJoinAhead; u++) {
+            const bool wanted = x[u] >= bound && x[u];
+            const unsigned who = __ballot_sync(0xFFFFFFFFu, wanted);
+            if (wanted) noted[warp][m + __popc(who & ((1u << lane) - 1))] = x[u];
+            m += __popc(who);
+        }
+        list = top_add_noted(list, noted[warp], m, a.top);
     }
     if (SHARED && a.top) {
         found[warp][lane] = list.key;
@@ -328,6 +361,7 @@ size_t plan(void *base, size_t tokens, size_t dim, size_t vocab, int p, int top,
         k->z_target = w.take<float>(pass);
         k->sums = w.take<float4>(lists * pass);
         k->lists = w.take<unsigned long long>(lists * pass * (size_t)top);
+        k->bars = w.take<uint32_t>(top ? pass : 0);
     }
     return w.used;
 }
@@ -466,6 +500,10 @@ int vocab_logprobs(rar_ctx *h, const rar_vocab_logprobs_args *a, cudaStream_t st
             const int tb = tiles_of(part.tokens);
             part.width = choose_width(tb, k.n_blocks, (int)kPairs);
             part.pairs = std::min(std::min(h->sm_count / 2, (int)kPairs), std::min(tb, part.width) * k.n_blocks);
+            // (a pair with one tile of a row learns nothing from the others)
+            const bool share = a->top && k.n_blocks > pairs_a_row(part.pairs, std::min(part.width, tb));
+            if (!share) part.bars = nullptr;
+            else if ((e = cudaMemsetAsync(part.bars, 0, sizeof(uint32_t) * (size_t)part.tokens, stream)) != cudaSuccess) return e;
             if (t0 && !make_map(&m.logits.one, a->dtype, part.hidden, part.tokens, k.dim, k.hidden_stride, 128)) return cudaErrorInvalidValue;
             e = k.dim > 64 * kStepsPerSum ? launch_tiles<TILES_LOGPROB_SUMS, DT>(h, part, m.logits, 0, k.n_blocks, stream)
                                           : launch_tiles<TILES_LOGPROB, DT>(h, part, m.logits, 0, k.n_blocks, stream);

@@ -56,6 +56,7 @@ struct VocabArgs {
     int top;
     float4 *sums;                 // [2 slots][tokens]: max, S, U (see LogitSums)
     unsigned long long *lists;    // [2 slots][top][tokens]: keys, in no order
+    uint32_t *bars;               // [tokens]: the largest least logit (as in a key) of a full list so far, or NULL
     WaitLimits limits;
 };
 
@@ -741,6 +742,9 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(152)
             bool ok = true;
             const int half = warp / 4 * 128, row = it.row + (int)rank * 128 + quarter * 32 + lane;
             TileRow r = tile_row<MODE, DT>(a, g, b0, it, row, half);
+            [[maybe_unused]] uint32_t seen = 0;
+            if constexpr (Mode<MODE>::resident)
+                if (a.bars && r.live) seen = *(volatile const uint32_t *)(a.bars + row);
             auto at = [&](int c) { return sh.tmem + ((uint32_t)quarter << 21) + (sums & 1) * kTile + half + c; };
             if (Mode<MODE>::sums) {
                 // all sums but the last into registers, and these onto the last
@@ -796,10 +800,14 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(152)
                 }
             }
             if constexpr (Mode<MODE>::resident) {
-                // a second look, where a row of the warp has a column for its list
-                if (a.top && __any_sync(0xFFFFFFFFu, r.live && groups.most > top.bar())) {
-                    // (a bound that is itself a logit counts; columns beyond the block's last bound nothing)
-                    const float bound = !r.live ? INFINITY : r.cols < 128 ? -INFINITY : nextafterf(groups.bound(a.top), -INFINITY);
+                // A second look, where a row of the warp has a column for its list.  What lies below
+                // `top` logits that another pair has is not wanted; what equals the least of them may have
+                // the lower token.  (When a bar is seen decides what is noted, not what comes out.)
+                const float shared = seen ? top_value((unsigned long long)(seen - 1) << 32) : -INFINITY;
+                if (a.top && __any_sync(0xFFFFFFFFu, r.live && groups.most > fmaxf(top.bar(), shared))) {
+                    // (columns beyond the block's last bound nothing)
+                    const float bound = !r.live ? INFINITY : r.cols < 128 ? shared : fmaxf(shared, nextafterf(groups.bound(a.top), -INFINITY));
+                    const unsigned long long least = top.least;
 #pragma unroll 1
                     for (int c0 = 0; c0 < 128; c0 += 32) {
                         if (r.cols - c0 <= 0) break;
@@ -810,6 +818,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(152)
                         top.add(v, bound, c0, (uint32_t)r.first);
                     }
                     top.insert_noted((uint32_t)r.first);
+                    if (a.bars && r.live && top.least > least && (uint32_t)(top.least >> 32) > seen) atomicMax(a.bars + row, (uint32_t)(top.least >> 32));
                 }
             }
             release();
