@@ -549,7 +549,7 @@ typedef struct {
     size_t tokens, dim, vocab;  /* tokens may be 0, dim and vocab at least 1 */
     const void *targets;        /* tokens indices */
     int index_bytes;
-    float logit_scale;          /* positive and finite */
+    float logit_scale;          /* positive, at most 2^126 */
     int top;                    /* 0 .. RAR_LOGPROBS_MAX_TOP, at most vocab */
     float *logprob;             /* out: tokens, or NULL */
     float *entropy;             /* out: tokens, or NULL */

@@ -59,32 +59,39 @@ __device__ __forceinline__ float element(const GradEntry &t, long long i) {
     return load_f<DT>(t.data, r * t.stride + (i - r * t.cols));
 }
 
-// Calls f for the 16-byte vectors of elements [e0, e1) of a dense tensor, kAhead of them read
-// together, and g for the elements at the ends that fill none.
+// Calls f for the 16-byte vectors of elements [e0, e1) that lie one after the other from `base` (element
+// 0) on, kAhead of them read together, and g for the elements at the ends that fill none; as thread `tid`
+// of n, at least a vector's elements.
 template <int DT, int kAhead, typename F, typename G>
-__device__ __forceinline__ void walk(const GradEntry &t, long long e0, long long e1, F &&f, G &&g) {
+__device__ __forceinline__ void walk(const char *base, long long e0, long long e1, int tid, int n, F &&f, G &&g) {
     constexpr int VE = RowBits<DT>::VE, EB = ElemInfo<DT>::bytes;
-    const char *base = static_cast<const char *>(t.data);
     const uintptr_t at = (uintptr_t)(base + e0 * EB);
     const long long lead = min((long long)((0 - at) % 16 / EB), e1 - e0);
     const long long v0 = e0 + lead, vecs = (e1 - v0) / VE, tail = v0 + vecs * VE;
-    if (threadIdx.x < lead) g(e0 + threadIdx.x);
-    if (threadIdx.x < e1 - tail) g(tail + threadIdx.x);
+    if (tid < lead) g(e0 + tid);
+    if (tid < e1 - tail) g(tail + tid);
     const char *from = base + v0 * EB;
-    long long v = threadIdx.x;
-    for (; v + (kAhead - 1) * kGradThreads < vecs; v += kAhead * kGradThreads) {
+    long long v = tid;
+    for (; v + (kAhead - 1) * n < vecs; v += kAhead * n) {
         RowBits<DT> b[kAhead];
 #pragma unroll
-        for (int k = 0; k < kAhead; k++) b[k].load(from + (v + k * kGradThreads) * 16, 0, true);
+        for (int k = 0; k < kAhead; k++) b[k].load(from + (v + k * n) * 16, 0, true);
 #pragma unroll
-        for (int k = 0; k < kAhead; k++) f(v0 + (v + k * kGradThreads) * VE, b[k]);
+        for (int k = 0; k < kAhead; k++) f(v0 + (v + k * n) * VE, b[k]);
     }
-    for (; v < vecs; v += kGradThreads) {
+    for (; v < vecs; v += n) {
         RowBits<DT> b;
         b.load(from + v * 16, 0, true);
         f(v0 + v * VE, b);
     }
 }
+// The same for elements [e0, e1) of a matrix with gaps, a warp a row: f(row, first and last element) of its parts.
+template <typename F>
+__device__ __forceinline__ void walk_rows(const GradEntry &t, long long e0, long long e1, F &&f) {
+    for (long long r = e0 / t.cols + threadIdx.x / 32; r * t.cols < e1; r += kGradThreads / 32) f(r, max(e0, r * t.cols), min(e1, (r + 1) * t.cols));
+}
+// Rows of fewer elements go one by one, a thread each, with a division for its row.
+constexpr int kShortRow = 64;
 
 // Sum over the CTA, in every thread.
 __device__ __forceinline__ float cta_sum(float v, float *red) {
@@ -110,25 +117,30 @@ template <int DT>
 __device__ __forceinline__ double chunk_sum(const GradEntry &t, long long e0, long long e1) {
     __shared__ float red[kGradThreads / 32];
     float s[4] = {};
-    uint32_t bits = 0;
-    auto one = [&](long long i) {
-        const float x = element<DT>(t, i);
+    uint32_t bits = 0;  // of all elements
+    auto one = [&](float x) {
         bits |= __float_as_uint(x) << 1;
         s[0] = fmaf(x, x, s[0]);
     };
-    const bool dense = t.cols == t.n;
-    if (dense) {
-        walk<DT, 8>(t, e0, e1, [&](long long, const RowBits<DT> &b) {
+    auto eight = [&](long long, const RowBits<DT> &b) {
 #pragma unroll
-            for (int e = 0; e < RowBits<DT>::VE; e++) {
-                const float x = b.get(e);
-                s[e % 4] = fmaf(x, x, s[e % 4]);
-            }
-            // (not the signs)
-            bits |= DT == DT_F32 ? (b.w[0] | b.w[1] | b.w[2] | b.w[3]) << 1 : (b.w[0] | b.w[1] | b.w[2] | b.w[3]) & 0x7FFF7FFFu;
-        }, one);
+        for (int e = 0; e < RowBits<DT>::VE; e++) {
+            const float x = b.get(e);
+            s[e % 4] = fmaf(x, x, s[e % 4]);
+        }
+        // (not the signs)
+        bits |= DT == DT_F32 ? (b.w[0] | b.w[1] | b.w[2] | b.w[3]) << 1 : (b.w[0] | b.w[1] | b.w[2] | b.w[3]) & 0x7FFF7FFFu;
+    };
+    const char *data = static_cast<const char *>(t.data);
+    if (t.cols == t.n) {
+        walk<DT, 8>(data, e0, e1, threadIdx.x, kGradThreads, eight, [&](long long i) { one(load_f<DT>(data, i)); });
+    } else if (t.cols >= kShortRow) {
+        walk_rows(t, e0, e1, [&](long long r, long long r0, long long r1) {
+            const char *row = data + r * (t.stride - t.cols) * ElemInfo<DT>::bytes;
+            walk<DT, 4>(row, r0, r1, threadIdx.x % 32, 32, eight, [&](long long i) { one(load_f<DT>(row, i)); });
+        });
     } else {
-        for (long long i = e0 + threadIdx.x; i < e1; i += kGradThreads) one(i);
+        for (long long i = e0 + threadIdx.x; i < e1; i += kGradThreads) one(element<DT>(t, i));
     }
     const float sum = cta_sum((s[0] + s[1]) + (s[2] + s[3]), red);
     const bool any = __syncthreads_or(bits != 0);
@@ -212,23 +224,34 @@ __global__ void __launch_bounds__(1024) grad_norm_join_kernel(const __grid_const
 template <int DT, int OUT>
 __device__ __forceinline__ void scale_chunk(const GradEntry &t, long long e0, long long e1, float f) {
     constexpr int VE = RowBits<DT>::VE, EB = ElemInfo<DT>::bytes, OB = ElemInfo<OUT>::bytes;
+    const char *data = static_cast<const char *>(t.data);
     char *out = static_cast<char *>(t.out);
-    // the first element of a vector that is read, and where it goes
-    const long long lead = (0 - (uintptr_t)(static_cast<const char *>(t.data) + e0 * EB)) % 16 / EB;
-    if (t.cols == t.n && (uintptr_t)(out + (e0 + lead) * OB) % 16 == 0) {
-        walk<DT, 4>(t, e0, e1, [&](long long i, const RowBits<DT> &b) {
+    // elements [i0, i1) of runs that begin (element 0) at `from` and `to`
+    auto run = [&](const char *from, char *to, long long i0, long long i1, int tid, int n) {
+        const long long lead = (0 - (uintptr_t)(from + i0 * EB)) % 16 / EB;
+        if ((uintptr_t)(to + (i0 + lead) * OB) % 16) {  // vectors that are read go to no whole ones
+            for (long long i = i0 + tid; i < i1; i += n) store_f<OUT>(to, i, load_f<DT>(from, i) * f);
+            return;
+        }
+        walk<DT, 4>(from, i0, i1, tid, n, [&](long long i, const RowBits<DT> &b) {
             float v[VE];
 #pragma unroll
             for (int e = 0; e < VE; e++) v[e] = b.get(e) * f;
 #pragma unroll
-            for (int q = 0; q < VE * OB / 16; q++) store_vec<OUT>(out + i * OB, q, v + q * (16 / OB));
-        }, [&](long long i) { store_f<OUT>(t.out, i, load_f<DT>(t.data, i) * f); });
-        return;
-    }
-    for (long long i = e0 + threadIdx.x; i < e1; i += kGradThreads) {
-        const float x = element<DT>(t, i) * f;
-        const long long r = t.cols == t.n ? 0 : i / t.cols;
-        store_f<OUT>(t.out, r * t.out_stride + (i - r * t.cols), x);
+            for (int q = 0; q < VE * OB / 16; q++) store_vec<OUT>(to + i * OB, q, v + q * (16 / OB));
+        }, [&](long long i) { store_f<OUT>(to, i, load_f<DT>(from, i) * f); });
+    };
+    if (t.cols == t.n) {
+        run(data, out, e0, e1, threadIdx.x, kGradThreads);
+    } else if (t.cols >= kShortRow) {
+        walk_rows(t, e0, e1, [&](long long r, long long r0, long long r1) {
+            run(data + r * (t.stride - t.cols) * EB, out + r * (t.out_stride - t.cols) * OB, r0, r1, threadIdx.x % 32, 32);
+        });
+    } else {
+        for (long long i = e0 + threadIdx.x; i < e1; i += kGradThreads) {
+            const long long r = i / t.cols;
+            store_f<OUT>(out, r * t.out_stride + (i - r * t.cols), element<DT>(t, i) * f);
+        }
     }
 }
 

@@ -107,6 +107,7 @@ __device__ __forceinline__ void write_token(const LogprobOut &o, long long t, co
         if (o.lse) o.lse[t] = fmaf(o.scale, sums.max, log_s);
     }
     if (lane < o.top) {
+        if (top_token(key) >= o.vocab) key = 0;  // (after a wait that ran out nothing is certain but this)
         o.top_token[t * o.top + lane] = key ? (long long)top_token(key) : -1ll;
         o.top_logprob[t * o.top + lane] = key ? fmaf(o.scale, top_value(key) - sums.max, -log_s) : -INFINITY;
     }
@@ -390,7 +391,7 @@ int check_inputs(OpCheck &c, const Args *a) {
     if (a->dim < 1 || a->vocab < 1) return c.bad("dim and vocab must be at least 1");
     if (a->dim % 8) return c.bad("dim must be a multiple of 8");
     if (a->index_bytes != 4 && a->index_bytes != 8) return c.bad("index_bytes must be 4 or 8");
-    if (!(a->logit_scale > 0.0f && a->logit_scale <= 3.402823466e38f)) return c.bad("logit_scale must be positive and finite");
+    if (!(a->logit_scale > 0.0f && a->logit_scale <= 0x1p126f)) return c.bad("logit_scale must be positive and at most 2^126");
     if (!sizes_ok(a->tokens, a->dim, a->vocab, a->p)) return c.bad("the sizes are too large");
     MatrixSpan s;
     if ((rc = c.matrix("hidden", a->hidden, a->tokens, a->dim, a->hidden_stride, 2, 16, &s)) != RAR_OK) return rc;

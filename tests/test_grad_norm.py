@@ -102,7 +102,7 @@ def test_tensors_that_begin_anywhere(h, dtype):  # noqa: F811
 
 @gpu
 @pytest.mark.parametrize("dtype", DTYPES)
-@pytest.mark.parametrize("rows,cols,gap", [(3, 5, 1), (70, 64, 8), (129, 1001, 7), (9000, 2, 3), (1, 50, 6), (50, 1, 4)])
+@pytest.mark.parametrize("rows,cols,gap", [(3, 5, 1), (70, 64, 8), (129, 1001, 7), (9000, 2, 3), (1, 50, 6), (50, 1, 4), (70, 63, 2), (3, 20000, 24)])
 def test_matrices_with_gaps_and_other_orders(h, dtype, rows, cols, gap):  # noqa: F811
     g = gen(rows + cols)
     t = normal(g, rows, cols, dtype=dtype)
@@ -197,7 +197,7 @@ def test_clipping_at_any_alignment(h, dtype):  # noqa: F811
 
 @gpu
 @pytest.mark.parametrize("dtype", DTYPES)
-@pytest.mark.parametrize("rows,cols,gap", [(3, 5, 1), (129, 1001, 7), (9000, 2, 3), (70, 64, 8)])
+@pytest.mark.parametrize("rows,cols,gap", [(3, 5, 1), (129, 1001, 7), (9000, 2, 3), (70, 64, 8), (70, 63, 2), (3, 20000, 24)])
 def test_clipping_matrices_with_gaps(h, dtype, rows, cols, gap):  # noqa: F811
     g = gen(rows)
     t = normal(g, rows, cols, dtype=dtype)

@@ -116,6 +116,8 @@ SHAPES = [
     (8, 300, 520, 5003), (16, 33, 8, 9), (5, 513, 200, 3001), (64, 20, 64, 64), (64, 5, 16, 3), (2, 1100, 136, 777),
     (3, 256, 1024, 4099), (1, 640, 64, 16384), (4, 1, 2048, 32768), (8, 16, 4096, 10007), (3, 17, 1032, 5003), (8, 64, 2048, 20011),
     (1, 65, 2056, 3001), (2, 40, 16384, 700), (6, 2600, 64, 4100),
+    (3, 128, 2048, 1501), (2, 129, 2048, 9000), (1, 64, 8192, 900), (2, 65, 8192, 300), (2, 90, 4104, 601), (1, 16, 32768, 130), (1, 17, 32768, 70),
+    (2, 16700, 64, 1500), (1, 2304, 24, 70000),
 ]
 
 
@@ -149,7 +151,8 @@ def grid_inputs(g, tokens, dim, vocab, dtype, levels=4):
 @gpu
 @pytest.mark.parametrize("dtype", HALF)
 @pytest.mark.parametrize("p,tokens,dim,vocab", [(1, 1, 16, 4000), (3, 5, 8, 999), (4, 16, 64, 30011), (8, 64, 2048, 9001), (2, 70, 24, 5000),
-                                                (5, 300, 40, 2000), (3, 1300, 16, 8191), (1, 3, 8, 40)])
+                                                (5, 300, 40, 2000), (3, 1300, 16, 8191), (1, 3, 8, 40),
+                                                (2, 17000, 16, 900), (4, 600, 24, 70000), (1, 2, 16, 300000)])
 def test_equal_logits_go_to_the_lowest_token(h, dtype, p, tokens, dim, vocab):  # noqa: F811
     whole, hidden, targets = grid_inputs(gen(dim + vocab), tokens, dim, vocab, dtype)
     z = hidden.double() @ whole.double().T
@@ -163,15 +166,18 @@ def test_equal_logits_go_to_the_lowest_token(h, dtype, p, tokens, dim, vocab):  
 @gpu
 @pytest.mark.parametrize("dtype", HALF)
 @pytest.mark.parametrize("rising", [True, False])
-def test_alternatives_in_any_order_of_the_vocabulary(h, dtype, rising):  # noqa: F811
+@pytest.mark.parametrize("tokens", [3, 80, 300])
+def test_alternatives_in_any_order_of_the_vocabulary(h, dtype, rising, tokens):  # noqa: F811
     """Logits that rise, or fall, along the vocabulary: every one is better, or worse, than all before."""
-    vocab, tokens = 3000, 80
+    vocab = 3000
     digits = torch.arange(vocab, device="cuda").flip(0) if not rising else torch.arange(vocab, device="cuda")
     whole = torch.zeros(vocab, 16, dtype=dtype, device="cuda")
     whole[:, 0], whole[:, 1], whole[:, 2] = digits % 16, digits // 16 % 16, digits // 256
     hidden = torch.zeros(tokens, 16, dtype=dtype, device="cuda")
     hidden[:, 0], hidden[:, 1], hidden[:, 2] = 2.0 ** -8, 2.0 ** -4, 1.0
-    r = h.vocab_logprobs(hidden, pieces(whole, 3), torch.zeros(tokens, dtype=torch.int64, device="cuda"), top=32)
+    none = torch.zeros(tokens, dtype=torch.int64, device="cuda")
+    assert torch.equal(h.vocab_logprobs(hidden * 0, pieces(whole, 3), none, top=32).top_token, torch.arange(32, device="cuda").expand(tokens, 32))  # all equal
+    r = h.vocab_logprobs(hidden, pieces(whole, 3), none, top=32)
     want = torch.arange(32, device="cuda")
     assert torch.equal(r.top_token, (vocab - 1 - want if rising else want).expand(tokens, 32))
 
@@ -239,6 +245,21 @@ def test_impossible_and_far_logits(h, dtype, tokens):  # noqa: F811
     for name, (value, bound) in ref[0].items():
         within(getattr(r, name), value, bound, name)
     assert not bool(((r.top_token >= 100) & (r.top_token < 300)).any())
+
+
+@gpu
+@pytest.mark.parametrize("tokens", [3, 200])
+def test_scales_at_the_ends(h, tokens):  # noqa: F811
+    """A distribution that is uniform, or a single token."""
+    whole, hidden, targets = grid_inputs(gen(2), tokens, 16, 700, torch.bfloat16)
+    z = hidden.double() @ whole.double().T
+    flat = h.vocab_logprobs(hidden, [whole], targets, logit_scale=1e-30, top=2)
+    for x in (flat.lse, flat.entropy, -flat.logprob, -flat.top_logprob[:, 1]):
+        assert bool(((x.double() - math.log(700)).abs() < 2.0 ** -17).all())
+    sharp = h.vocab_logprobs(hidden, [whole], targets, logit_scale=2.0 ** 126, top=1)
+    ties = (z == z.amax(1, keepdim=True)).sum(1).double()
+    assert bool(((sharp.entropy.double() - ties.log()).abs() < 2.0 ** -17).all())
+    assert bool(((sharp.top_logprob[:, 0].double() + ties.log()).abs() < 2.0 ** -17).all())
 
 
 @gpu
@@ -527,6 +548,7 @@ def test_refusals(h):  # noqa: F811
                        (1, lambda: h.vocab_logprobs(half, pieces(torch.zeros(65, 64, dtype=torch.bfloat16, device="cuda"), 65), tok)),
                        (1, lambda: h.vocab_logprobs(half, [half], tok, logit_scale=0.0)), (1, lambda: h.vocab_logprobs(half, [half], tok, logit_scale=float("nan"))),
                        (1, lambda: h.vocab_logprobs(half, [half], tok, logit_scale=float("inf"))), (1, lambda: h.vocab_logprobs(half, [half], tok, logit_scale=-1.0)),
+                       (1, lambda: h.vocab_logprobs(half, [half], tok, logit_scale=2.0 ** 127)),
                        (1, lambda: h.vocab_logprobs_grad(half, [half], tok, one, None, one, logit_scale=0.0)),
                        (2, lambda: h.vocab_logprobs_grad(x, [x], tok, one, None, one))):
         with pytest.raises(rar.RarError) as e:
