@@ -214,9 +214,10 @@ __device__ __forceinline__ void tile_walk(const VocabArgs &a, int b0, int nb, F 
         const int tb = tiles_of(a.tokens);
         TileItem o{};
         o.k1 = (int)((a.dim + 63) / 64);
-        int turn = 0;
+        int next = 0;
         for (int r0 = 0; r0 < tb; r0 += a.width) {
-            const int w = min(a.width, tb - r0), share = pairs_a_row(pairs, w), slot = first / w;
+            const int w = min(a.width, tb - r0), share = pairs_a_row(pairs, w), slot = first / w, turn = next % share;
+            next = (turn + nb) % share;  // the blocks that are left over go to other pairs the next time
             if (slot >= share) continue;
             o.row = (r0 + first % w) * kTile;
             o.slot = slot + turn < share ? slot + turn : slot + turn - share;
@@ -228,7 +229,6 @@ __device__ __forceinline__ void tile_walk(const VocabArgs &a, int b0, int nb, F 
                 if (!f(o)) return;
                 o.begins = false;
             }
-            turn = (turn + nb) % share;  // the blocks that are left over go to other pairs the next time
         }
     }
 }
