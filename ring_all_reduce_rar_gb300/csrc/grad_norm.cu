@@ -177,6 +177,15 @@ __global__ void __launch_bounds__(kGradThreads) grad_norm_kernel(const __grid_co
     if (threadIdx.x == 0) a.sums[chunk] = s;
 }
 
+// The root of a sum of squares, rounded to binary32: that of its significand times an even power of two, in
+// binary32 (half a unit in the last place for the rounding, half for the root).  A root in binary64
+// takes some 30 operations at 2 a clock and SM, for 440 tensors most of the join's 13 us.
+__device__ __forceinline__ float norm_of(double s) {
+    if (!(s > 0.0) || isinf(s)) return (float)s;
+    const int hi = __double2hiint(s), e = ((hi >> 20) - 1023) & ~1;
+    return ldexpf(sqrtf((float)__hiloint2double(hi - e * (1 << 20), __double2loint(s))), e / 2);
+}
+
 // Sum over groups of n lanes, in each of them.
 __device__ __forceinline__ double lanes_sum(double v, int n) {
     for (int o = n / 2; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
@@ -207,7 +216,7 @@ __global__ void __launch_bounds__(1024) grad_norm_join_kernel(const __grid_const
         s = lanes_sum(s, lanes);
         if (i < a.n && sub == 0) {
             tensor[i] = s;
-            if (a.norms) a.norms[i] = (float)sqrt(s);
+            if (a.norms) a.norms[i] = norm_of(s);
         }
     }
     __syncthreads();
@@ -218,7 +227,7 @@ __global__ void __launch_bounds__(1024) grad_norm_join_kernel(const __grid_const
     if (threadIdx.x) return;
     if (!a.begins) s += *a.total;
     if (!a.ends) *a.total = s;
-    else if (a.norm) *a.norm = (float)sqrt(s);
+    else if (a.norm) *a.norm = norm_of(s);
 }
 
 template <int DT, int OUT>
