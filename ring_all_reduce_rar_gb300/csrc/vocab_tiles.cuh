@@ -566,8 +566,10 @@ __device__ __forceinline__ void tile_columns(const VocabArgs &a, TileRow &r, int
 #pragma unroll
         for (int c = 0; c < 32; c++) {
             if constexpr (Mode<MODE>::logprob) {
-                const float logp = fmaf(v[c], a.scale, -r.lse), w = fmaf(r.w_log, logp, r.w);
-                v[c] = c < cols && r.used ? fmaf(exp_of(logp), w, c == y ? r.w_target : 0.0f) : 0.0f;
+                // (every step for every column: one that is made on a condition becomes a branch)
+                const float logp = fmaf(v[c], a.scale, -r.lse), w = fmaf(r.w_log, logp, r.w), p = exp_of(logp);
+                const float x = fmaf(p, w, c == y ? r.w_target : 0.0f);
+                v[c] = c < cols && r.used ? x : 0.0f;
             } else {
                 const float p = exp_of(v[c] - r.lse) - (c == y ? 1.0f : 0.0f);
                 v[c] = c < cols && r.w != 0.0f ? p * r.w : 0.0f;
