@@ -60,10 +60,10 @@ __device__ __forceinline__ float element(const GradEntry &t, long long i) {
 }
 
 // Calls f for the 16-byte vectors of elements [e0, e1) that lie one after the other from `base` (element
-// 0) on, kAhead of them read together, and g for the elements at the ends that fill none; as thread `tid`
-// of n, at least a vector's elements.
-template <int DT, int kAhead, typename F, typename G>
-__device__ __forceinline__ void walk(const char *base, long long e0, long long e1, int tid, int n, F &&f, G &&g) {
+// 0) on, kAhead of them read together and `after` called after these, and g for the elements at the ends that
+// fill none; as thread `tid` of n, at least a vector's elements.
+template <int DT, int kAhead, typename F, typename G, typename H>
+__device__ __forceinline__ void walk(const char *base, long long e0, long long e1, int tid, int n, F &&f, G &&g, H &&after) {
     constexpr int VE = RowBits<DT>::VE, EB = ElemInfo<DT>::bytes;
     const uintptr_t at = (uintptr_t)(base + e0 * EB);
     const long long lead = min((long long)((0 - at) % 16 / EB), e1 - e0);
@@ -78,6 +78,7 @@ __device__ __forceinline__ void walk(const char *base, long long e0, long long e
         for (int k = 0; k < kAhead; k++) b[k].load(from + (v + k * n) * 16, 0, true);
 #pragma unroll
         for (int k = 0; k < kAhead; k++) f(v0 + (v + k * n) * VE, b[k]);
+        after();
     }
     for (; v < vecs; v += n) {
         RowBits<DT> b;
@@ -116,7 +117,13 @@ __device__ __forceinline__ float cta_max(float v, float *red) {
 template <int DT>
 __device__ __forceinline__ double chunk_sum(const GradEntry &t, long long e0, long long e1) {
     __shared__ float red[kGradThreads / 32];
-    float s[4] = {};
+    // (a long run of additions to one sum of squares loses more than their rounding's share: those of 256 bf16 values
+    // come out 2.5e-7 low, of 16 1e-8; so what a few loads bring is added up first)
+    float s[4] = {}, total = 0.0f;
+    auto batch = [&] {
+        total += (s[0] + s[1]) + (s[2] + s[3]);
+        s[0] = s[1] = s[2] = s[3] = 0.0f;
+    };
     uint32_t bits = 0;  // of all elements
     auto one = [&](float x) {
         bits |= __float_as_uint(x) << 1;
@@ -133,16 +140,21 @@ __device__ __forceinline__ double chunk_sum(const GradEntry &t, long long e0, lo
     };
     const char *data = static_cast<const char *>(t.data);
     if (t.cols == t.n) {
-        walk<DT, 8>(data, e0, e1, threadIdx.x, kGradThreads, eight, [&](long long i) { one(load_f<DT>(data, i)); });
+        walk<DT, 8>(data, e0, e1, threadIdx.x, kGradThreads, eight, [&](long long i) { one(load_f<DT>(data, i)); }, batch);
     } else if (t.cols >= kShortRow) {
         walk_rows(t, e0, e1, [&](long long r, long long r0, long long r1) {
             const char *row = data + r * (t.stride - t.cols) * ElemInfo<DT>::bytes;
-            walk<DT, 4>(row, r0, r1, threadIdx.x % 32, 32, eight, [&](long long i) { one(load_f<DT>(row, i)); });
+            walk<DT, 4>(row, r0, r1, threadIdx.x % 32, 32, eight, [&](long long i) { one(load_f<DT>(row, i)); }, [] {});
+            batch();
         });
     } else {
-        for (long long i = e0 + threadIdx.x; i < e1; i += kGradThreads) one(element<DT>(t, i));
+        for (long long i = e0 + threadIdx.x; i < e1; i += kGradThreads) {
+            one(element<DT>(t, i));
+            if ((i / kGradThreads) % 16 == 15) batch();
+        }
     }
-    const float sum = cta_sum((s[0] + s[1]) + (s[2] + s[3]), red);
+    batch();
+    const float sum = cta_sum(total, red);
     const bool any = __syncthreads_or(bits != 0);
     // Squares that pass binary32 or vanish in it: the chunk once more, relative to its largest
     // element (in these bounds what was lost is below 2^-24 of the sum for a chunk of 2^30 elements)
@@ -248,7 +260,7 @@ __device__ __forceinline__ void scale_chunk(const GradEntry &t, long long e0, lo
             for (int e = 0; e < VE; e++) v[e] = b.get(e) * f;
 #pragma unroll
             for (int q = 0; q < VE * OB / 16; q++) store_vec<OUT>(to + i * OB, q, v + q * (16 / OB));
-        }, [&](long long i) { store_f<OUT>(to, i, load_f<DT>(from, i) * f); });
+        }, [&](long long i) { store_f<OUT>(to, i, load_f<DT>(from, i) * f); }, [] {});
     };
     if (t.cols == t.n) {
         run(data, out, e0, e1, threadIdx.x, kGradThreads);
