@@ -2,7 +2,8 @@
 // once, with the vocabulary along the tensor cores' 128 rows and the tokens along
 // their columns.
 //
-// Bound by memory: 2 vocab x dim bytes.  A CTA an SM takes passes of up to 256
+// Bound by memory: 2 vocab x dim bytes.  65536 x 4096 bf16 take 85 us for 16 tokens and 89 for 64 (6.0 to 6.3
+// TB/s, 0.9 of a copy); 32768 x 2048 26 us, of which some 5 are the first loads' and the last epilogue's.  A CTA an SM takes passes of up to 256
 // vocabulary rows, as many in each as give all CTAs the same share; a stage of its
 // ring holds 64 columns of dim of all the pass's rows, one box, and of the hidden states, so
 // that these are read once a pass.  A sum of 1024 of dim has accumulators of its own (see

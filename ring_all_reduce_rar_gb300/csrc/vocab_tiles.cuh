@@ -379,7 +379,8 @@ struct GroupMaxima {
 // side by side, so that a step of a warp serves all of its rows (column by column, with a step for each
 // column that any of 32 rows wants, there would be several times as many).  A new key takes
 // the place of the least one; which is the least then is known from the 8 places around and the other
-// groups' least, in registers.
+// groups' least, in registers.  (2048 tokens by 50021 x 2048 fp16: 280 us without alternatives, 303 with 1, 342
+// with 8, 507 with 32; with a look at all places for each key 876 with 32.)
 struct TileTop {
     static constexpr int kNoted = 24, kRow = 32 * kTcEpilogueWarps, kGroups = RAR_LOGPROBS_MAX_TOP / 8;
     static constexpr int kNotedBytes = kNoted * kRow * 5;
