@@ -18,7 +18,7 @@
 //   up to 128 tokens (stream_fits), memory: the pieces are streamed once (vocab_stream.cuh), the logits go
 //     through L2 to a cluster of CTAs a token.  16 tokens by 65536 x 4096 bf16: 85 us for 537 MB (6.3 TB/s), 102 us
 //     with the selection of 5 alternatives; 1 by 32768 x 2048: 26 us, 37 with 20.  By tiles 64 tokens by 32768 x
-//     2048 took 75 us with 8 alternatives, here 57; 128 by 4096 x 50021, whose accumulators leave room for one
+//     2048 took 75 us with 8 alternatives, here 56 with 5; 128 by 4096 x 50021, whose accumulators leave room for one
 //     tile of rows at a time, took longer here than by tiles (160 us for the logits alone), so that is left to them.
 //   above, the tensor cores: tiles whose epilogues keep sums and alternatives (vocab_tiles.cuh), joined by token.  8192
 //     by 65536 x 4096 bf16 2.46 ms (1.79 PFLOP/s at the power limit), 2048 by 50021 x 2048 fp16 280 us, with 8
@@ -131,13 +131,15 @@ struct SelectArgs {
     long long pitch;
 };
 
-// Warps of a CTA, CTAs of a token, 16-byte loads that a lane has in flight.  A round of these loads costs a
-// sort whatever it brings, so rounds are long: a whole call for 16 tokens by 65536 x 4096 bf16 with 5
-// alternatives takes 101 us, 107 with 8 warps of 4 loads; 64 by 32768 x 2048 56 us with either.
-constexpr int kSelectWarps = 4, kSelectCluster = 8, kSelectAhead = 16, kSelectNoted = 256;
+// Warps of a CTA, CTAs of a token at most.
+constexpr int kSelectWarps = 4, kSelectCluster = 8, kSelectNoted = 256;
 
 // Everything about a token from its logits, for few tokens: a cluster of CTAs a token, each with a range
-// of the vocabulary, whose warps keep sums and a list of their own.
+// of the vocabulary, whose warps keep sums and a list of their own.  AHEAD: 16-byte loads that a lane has in flight.  A
+// round of these loads costs a sort whatever it brings, so there is one round where 16 loads suffice for the
+// range: a whole call for 16 tokens by 65536 x 4096 bf16 with 5 alternatives takes 101 us, 107 in rounds of 4
+// with 8 warps.  Where fewer do, fewer: the others' instructions are executed, too.
+template <int AHEAD>
 __global__ void __launch_bounds__(32 * kSelectWarps) logprob_select_kernel(const __grid_constant__ SelectArgs a) {
     __shared__ unsigned long long lists[kSelectWarps][32], noted[kSelectWarps][kSelectNoted];
     __shared__ float3 sums[kSelectWarps];
@@ -152,31 +154,31 @@ __global__ void __launch_bounds__(32 * kSelectWarps) logprob_select_kernel(const
     const uint32_t v0 = (uint32_t)((unsigned long long)vecs * rank / ctas), v1 = (uint32_t)((unsigned long long)vecs * (rank + 1) / ctas);
     LogitSums own;
     TopList list;
-    for (uint32_t v = v0 + warp * 32; v < v1; v += 32 * kSelectWarps * kSelectAhead) {
-        float z[4 * kSelectAhead];
+    for (uint32_t v = v0 + warp * 32; v < v1; v += 32 * kSelectWarps * AHEAD) {
+        float z[4 * AHEAD];
         const uint32_t at = v + lane;
 #pragma unroll
-        for (int u = 0; u < kSelectAhead; u++) {  // loads in flight together
+        for (int u = 0; u < AHEAD; u++) {  // loads in flight together
             float4 q = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
             if (at + u * 32 * kSelectWarps < v1) q = __ldcg(reinterpret_cast<const float4 *>(row) + at + u * 32 * kSelectWarps);
             z[4 * u] = q.x, z[4 * u + 1] = q.y, z[4 * u + 2] = q.z, z[4 * u + 3] = q.w;
         }
         auto token = [&](int i) { return (at + (i / 4) * 32 * kSelectWarps) * 4 + i % 4; };
 #pragma unroll
-        for (int i = 0; i < 4 * kSelectAhead; i++)
+        for (int i = 0; i < 4 * AHEAD; i++)
             if (token(i) >= vocab) z[i] = -INFINITY;  // (behind the row's last)
         own.add(z, k);
         if (!top) continue;
         float best = z[0];
 #pragma unroll
-        for (int i = 1; i < 4 * kSelectAhead; i++) best = fmaxf(best, z[i]);
+        for (int i = 1; i < 4 * AHEAD; i++) best = fmaxf(best, z[i]);
         const float full = list.least ? top_value(list.least) : -INFINITY;
         if (!__any_sync(0xFFFFFFFFu, best >= full)) continue;
         const unsigned long long bound = top_bound(list, best > -INFINITY ? top_key(best, 0) : 0ull, top);
         const float bar = bound ? top_value(bound) : -INFINITY;
         int n = 0;  // noted so far
 #pragma unroll
-        for (int i = 0; i < 4 * kSelectAhead; i++) {
+        for (int i = 0; i < 4 * AHEAD; i++) {
             const bool wanted = z[i] >= bar && z[i] > -INFINITY;
             const unsigned who = __ballot_sync(0xFFFFFFFFu, wanted);
             if (wanted) noted[warp][n + __popc(who & ((1u << lane) - 1))] = top_key(z[i], token(i));
@@ -394,7 +396,8 @@ size_t plan_gradients(void *base, size_t tokens, size_t dim, size_t vocab, int p
     k->row_weight = w.take<float>(tokens);
     k->row_entropy = w.take<float>(tokens);
     k->pair = tokens <= kPairedTokens ? (long long)tokens : 0;
-    plan_grad(w, k->pair ? 2 * tokens : tokens, dim, k);
+    // (one round: 333 tokens by 10007 x 520 63 us, 66 with two, 71 with three)
+    plan_grad(w, k->pair ? 2 * tokens : tokens, dim, 1, k);
     return w.used;
 }
 
@@ -442,9 +445,10 @@ void set_inputs(rar_ctx *h, const Args *a, VocabArgs *k) {
 struct Vec { const char *name; const void *ptr; size_t n, eb; };
 
 cudaError_t launch_select(const rar_ctx *h, const SelectArgs &s, int tokens, cudaStream_t stream) {
-    // CTAs a token: until there are two an SM, but at least 1024 logits each
+    // CTAs a token: until there are two an SM, but at least 2048 logits each (with 1024, 90 tokens by 4000 x 512 took 27 us,
+    // now 24)
     unsigned ctas = 1;
-    while (ctas < kSelectCluster && tokens * (int)ctas < 2 * h->sm_count && s.out.vocab / (2 * ctas) >= 1024) ctas *= 2;
+    while (ctas < kSelectCluster && tokens * (int)ctas < 2 * h->sm_count && s.out.vocab / (2 * ctas) >= 2048) ctas *= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas, (unsigned)tokens);
     cfg.blockDim = dim3(32 * kSelectWarps);
@@ -458,7 +462,9 @@ cudaError_t launch_select(const rar_ctx *h, const SelectArgs &s, int tokens, cud
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, logprob_select_kernel, s);
+    const long long range = ((s.out.vocab + 3) / 4 + ctas - 1) / ctas, loads = (range + 32 * kSelectWarps - 1) / (32 * kSelectWarps);
+    return cudaLaunchKernelEx(&cfg, loads <= 2 ? logprob_select_kernel<2> : loads <= 4 ? logprob_select_kernel<4> : loads <= 8 ? logprob_select_kernel<8>
+                                                                                                        : logprob_select_kernel<16>, s);
 }
 
 int vocab_logprobs(rar_ctx *h, const rar_vocab_logprobs_args *a, cudaStream_t stream) {

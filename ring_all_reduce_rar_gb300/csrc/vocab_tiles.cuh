@@ -358,7 +358,8 @@ struct GroupMaxima {
         float m4[8];
 #pragma unroll
         for (int i = 0; i < 8; i++) {
-            m4[i] = fmaxf(fmaxf(v[4 * i], v[4 * i + 1]), fmaxf(v[4 * i + 2], v[4 * i + 3]));
+            // (-infinity where all four are NaN: a group without a logit bounds nothing)
+            m4[i] = fmaxf(fmaxf(fmaxf(v[4 * i], v[4 * i + 1]), fmaxf(v[4 * i + 2], v[4 * i + 3])), -INFINITY);
             least4 = fminf(least4, m4[i]);
         }
 #pragma unroll
@@ -928,7 +929,8 @@ void plan_blocks(size_t vocab, int p, VocabArgs *k) {
 }
 
 // The gradients' share of a workspace: G for a window of blocks, and dhidden's sums.  tokens: rows of G.
-void plan_grad(WorkspacePlan &w, size_t tokens, size_t dim, VocabArgs *k) {
+// rounds: tiles a pair of SMs that dhidden's sum is split into.
+void plan_grad(WorkspacePlan &w, size_t tokens, size_t dim, size_t rounds, VocabArgs *k) {
     const size_t n_blocks = (size_t)k->n_blocks;
     k->hidden_used = w.take<uint16_t>(tokens * dim);
     size_t window = kWindowBytes / (sizeof(uint16_t) * kBlock * std::max<size_t>(tokens, 1));
@@ -936,9 +938,9 @@ void plan_grad(WorkspacePlan &w, size_t tokens, size_t dim, VocabArgs *k) {
     k->window = (int)window;
     k->g = w.take<uint16_t>(tokens * window * kBlock);
     // few tiles: dhidden's sum over the window is split until there are
-    // about two tiles a pair of SMs
+    // about so many
     const size_t tiles = ((tokens + kTile - 1) / kTile) * ((dim + kTile - 1) / kTile);
-    const size_t splits = std::min(std::max<size_t>(2 * kPairs / std::max<size_t>(tiles, 1), 1), window);
+    const size_t splits = std::min(std::max<size_t>(rounds * kPairs / std::max<size_t>(tiles, 1), 1), window);
     k->splits = (int)splits;
     k->direct = splits == 1 && !k->pair;
     k->dh_part = w.take<float>(window < n_blocks || !k->direct ? splits * tokens * dim : 0);

@@ -107,7 +107,7 @@ size_t plan(void *base, size_t tokens, size_t dim, size_t vocab, int p, bool gra
     if (grad) {
         k->lse_ws = w.take<float>(tokens);
         k->row_weight = w.take<float>(tokens);
-        plan_grad(w, tokens, dim, k);
+        plan_grad(w, tokens, dim, 2, k);
     }
     return w.used;
 }

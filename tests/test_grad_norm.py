@@ -247,7 +247,7 @@ def test_more_than_32_bits_of_elements(h):  # noqa: F811
 def test_on_another_stream_and_in_graphs(h):  # noqa: F811
     g = gen(3)
     a = some_tensors(g, ODD, DTYPES)
-    b = some_tensors(g, [(70000,), (5, 3)], [torch.float32])
+    b = some_tensors(g, [(70000,), (5, 3)] * 300, [torch.float32])
     for t in (a, b):
         want = h.grad_norm(t)
         torch.cuda.synchronize()

@@ -226,6 +226,27 @@ def test_bad_rows_stay_alone(h, dtype, tokens):  # noqa: F811
 
 
 @gpu
+@pytest.mark.parametrize("tokens", [5, 200])
+@pytest.mark.parametrize("dtype", HALF)
+def test_runs_of_nan_in_the_vocabulary(h, dtype, tokens):  # noqa: F811
+    """Logits around runs of rows that hold NaN are still listed, in their order."""
+    vocab = 1500
+    whole, hidden, targets = grid_inputs(gen(6), tokens, 16, vocab, dtype)
+    z = hidden.double() @ whole.double().T
+    for runs in ([(4, 8)], [(0, 64), (128, 256), (300, 304)], [(0, vocab - 40)], [(20, vocab)]):
+        bad = whole.clone()
+        left = torch.ones(vocab, dtype=torch.bool, device="cuda")
+        for lo, hi in runs:
+            bad[lo:hi, 3] = float("nan")
+            left[lo:hi] = False
+        order = torch.sort(torch.where(left, z, torch.full_like(z, -1e9)), dim=1, descending=True, stable=True).indices
+        for top in (1, 8, 16, 32):
+            r = h.vocab_logprobs(hidden, pieces(bad, 3), targets, top=top)
+            n = min(top, int(left.sum()))
+            assert torch.equal(r.top_token[:, :n], order[:, :n]) and bool((r.top_token[:, n:] == -1).all())
+
+
+@gpu
 @pytest.mark.parametrize("tokens", [3, 130])
 @pytest.mark.parametrize("dtype", HALF)
 def test_impossible_and_far_logits(h, dtype, tokens):  # noqa: F811
