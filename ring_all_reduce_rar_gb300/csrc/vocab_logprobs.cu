@@ -524,7 +524,8 @@ int vocab_logprobs(rar_ctx *h, const rar_vocab_logprobs_args *a, cudaStream_t st
             const int tb = tiles_of(part.tokens);
             part.width = choose_width(tb, k.n_blocks, (int)kPairs);
             part.pairs = std::min(std::min(h->sm_count / 2, (int)kPairs), std::min(tb, part.width) * k.n_blocks);
-            // (a pair with one tile of a row learns nothing from the others)
+            // (a pair with one tile of a row has little to learn from the others, who are at theirs: 98 us against 104 for
+            // 333 tokens by 10007 x 520 with 32 alternatives, none with 8)
             const bool share = a->top && k.n_blocks > pairs_a_row(part.pairs, std::min(part.width, tb));
             if (!share) part.bars = nullptr;
             else if ((e = cudaMemsetAsync(part.bars, 0, sizeof(uint32_t) * (size_t)part.tokens, stream)) != cudaSuccess) return e;

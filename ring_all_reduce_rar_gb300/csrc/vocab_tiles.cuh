@@ -351,28 +351,28 @@ struct LogitSums {
     }
 };
 
-// Bounds of the k-th largest of a row's columns: the least of the maxima of k groups of them.
-struct GroupMaxima {
-    float most = -INFINITY, least4 = INFINITY, least8 = INFINITY, least16 = INFINITY;  // of all, of groups of 4, 8, 16
-    __device__ __forceinline__ void add(const float (&v)[32]) {
-        float m4[8];
+// Maxima of groups of 4 columns (-infinity where all four are NaN: a group without a logit bounds nothing).
+__device__ __forceinline__ void group_maxima(const float (&v)[32], float (&m)[8]) {
 #pragma unroll
-        for (int i = 0; i < 8; i++) {
-            // (-infinity where all four are NaN: a group without a logit bounds nothing)
-            m4[i] = fmaxf(fmaxf(fmaxf(v[4 * i], v[4 * i + 1]), fmaxf(v[4 * i + 2], v[4 * i + 3])), -INFINITY);
-            least4 = fminf(least4, m4[i]);
-        }
+    for (int i = 0; i < 8; i++) m[i] = fmaxf(fmaxf(fmaxf(v[4 * i], v[4 * i + 1]), fmaxf(v[4 * i + 2], v[4 * i + 3])), -INFINITY);
+}
+// In falling order (Batcher's odd-even merges: runs of P into runs of 2 P, by steps of K = P, P / 2, .. 1).
+// (Template arguments: with loop variables in their place x would lie in memory.)
+template <int P = 1, int K = P>
+__device__ __forceinline__ void sort_falling(float (&x)[32]) {
 #pragma unroll
-        for (int i = 0; i < 8; i += 4) {
-            const float a = fmaxf(m4[i], m4[i + 1]), b = fmaxf(m4[i + 2], m4[i + 3]), c = fmaxf(a, b);
-            least8 = fminf(least8, fminf(a, b));
-            least16 = fminf(least16, c);
-            most = fmaxf(most, c);
+    for (int n = 0; n < 32; n++) {
+        constexpr int kFirst = K % P;
+        const bool leads = n >= kFirst && (n - kFirst) % (2 * K) < K && n + K < 32 && n / (2 * P) == (n + K) / (2 * P);
+        if (leads) {
+            const float hi = fmaxf(x[n], x[n + K < 32 ? n + K : n]);
+            x[n + K < 32 ? n + K : n] = fminf(x[n], x[n + K < 32 ? n + K : n]);
+            x[n] = hi;
         }
     }
-    // a logit below this is not among the `top` largest of 128
-    __device__ __forceinline__ float bound(int top) const { return top == 1 ? most : top <= 8 ? least16 : top <= 16 ? least8 : least4; }
-};
+    if constexpr (K > 1) sort_falling<P, K / 2>(x);
+    else if constexpr (P < 16) sort_falling<2 * P>(x);
+}
 
 // The `top` largest keys that a thread has seen, in shared memory: place i of thread t at
 // [i][t], so that a warp's accesses meet no bank twice.  Each thread first notes the columns
@@ -380,8 +380,10 @@ struct GroupMaxima {
 // side by side, so that a step of a warp serves all of its rows (column by column, with a step for each
 // column that any of 32 rows wants, there would be several times as many).  A new key takes
 // the place of the least one; which is the least then is known from the 8 places around and the other
-// groups' least, in registers.  (2048 tokens by 50021 x 2048 fp16: 280 us without alternatives, 303 with 1, 342
-// with 8, 507 with 32; with a look at all places for each key 876 with 32.)
+// groups' least, in registers.  In a row's first tile the bound is the `top`-th largest of the maxima of 32
+// groups of columns.  (2048 tokens by 50021 x 2048 fp16: 280 us without alternatives, 303 with 1, 339
+// with 8, 429 with 32; with the least of as many groups' maxima for a bound 342 and 507, with a look at all
+// places for each key 876 with 32.)
 struct TileTop {
     static constexpr int kNoted = 24, kRow = 32 * kTcEpilogueWarps, kGroups = RAR_LOGPROBS_MAX_TOP / 8;
     static constexpr int kNotedBytes = kNoted * kRow * 5;
@@ -432,6 +434,28 @@ struct TileTop {
             if (i == 0 || group[i] < least) least = group[i], worst = i;
         }
         at |= worst * 8 + (at >> (8 + 3 * worst) & 7u);
+    }
+    // The first tile of a row: maxima of its groups of columns c0 .. c0 + 31, before the list is there, and the
+    // `top`-th largest of them all, which so many logits are not below.
+    // (They lie where this thread's logits are noted, and the last ones in its list's first places: no
+    // other thread's, which may be at another row.)
+    __device__ __forceinline__ uint32_t maximum_at(int i) const {
+        return i < kNoted ? noted + i * kRow * 4 : list + (i - kNoted) / 2 * kRow * 8 + (i - kNoted) % 2 * 4;
+    }
+    static_assert(kNoted % 8 == 0 && kNoted + 16 >= 32, "8 places of a list take what the noted ones leave");
+    __device__ __forceinline__ void keep_maxima(const float (&m)[8], int c0) {
+#pragma unroll
+        for (int i = 0; i < 8; i++) asm volatile("st.shared.f32 [%0], %1;" ::"r"(maximum_at(c0 / 4 + i)), "f"(m[i]) : "memory");
+    }
+    __device__ __forceinline__ float bound_of_maxima(int top) const {
+        float x[32], b = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 32; i++) asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x[i]) : "r"(maximum_at(i)));
+        sort_falling(x);
+#pragma unroll
+        for (int i = 0; i < 32; i++)  // (in this form x stays in registers)
+            asm("{\n\t.reg .pred P;\n\tsetp.eq.s32 P, %1, %2;\n\tselp.f32 %0, %3, %0, P;\n\t}" : "+f"(b) : "r"(top - 1), "r"(i), "f"(x[i]));
+        return b;
     }
     // what has to be passed to get into the list
     __device__ __forceinline__ float bar() const { return least ? top_value(least) : -INFINITY; }
@@ -782,12 +806,14 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(152)
             } else if (!ready()) {
                 return false;
             }
-            if constexpr (Mode<MODE>::resident)
-                if (it.begins) {
-                    own = LogitSums();
-                    if (a.top) top.clear(a.top);
+            [[maybe_unused]] float most = -INFINITY;
+            if constexpr (Mode<MODE>::resident) {
+                if (it.begins) own = LogitSums();
+                if (it.begins && r.cols < 128 && a.top > 1) {  // (columns that the block does not have)
+                    const float none[8] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY, -INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    for (int c0 = 0; c0 < 128; c0 += 32) top.keep_maxima(none, c0);
                 }
-            [[maybe_unused]] GroupMaxima groups;
+            }
 #pragma unroll 1
             for (int c0 = 0; c0 < 128; c0 += 32) {
                 float v[32];
@@ -798,19 +824,35 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(152)
                     mask_columns(v, r.cols - c0);
                     keep_target(a, r, c0, v);
                     own.add(v, a.scale * 1.4426950408889634f);
-                    if (a.top) groups.add(v);
+                    if (a.top) {
+                        float m[8];
+                        group_maxima(v, m);
+#pragma unroll
+                        for (int i = 0; i < 8; i++) most = fmaxf(most, m[i]);
+                        if (it.begins && a.top > 1) top.keep_maxima(m, c0);
+                    }
                 } else {
                     tile_columns<MODE, DT>(a, r, c0, undo, first_window, direct, v);
                 }
             }
             if constexpr (Mode<MODE>::resident) {
                 // A second look, where a row of the warp has a column for its list.  What lies below
-                // `top` logits that another pair has is not wanted; what equals the least of them may have
-                // the lower token.  (When a bar is seen decides what is noted, not what comes out.)
-                const float shared = seen ? top_value((unsigned long long)(seen - 1) << 32) : -INFINITY;
-                if (a.top && __any_sync(0xFFFFFFFFu, r.live && groups.most > fmaxf(top.bar(), shared))) {
-                    // (columns beyond the block's last bound nothing)
-                    const float bound = !r.live ? INFINITY : r.cols < 128 ? shared : fmaxf(shared, nextafterf(groups.bound(a.top), -INFINITY));
+                // `top` logits of this tile, or of those that another pair has, is not wanted; what equals the least
+                // of them may have the lower token.  (When a bar is seen decides what is noted, not what comes out.)
+                float bound = -INFINITY;
+                if (a.top && it.begins) {
+                    bound = a.top == 1 ? most : top.bound_of_maxima(a.top);
+                    top.clear(a.top);
+                    if (a.bars && r.live && bound > -INFINITY) {
+                        const uint32_t bar = (uint32_t)(top_key(bound, 0) >> 32);
+                        if (bar > seen) atomicMax(a.bars + row, bar);
+                        seen = *(volatile const uint32_t *)(a.bars + row);
+                    }
+                    bound = nextafterf(bound, -INFINITY);
+                }
+                if (seen) bound = fmaxf(bound, top_value((unsigned long long)(seen - 1) << 32));
+                if (!r.live) bound = INFINITY;
+                if (a.top && __any_sync(0xFFFFFFFFu, most > fmaxf(top.bar(), bound))) {
                     const unsigned long long least = top.least;
 #pragma unroll 1
                     for (int c0 = 0; c0 < 128; c0 += 32) {

@@ -103,6 +103,7 @@ def check(r, ref, top):
         return
     # each alternative has its own log probability, none comes twice, and the k-th is as likely as the k-th of all
     assert r.top_token.dtype == torch.int64 and r.top_token.shape == (logp.shape[0], top) == r.top_logprob.shape
+    assert bool(((r.top_token >= 0) & (r.top_token < logp.shape[1])).all())
     within(r.top_logprob, logp.gather(1, r.top_token), dany.gather(1, r.top_token), "alternatives")
     best = torch.topk(logp, top, dim=1)
     within(r.top_logprob, best.values, dany.amax(1, keepdim=True).expand_as(best.values), "alternatives' order")
