@@ -65,7 +65,8 @@ __device__ __noinline__ TopList top_add(TopList list, unsigned long long x, int 
     const int lane = threadIdx.x % 32;
     unsigned more = __ballot_sync(0xFFFFFFFFu, x > list.least);
     if (__popc(more) > 6) {  // sorted and merged, 20 steps: as much as inserting six
-        list.key = top_merged(list.key, top_sorted(x));
+        x = top_sorted(x);
+        list.key = __any_sync(0xFFFFFFFFu, list.key) ? top_merged(list.key, x) : x;
         list.least = __shfl_sync(0xFFFFFFFFu, list.key, top - 1);
         return list;
     }
@@ -80,10 +81,17 @@ __device__ __noinline__ TopList top_add(TopList list, unsigned long long x, int 
     }
     return list;
 }
-// The lanes' largest of several keys each, in falling order: as many keys as there are lanes above one of
-// these are not below it.  What is below the one at `top` is not among the `top` largest.
-__device__ __forceinline__ unsigned long long top_bound(const TopList &list, unsigned long long best, int top) {
-    return list.least ? list.least : __shfl_sync(0xFFFFFFFFu, top_sorted(best), top - 1);
+// The lanes' values, no NaN among them, in falling order (as top_sorted).
+__device__ __noinline__ float falling(float x) {
+    const int lane = threadIdx.x % 32;
+#pragma unroll 1
+    for (int n = 2; n <= 32; n *= 2)
+#pragma unroll 1
+        for (int d = n / 2; d; d /= 2) {
+            const float y = __shfl_xor_sync(0xFFFFFFFFu, x, d);
+            x = ((lane & d) == 0) == ((lane & n) == 0) ? fmaxf(x, y) : fminf(x, y);
+        }
+    return x;
 }
 // takes the keys noted in shared memory
 __device__ __noinline__ TopList top_add_noted(TopList list, const unsigned long long *noted, int n, int top) {
@@ -169,13 +177,13 @@ __global__ void __launch_bounds__(32 * kSelectWarps) logprob_select_kernel(const
             if (token(i) >= vocab) z[i] = -INFINITY;  // (behind the row's last)
         own.add(z, k);
         if (!top) continue;
+        // each lane's best: of these in falling order, what is below the one at `top` is not among the `top` largest
         float best = z[0];
 #pragma unroll
         for (int i = 1; i < 4 * AHEAD; i++) best = fmaxf(best, z[i]);
         const float full = list.least ? top_value(list.least) : -INFINITY;
         if (!__any_sync(0xFFFFFFFFu, best >= full)) continue;
-        const unsigned long long bound = top_bound(list, best > -INFINITY ? top_key(best, 0) : 0ull, top);
-        const float bar = bound ? top_value(bound) : -INFINITY;
+        const float bar = list.least ? full : __shfl_sync(0xFFFFFFFFu, falling(fmaxf(best, -INFINITY)), top - 1);
         int n = 0;  // noted so far
 #pragma unroll
         for (int i = 0; i < 4 * AHEAD; i++) {
@@ -190,7 +198,7 @@ __global__ void __launch_bounds__(32 * kSelectWarps) logprob_select_kernel(const
         }
         list = top_add_noted(list, noted[warp], n, top);
     }
-    own.join_lanes(32, k);
+    own.join_lanes(k);
     lists[warp][lane] = list.key;
     if (lane == 0) sums[warp] = make_float3(own.max, own.s, own.u);
     // the CTA's, and then the cluster's, in warp 0 of its first CTA
@@ -206,7 +214,7 @@ __global__ void __launch_bounds__(32 * kSelectWarps) logprob_select_kernel(const
         if (warp == 0) {
             own = LogitSums();
             if (lane < n) own.join(sums[lane].x, sums[lane].y, sums[lane].z, k);
-            own.join_lanes(32, k);
+            own.join_lanes(k);
         }
     };
     join(kSelectWarps);
@@ -275,7 +283,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) logprob_join_kernel(const __g
 #pragma unroll
         for (int u = 0; u < kJoinAhead; u++) best = x[u] > best ? x[u] : best;
         if (!__any_sync(0xFFFFFFFFu, best > list.least)) continue;
-        const unsigned long long bound = top_bound(list, best, a.top);
+        // (see logprob_select_kernel)
+        const unsigned long long bound = list.least ? list.least : __shfl_sync(0xFFFFFFFFu, top_sorted(best), a.top - 1);
         int m = 0;  // noted so far
 #pragma unroll
         for (int u = 0; u < kJoinAhead; u++) {
@@ -293,7 +302,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) logprob_join_kernel(const __g
             for (int w = 1; w < kWarps; w++) list.key = top_merged(list.key, found[w][lane]);
     }
     if (part) return;
-    own.join_lanes(32, k);
+    own.join_lanes(k);
     write_token(o, t, own, z, list.key);
 }
 

@@ -334,19 +334,16 @@ struct LogitSums {
         s += o.s;
         u += o.u;
     }
-    // over the lanes, in an order that gives every lane the same bits
-    __device__ __forceinline__ void join_lanes(int lanes, float k) {
-        const int lane = threadIdx.x % 32;
-#pragma unroll 1
-        for (int d = 1; d < lanes; d *= 2) {
-            const float om = __shfl_xor_sync(0xFFFFFFFFu, max, d), os = __shfl_xor_sync(0xFFFFFFFFu, s, d), ou = __shfl_xor_sync(0xFFFFFFFFu, u, d);
-            if (lane & d) {
-                LogitSums o{om, os, ou};
-                o.join(max, s, u, k);
-                *this = o;
-            } else {
-                join(om, os, ou, k);
-            }
+    // over all lanes, with the same bits in each: first to one maximum, then the sums
+    __device__ __forceinline__ void join_lanes(float k) {
+        float top = max;
+#pragma unroll
+        for (int d = 16; d; d /= 2) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+        if (top != -INFINITY) raise(top, k);
+#pragma unroll
+        for (int d = 16; d; d /= 2) {
+            s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
+            u += __shfl_xor_sync(0xFFFFFFFFu, u, d);
         }
     }
 };
