@@ -524,7 +524,7 @@ PyObject *grad_clip(PyObject *, PyObject *const *args, Py_ssize_t nargs) {
         const auto tensors = list("tensors", args[1]);
         std::vector<const Tensor *> outs;
         if (args[4] != Py_None) outs = list("out", args[4]);
-        const Tensors plain("a tensor", tensors), t = outs.empty() ? plain : Tensors("a tensor", tensors, &outs);
+        const Tensors t("a tensor", tensors, outs.empty() ? nullptr : &outs);
         const double max_norm = PyFloat_AsDouble(args[2]), eps = PyFloat_AsDouble(args[5]);
         if (PyErr_Occurred()) return nullptr;
         rar_grad_clip_args a{};
@@ -550,7 +550,7 @@ PyObject *grad_clip(PyObject *, PyObject *const *args, Py_ssize_t nargs) {
         if (!(a.max_norm >= 0.0f) || a.max_norm > 3.402823466e38f) refuse("max_norm must be finite and not negative");
         if (!(a.eps >= 0.0f) || a.eps > 3.402823466e38f) refuse("eps must be finite and not negative");
         if (args[3] == Py_None)
-            if (const int rc = norm_of(args[0], plain, norm, Tensor())) return PyLong_FromLong(rc);
+            if (const int rc = norm_of(args[0], t, norm, Tensor())) return PyLong_FromLong(rc);
         const int rc = rar_grad_clip(handle(args[0]), &a, stream_of(t.device));
         return rc ? PyLong_FromLong(rc) : tuple({norm});
     });
