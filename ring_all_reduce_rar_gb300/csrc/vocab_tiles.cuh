@@ -316,12 +316,27 @@ struct LogitSums {
         for (int i = 0; i < N; i++) top = fmaxf(top, z[i]);
         if (top > max) raise(top, k);
         const float ref = top == -INFINITY ? 0.0f : top;  // nothing but -inf, or NaN, which s then shows
+        // two logits an instruction, and two sums
+        float s2[2] = {s, 0.0f}, u2[2] = {u, 0.0f};
 #pragma unroll
-        for (int i = 0; i < N; i++) {
-            const float d = z[i] - ref, e = exp_scaled(d, k);
-            s += e;
-            u = fmaf(e, fmaxf(d, -1e30f), u);  // (-inf: 0 to be added)
+        for (int i = 0; i < N; i += 2) {
+            float d[2] = {z[i], z[i + 1]}, x[2], e[2];
+            asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%4, %4};\n\tadd.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t"
+                "mov.b64 b, {%5, %5};\n\tmul.rn.f32x2 a, a, b;\n\tmov.b64 {%2, %3}, a;\n\t}"
+                : "+f"(d[0]), "+f"(d[1]), "=f"(x[0]), "=f"(x[1])
+                : "f"(-ref), "f"(k));
+#pragma unroll
+            for (int j = 0; j < 2; j++) {
+                asm("ex2.approx.f32 %0, %1;" : "=f"(e[j]) : "f"(x[j]));
+                d[j] = fmaxf(d[j], -1e30f);  // (-inf: 0 to be added)
+            }
+            asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%4, %5};\n\tmov.b64 c, {%0, %1};\n\tadd.rn.f32x2 c, c, a;\n\tmov.b64 {%0, %1}, c;\n\t"
+                "mov.b64 b, {%6, %7};\n\tmov.b64 c, {%2, %3};\n\tfma.rn.f32x2 c, a, b, c;\n\tmov.b64 {%2, %3}, c;\n\t}"
+                : "+f"(s2[0]), "+f"(s2[1]), "+f"(u2[0]), "+f"(u2[1])
+                : "f"(e[0]), "f"(e[1]), "f"(d[0]), "f"(d[1]));
         }
+        s = s2[0] + s2[1];
+        u = u2[0] + u2[1];
     }
     __device__ __forceinline__ void join(float om, float os, float ou, float k) {
         if (os == 0.0f) return;  // nothing there
