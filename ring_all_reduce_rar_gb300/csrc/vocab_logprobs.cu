@@ -16,13 +16,13 @@
 //
 // Two forms of the forward pass, by what bounds it:
 //   up to 128 tokens (stream_fits), memory: the pieces are streamed once (vocab_stream.cuh), the logits go
-//     through L2 to a cluster of CTAs a token.  16 tokens by 65536 x 4096 bf16: 85 us for 537 MB (6.3 TB/s), 100 us
+//     through L2 to a cluster of CTAs a token.  16 tokens by 65536 x 4096 bf16: 85 us for 537 MB (6.3 TB/s), 99 us
 //     with the selection of 5 alternatives; 1 by 32768 x 2048: 26 us, 34 with 20.  By tiles 64 tokens by 32768 x
 //     2048 took 75 us with 8 alternatives, here 54 with 5; 128 by 4096 x 50021, whose accumulators leave room for one
 //     tile of rows at a time, took longer here than by tiles (160 us for the logits alone), so that is left to them.
 //   above, the tensor cores: tiles whose epilogues keep sums and alternatives (vocab_tiles.cuh), joined by token.  8192
-//     by 65536 x 4096 bf16 2.46 ms (1.79 PFLOP/s at the power limit), 2048 by 50021 x 2048 fp16 280 us, with 8
-//     alternatives 329: then the epilogues of a row's first tiles, whose lists fill, outlast the products.
+//     by 65536 x 4096 bf16 2.46 ms (1.79 PFLOP/s at the power limit), 2048 by 50021 x 2048 fp16 276 us, with 8
+//     alternatives 320: then the epilogues of a row's first tiles, whose lists fill, outlast the products.
 // Gradients: 8192 by 65536 x 4096 bf16 7.7 ms (1.72 PFLOP/s at the power limit); 333 by 10007 x 520 fp16 59 us, the latency
 // of six launches.
 #include <cmath>

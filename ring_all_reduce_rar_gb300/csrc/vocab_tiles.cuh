@@ -311,9 +311,15 @@ struct LogitSums {
     // z[n], of which those that are not there are -inf
     template <int N>
     __device__ __forceinline__ void add(const float (&z)[N], float k) {
-        float top = max;
+        float most = z[0];
 #pragma unroll
-        for (int i = 0; i < N; i++) top = fmaxf(top, z[i]);
+        for (int i = 1; i < N; i++) most = fmaxf(most, z[i]);
+        add(z, k, most);
+    }
+    // the same where their maximum is known
+    template <int N>
+    __device__ __forceinline__ void add(const float (&z)[N], float k, float most) {
+        const float top = fmaxf(max, most);
         if (top > max) raise(top, k);
         const float ref = top == -INFINITY ? 0.0f : top;  // nothing but -inf, or NaN, which s then shows
         // two logits an instruction, and two sums
@@ -393,9 +399,9 @@ __device__ __forceinline__ void sort_falling(float (&x)[32]) {
 // column that any of 32 rows wants, there would be several times as many).  A new key takes
 // the place of the least one; which is the least then is known from the 8 places around and the other
 // groups' least, in registers.  In a row's first tile the bound is the `top`-th largest of the maxima of 32
-// groups of columns.  (2048 tokens by 50021 x 2048 fp16: 280 us without alternatives, 303 with 1, 339
-// with 8, 429 with 32; with the least of as many groups' maxima for a bound 342 and 507, with a look at all
-// places for each key 876 with 32.)
+// groups of columns.  (2048 tokens by 50021 x 2048 fp16 back to back: 320 us with 8 alternatives; alone 276 us
+// without, 301 with 1, 332 with 8 and some 420 with 32; with the least of as many groups' maxima for a bound 78 us
+// more with 32, with a look at all places for each key twice the time.)
 struct TileTop {
     static constexpr int kNoted = 24, kRow = 32 * kTcEpilogueWarps, kGroups = RAR_LOGPROBS_MAX_TOP / 8;
     static constexpr int kNotedBytes = kNoted * kRow * 5;
@@ -835,14 +841,13 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(152)
                     if (r.cols - c0 <= 0) break;  // (the same for the whole warp)
                     mask_columns(v, r.cols - c0);
                     keep_target(a, r, c0, v);
-                    own.add(v, a.scale * 1.4426950408889634f);
-                    if (a.top) {
-                        float m[8];
-                        group_maxima(v, m);
+                    float m[8], here = -INFINITY;
+                    group_maxima(v, m);
 #pragma unroll
-                        for (int i = 0; i < 8; i++) most = fmaxf(most, m[i]);
-                        if (it.begins && a.top > 1) top.keep_maxima(m, c0);
-                    }
+                    for (int i = 0; i < 8; i++) here = fmaxf(here, m[i]);
+                    own.add(v, a.scale * 1.4426950408889634f, here);
+                    most = fmaxf(most, here);
+                    if (it.begins && a.top > 1) top.keep_maxima(m, c0);
                 } else {
                     tile_columns<MODE, DT>(a, r, c0, undo, first_window, direct, v);
                 }
