@@ -394,17 +394,22 @@ size_t plan(void *base, size_t tokens, size_t dim, size_t vocab, int p, int top,
     }
     return w.used;
 }
-// Up to so many tokens G is held as two 16-bit rows a token, the second what rounding left of the first, and the
-// products take both.  A gradient of few tokens is a sum of few products, in which G's rounding shows as much as the
-// gradient's own or, where one entry decides it, up to 2.6 times as much; over many tokens it adds 1.4 times.
-constexpr size_t kPairedTokens = 512;
+// G is held as two 16-bit rows a token, the second what rounding left of the first, and the products take both, for few
+// tokens.  A gradient of few tokens is a sum of few products, in which G's rounding shows as much as the
+// gradient's own or, where one entry decides it, up to 2.6 times as much; over many it adds 1.4 times.  A piece has only
+// the tokens that aim at it to decide it, so there up to 256 a piece count as few, while the work is little: the second
+// rows take 1.2 times the time for 1569 tokens by 854 x 480 (56 and 69 us), 1.5 times for 2048 by 4096 x 1024 (71 and
+// 105 us), which goes without.
+bool paired(size_t tokens, size_t dim, size_t vocab, int p) {
+    return tokens <= 512 || (tokens <= 256 * (size_t)p && (double)tokens * (double)dim * (double)vocab <= 0x1p32);
+}
 size_t plan_gradients(void *base, size_t tokens, size_t dim, size_t vocab, int p, VocabArgs *k) {
     WorkspacePlan w(base);
     plan_blocks(vocab, p, k);
     k->w_max = w.take<unsigned>(1);
     k->row_weight = w.take<float>(tokens);
     k->row_entropy = w.take<float>(tokens);
-    k->pair = tokens <= kPairedTokens ? (long long)tokens : 0;
+    k->pair = paired(tokens, dim, vocab, p) ? (long long)tokens : 0;
     // (one round: 333 tokens by 10007 x 520 63 us, 66 with two, 71 with three)
     plan_grad(w, k->pair ? 2 * tokens : tokens, dim, 1, k);
     return w.used;

@@ -11,7 +11,7 @@
 // time: the logit tiles again, G in the 16-bit type into the workspace, and
 // the two products with it.  dhidden adds up over the windows in 32 bits.
 //
-// All four products run on the tensor cores through one kernel (tc_gemm.cuh):
+// All four products run on the tensor cores through one kernel (vocab_tiles.cuh):
 // a pair of CTAs computes a 256 x 256 tile, and the epilogue of a tile overlaps the
 // next tile's product (two accumulators).  G is rounded once, to the
 // type of the products that it enters: an error of half a unit in its last place, of the

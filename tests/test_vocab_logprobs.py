@@ -366,6 +366,7 @@ def check_grad(got, ref, what=""):
 @pytest.mark.parametrize("p,tokens,dim,vocab", [
     (1, 1, 8, 2), (2, 1, 64, 300), (4, 127, 64, 255), (4, 129, 128, 1025), (8, 300, 520, 5003), (16, 33, 8, 9), (64, 5, 16, 3),
     (2, 1100, 136, 777), (3, 256, 1024, 4099), (3, 333, 1032, 5003), (8, 515, 2048, 10007), (1, 4096, 256, 33000), (3, 8192, 1288, 16700),
+    (16, 1569, 480, 854), (8, 2000, 64, 3001), (1, 512, 64, 900), (1, 513, 64, 900),
 ])
 def test_gradients(h, dtype, p, tokens, dim, vocab):  # noqa: F811
     g = gen(tokens * 7 + vocab)
