@@ -867,7 +867,8 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(152)
                     }
                     bound = nextafterf(bound, -INFINITY);
                 }
-                if (seen) bound = fmaxf(bound, top_value((unsigned long long)(seen - 1) << 32));
+                // (a bar of 0 has the key of -0 below it, which is no less)
+                if (seen) bound = fmaxf(bound, top_value((unsigned long long)(seen - (seen == 0x80000000u ? 2 : 1)) << 32));
                 if (!r.live) bound = INFINITY;
                 if (a.top && __any_sync(0xFFFFFFFFu, most > fmaxf(top.bar(), bound))) {
                     const unsigned long long least = top.least;
