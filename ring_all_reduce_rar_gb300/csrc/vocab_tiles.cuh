@@ -610,8 +610,10 @@ __device__ __forceinline__ void tile_columns(const VocabArgs &a, TileRow &r, int
 #pragma unroll
         for (int c = 0; c < 32; c++) {
             if constexpr (Mode<MODE>::logprob) {
-                // (every step for every column: one that is made on a condition becomes a branch)
-                const float logp = fmaf(v[c], a.scale, -r.lse), w = fmaf(r.w_log, logp, r.w), p = exp_of(logp);
+                // (every step for every column: one that is made on a condition becomes a branch.  Below -128 p is
+                // 0 in 32 bits, and so is p log p: for a logit of -infinity, too, where 0 x infinity would be NaN.
+                // p has the log probability as it is, so that NaN stays NaN.)
+                const float logp = fmaf(v[c], a.scale, -r.lse), w = fmaf(r.w_log, fmaxf(logp, -128.0f), r.w), p = exp_of(logp);
                 const float x = fmaf(p, w, c == y ? r.w_target : 0.0f);
                 v[c] = c < cols && r.used ? x : 0.0f;
             } else {
