@@ -116,27 +116,35 @@ __device__ __forceinline__ float cta_max(float v, float *red) {
     return v;
 }
 
+// A thread's sum of squares.  A long run of additions to one sum of squares loses more than their rounding's
+// share (small squares, which come more often than large ones, are rounded away from a sum that has grown): those of
+// 256 bf16 values come out 2.5e-7 low, of 2048 3.9e-6, of 16 1e-8.  So what a few loads bring is added up
+// first, and these batches with their additions' remainders (Knuth's two-sum), however many there are.
+struct Squares {
+    float s[4] = {}, total = 0.0f, rest = 0.0f;
+    __device__ __forceinline__ void add(int k, float x) { s[k] = fmaf(x, x, s[k]); }
+    __device__ __forceinline__ void batch() {
+        const float x = (s[0] + s[1]) + (s[2] + s[3]), t = total + x, y = t - total;
+        rest += (total - (t - y)) + (x - y);
+        total = t;
+        s[0] = s[1] = s[2] = s[3] = 0.0f;
+    }
+    __device__ __forceinline__ float sum() const { return total + rest; }  // (NaN where it passes binary32)
+};
+
 template <int DT>
 __device__ __forceinline__ double chunk_sum(const GradEntry &t, long long e0, long long e1) {
     __shared__ float red[kGradThreads / 32];
-    // (a long run of additions to one sum of squares loses more than their rounding's share: those of 256 bf16 values
-    // come out 2.5e-7 low, of 16 1e-8; so what a few loads bring is added up first)
-    float s[4] = {}, total = 0.0f;
-    auto batch = [&] {
-        total += (s[0] + s[1]) + (s[2] + s[3]);
-        s[0] = s[1] = s[2] = s[3] = 0.0f;
-    };
+    Squares own;
+    auto batch = [&] { own.batch(); };
     uint32_t bits = 0;  // of all elements
     auto one = [&](float x) {
         bits |= __float_as_uint(x) << 1;
-        s[0] = fmaf(x, x, s[0]);
+        own.add(0, x);
     };
     auto eight = [&](long long, const RowBits<DT> &b) {
 #pragma unroll
-        for (int e = 0; e < RowBits<DT>::VE; e++) {
-            const float x = b.get(e);
-            s[e % 4] = fmaf(x, x, s[e % 4]);
-        }
+        for (int e = 0; e < RowBits<DT>::VE; e++) own.add(e % 4, b.get(e));
         // (not the signs)
         bits |= DT == DT_F32 ? (b.w[0] | b.w[1] | b.w[2] | b.w[3]) << 1 : (b.w[0] | b.w[1] | b.w[2] | b.w[3]) & 0x7FFF7FFFu;
     };
@@ -146,7 +154,7 @@ __device__ __forceinline__ double chunk_sum(const GradEntry &t, long long e0, lo
     } else if (t.cols >= kShortRow) {
         walk_rows(t, e0, e1, [&](long long r, long long r0, long long r1) {
             const char *row = data + r * (t.stride - t.cols) * ElemInfo<DT>::bytes;
-            walk<DT, 4>(row, r0, r1, threadIdx.x % 32, 32, eight, [&](long long i) { one(load_f<DT>(row, i)); }, [] {});
+            walk<DT, 4>(row, r0, r1, threadIdx.x % 32, 32, eight, [&](long long i) { one(load_f<DT>(row, i)); }, batch);
             batch();
         });
     } else {
@@ -156,19 +164,20 @@ __device__ __forceinline__ double chunk_sum(const GradEntry &t, long long e0, lo
         }
     }
     batch();
-    const float sum = cta_sum(total, red);
+    const float sum = cta_sum(own.sum(), red);
     const bool any = __syncthreads_or(bits != 0);
     // Squares that pass binary32 or vanish in it: the chunk once more, relative to its largest
     // element (in these bounds what was lost is below 2^-24 of the sum for a chunk of 2^30 elements)
     if (!any || (sum >= 0x1p-90f && sum <= 0x1p126f)) return (double)sum;
     float most = 0.0f;
-    bool finite = true;
+    bool finite = true, nan = false;
     for (long long i = e0 + threadIdx.x; i < e1; i += kGradThreads) {
         const float x = fabsf(element<DT>(t, i));
         finite = finite && isfinite(x);
+        nan = nan || isnan(x);
         most = fmaxf(most, x);
     }
-    if (__syncthreads_or(!finite)) return (double)sum;  // inf or NaN, as the sum is
+    if (__syncthreads_or(!finite)) return (double)(__syncthreads_or(nan) ? NAN : INFINITY);
     most = cta_max(most, red);
     const int e = ilogbf(most);
     float v = 0.0f;
