@@ -180,12 +180,13 @@ __device__ __forceinline__ double chunk_sum(const GradEntry &t, long long e0, lo
     if (__syncthreads_or(!finite)) return (double)(__syncthreads_or(nan) ? NAN : INFINITY);
     most = cta_max(most, red);
     const int e = ilogbf(most);
-    float v = 0.0f;
+    Squares v;
     for (long long i = e0 + threadIdx.x; i < e1; i += kGradThreads) {
-        const float x = ldexpf(element<DT>(t, i), -e);
-        v = fmaf(x, x, v);
+        v.add(0, ldexpf(element<DT>(t, i), -e));
+        if ((i / kGradThreads) % 16 == 15) v.batch();
     }
-    return ldexp((double)cta_sum(v, red), 2 * e);
+    v.batch();
+    return ldexp((double)cta_sum(v.sum(), red), 2 * e);
 }
 
 template <int N>

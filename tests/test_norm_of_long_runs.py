@@ -1,4 +1,5 @@
-"""The norm where a thread adds up many squares: long rows of matrices with gaps, and large chunks.
+"""The norm where a thread adds up many squares: long rows of matrices with gaps, large chunks, and the second pass over
+values whose squares overflow or vanish in 32 bits.
 
 Squares of normal values lie close to 0 more often than not, so that a long run of additions comes out low.  A thread adds at
 most 18 squares one after the other (16 from its loads, an element at each end of a run), two more for its four
@@ -46,6 +47,16 @@ def test_large_chunks(h, dtype, cols, gap):  # noqa: F811
     """Chunks of 2^20 elements and more, without gaps and in rows too short for a warp."""
     x = torch.randn((1 << 27) // cols, cols + gap, generator=gen(cols), device="cuda").to(dtype)[:, :cols]
     check(h, [x] * 33)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("cols,gap", [(1 << 27, 0), (8192, 8), (60, 4)])
+def test_the_second_pass(h, dtype, cols, gap):  # noqa: F811
+    """Squares that vanish, and that overflow, in chunks of 2^20 elements and more.  (fp16 knows no such values
+    but below its normal ones, where a few bits are left: exact all the same.)"""
+    for size in (2.0 ** -70, 2.0 ** 62) if dtype != torch.float16 else (2.0 ** -23,):
+        x = (torch.randn((1 << 27) // cols, cols + gap, generator=gen(3), device="cuda") * size).to(dtype)[:, :cols]
+        check(h, [x] * 33)
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
