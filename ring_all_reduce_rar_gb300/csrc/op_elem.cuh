@@ -104,9 +104,11 @@ template <int DT>
 struct RowBits {
     static constexpr int VE = 16 / ElemInfo<DT>::bytes;
     uint32_t w[4];
+    // (coherent: where a call works in place the row is written later, and the read-only path is
+    // for what no thread writes while the kernel runs)
     __device__ __forceinline__ void load(const void *row, int vec, bool has) {
         uint4 q = make_uint4(0, 0, 0, 0);
-        if (has) q = __ldg(static_cast<const uint4 *>(row) + vec);
+        if (has) q = static_cast<const uint4 *>(row)[vec];
         w[0] = q.x, w[1] = q.y, w[2] = q.z, w[3] = q.w;
     }
     __device__ __forceinline__ float get(int e) const {
