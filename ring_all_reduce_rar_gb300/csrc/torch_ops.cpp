@@ -88,6 +88,12 @@ std::vector<const Tensor *> list(const std::string &name, PyObject *o) {
     for (Py_ssize_t i = 0; i < n; i++) v.push_back(&tensor(name, PySequence_Fast_GET_ITEM(o, i)));
     return v;
 }
+// For tensors that a call has written: autograd's count of a tensor's changes, by which a backward
+// pass knows that a value it kept is no longer the one it needs.
+void written(const std::vector<const Tensor *> &v) {
+    for (const Tensor *t : v)
+        if (!t->is_inference()) t->unsafeGetTensorImpl()->bump_version();
+}
 // Pointers of matrices with one row stride, which those of a single row do
 // not decide.
 struct Matrices {
@@ -383,7 +389,8 @@ PyObject *embedding_grad(PyObject *, PyObject *const *args, Py_ssize_t nargs) {
     return call(nargs, 6, [&]() -> PyObject * {
         const Tensor &dout = tensor("dout", args[1]), &tokens = tensor("tokens", args[2]);
         const Common c("dout", dout);
-        const Pieces w("a gradient piece", list("dtables", args[3]), c);
+        const auto dtables = list("dtables", args[3]);
+        const Pieces w("a gradient piece", dtables, c);
         rar_embedding_grad_args a{};
         a.dout_stride = matrix("dout", dout, dout.size(0), w.dim, c);
         a.dout = dout.data_ptr();
@@ -403,7 +410,9 @@ PyObject *embedding_grad(PyObject *, PyObject *const *args, Py_ssize_t nargs) {
         Tensor ws = c.bytes(a.workspace_bytes);
         a.workspace = ws.data_ptr();
         const int rc = rar_embedding_grad(handle(args[0]), &a, stream_of(c));
-        return rc ? PyLong_FromLong(rc) : tuple({});
+        if (rc) return PyLong_FromLong(rc);
+        written(dtables);
+        return tuple({});
     });
 }
 
@@ -552,7 +561,9 @@ PyObject *grad_clip(PyObject *, PyObject *const *args, Py_ssize_t nargs) {
         if (args[3] == Py_None)
             if (const int rc = norm_of(args[0], t, norm, Tensor())) return PyLong_FromLong(rc);
         const int rc = rar_grad_clip(handle(args[0]), &a, stream_of(t.device));
-        return rc ? PyLong_FromLong(rc) : tuple({norm});
+        if (rc) return PyLong_FromLong(rc);
+        written(outs.empty() ? tensors : outs);
+        return tuple({norm});
     });
 }
 

@@ -1,7 +1,8 @@
-"""Tensors that a call writes where they lie."""
+"""Tensors that a call writes where they lie, and what autograd learns of it."""
 import pytest
 import torch
 
+import ring_all_reduce_rar_gb300 as rar
 from tests.test_model_ops import DTYPES, gen, h, normal  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -22,3 +23,43 @@ def test_clipping_in_place_is_as_apart(h, dtype, rows, cols, gap):  # noqa: F811
         kept[lead:].view(rows, cols + gap)[:, :cols] = apart
         assert torch.equal(flat, kept)
     h.check()
+
+
+def test_autograd_refuses_values_that_were_scaled(h):  # noqa: F811
+    """A value that a backward pass still needs is not used after it changed."""
+    for write in (lambda t: h.grad_clip([t], 0.1), lambda t: h.grad_clip([torch.ones(50, device="cuda")], 0.1, out=[t]),
+                  lambda t: h.grad_clip([t.view(5, 10)[:, :4]], 0.1)):
+        x = torch.ones(50, device="cuda", requires_grad=True)
+        kept = x * 2.0
+        loss = (kept * kept).sum()
+        before = kept._version
+        write(kept.detach())
+        assert kept._version > before
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            loss.backward()
+
+
+def test_tensors_that_are_read_keep_their_version(h):  # noqa: F811
+    x, out, norm = torch.ones(50, device="cuda"), torch.empty(50, device="cuda"), torch.ones((), device="cuda")
+    versions = x._version, norm._version
+    h.grad_norm([x])
+    h.grad_clip([x], 0.1, norm=norm, out=[out])
+    assert (x._version, norm._version) == versions
+    with pytest.raises(ValueError):
+        h.grad_clip([x], -1.0)
+    with pytest.raises(rar.RarError):
+        h.grad_clip([x, x], 1.0)
+    assert x._version == versions[0]
+    # (tensors made for inference have no version)
+    with torch.inference_mode():
+        y = torch.full((50,), 2.0, device="cuda")
+    h.grad_clip([y], 1.0)
+    assert abs(float(torch.linalg.vector_norm(y)) - 1) < 1e-5
+
+
+def test_a_table_gradient_that_is_added_to(h):  # noqa: F811
+    g = gen(3)
+    tables = [torch.zeros(20, 16, device="cuda") for _ in range(2)]
+    before = [t._version for t in tables]
+    h.embedding_grad(normal(g, 7, 16), torch.arange(7, device="cuda"), tables, accumulate=True)
+    assert all(t._version > v for t, v in zip(tables, before))
