@@ -21,7 +21,8 @@ struct MatrixSpan {
     uintptr_t base;
     size_t rows, width, pitch;
     size_t extent() const { return rows ? (rows - 1) * pitch + width : 0; }
-    bool same_as(const MatrixSpan &o) const { return base == o.base && pitch == o.pitch && width == o.width; }
+    // (one row is itself whatever the distance to a next one)
+    bool same_as(const MatrixSpan &o) const { return base == o.base && rows == o.rows && width == o.width && (rows <= 1 || pitch == o.pitch); }
 };
 
 // Whether two matrices share a byte.  Two column ranges of one wider matrix

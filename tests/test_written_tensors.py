@@ -1,8 +1,11 @@
 """Tensors that a call writes where they lie, and what autograd learns of it."""
+import ctypes
+
 import pytest
 import torch
 
 import ring_all_reduce_rar_gb300 as rar
+from ring_all_reduce_rar_gb300 import _ops
 from tests.test_model_ops import DTYPES, gen, h, normal  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -63,3 +66,34 @@ def test_a_table_gradient_that_is_added_to(h):  # noqa: F811
     before = [t._version for t in tables]
     h.embedding_grad(normal(g, 7, 16), torch.arange(7, device="cuda"), tables, accumulate=True)
     assert all(t._version > v for t, v in zip(tables, before))
+
+
+@pytest.mark.parametrize("stride,out_stride", [(0, 40), (40, 0), (40, 64), (1 << 40, 40)])
+def test_one_row_in_place_with_any_stride(h, stride, out_stride):  # noqa: F811
+    x = normal(gen(1), 40)
+    norm = torch.linalg.vector_norm(x).reshape(1)
+    want = x * (0.5 / norm)
+    tensors, out = (_ops.Tensor(x.data_ptr(), 1, 1, 40, s) for s in (stride, out_stride))
+    a = _ops.GradClipArgs()
+    a.tensors, a.n, a.out = ctypes.addressof(tensors), 1, ctypes.addressof(out)
+    a.norm, a.max_norm, a.eps = norm.data_ptr(), 0.5, 0.0
+    lib, stream = rar.load_library(), torch.cuda.current_stream().cuda_stream
+    assert lib.rar_grad_clip(h.h, ctypes.byref(a), stream) == 0, rar.rar_last_error(h.h)
+    # (the quotient and the product are rounded)
+    assert bool(((x.double() - want.double()).abs() <= 4 * 2.0 ** -24 * want.double().abs()).all())
+    h.check()
+
+
+@pytest.mark.parametrize("residual_stride,sum_stride", [(0, 40), (40, 64), (1 << 40, 0)])
+def test_a_residual_of_one_row_is_written_with_any_stride(h, residual_stride, sum_stride):  # noqa: F811
+    g = gen(2)
+    part, residual = normal(g, 1, 40), normal(g, 1, 40)
+    want = h.add_rmsnorm([part], residual=residual).sum
+    ptrs = (ctypes.c_void_p * 1)(part.data_ptr())
+    a = _ops.RmsNormArgs()
+    a.parts, a.p, a.dtype, a.rows, a.dim = ctypes.addressof(ptrs), 1, 1, 1, 40
+    a.residual, a.residual_stride, a.sum, a.sum_stride = residual.data_ptr(), residual_stride, residual.data_ptr(), sum_stride
+    lib, stream = rar.load_library(), torch.cuda.current_stream().cuda_stream
+    assert lib.rar_add_rmsnorm(h.h, ctypes.byref(a), stream) == 0, rar.rar_last_error(h.h)
+    assert torch.equal(residual, want)
+    h.check()
