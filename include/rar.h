@@ -568,7 +568,8 @@ int rar_vocab_logprobs(rar_handle h, const rar_vocab_logprobs_args *a, void *str
  *   G = logit_scale (a onehot(target) - q (a + b (log q + entropy))),
  *   q = exp(l - lse),  dhidden = G W,  dweights = G^T hidden,
  * with lse and entropy as the call above gave them.  A token whose target is
- * left out, or with a = b = 0, has no part in them, whatever its hidden state holds.
+ * left out, or with a = b = 0, has no part in them, whatever its hidden state holds;
+ * for a target left out that holds of dentropy, too.
  * Where q is 0 (a logit of -infinity, or one that is it after scaling) q log q is 0, too.
  * G is held in the dtype for a window of the vocabulary at a time. */
 typedef struct {

@@ -237,7 +237,8 @@ def rar_vocab_logprobs_grad(handle, hidden, weights, targets, lse, entropy=None,
                             logit_scale=1.0, stream=None):
     """(dhidden, dweights) of rar_vocab_logprobs from the gradients of its
     log probabilities and entropies (float32 vectors; None: zeros).  lse and
-    entropy are its results; entropy is needed with dentropy."""
+    entropy are its results; entropy is needed with dentropy.  A token whose
+    target is left out has no part in the gradients, its dentropy neither."""
     return _run(handle, stream, _module().vocab_logprobs_grad, hidden, weights, targets, lse, entropy, dlogprob, dentropy,
                 logit_scale)
 

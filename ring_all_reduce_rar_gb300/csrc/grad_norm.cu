@@ -8,7 +8,7 @@
 // sums go to the workspace and are added in a fixed order (no atomics).  Bound by
 // memory: one read of everything, and a read and a write.  The norm of 1.07 G bf16 elements takes 296 us
 // (7.2 TB/s, a read alone runs above a copy's rate), of 157 M float32 in 440 tensors 95 us; clipping the 1.07 G into 32 bits
-// 1.08 ms more for 6.4 GB, two thirds of them written (a write alone runs at 4.1 TB/s).
+// 1.01 ms more for 6.4 GB, two thirds of them written (a write alone runs at 4.1 TB/s), in place 0.62 (7.0 TB/s).
 #include <algorithm>
 
 #include "op_elem.cuh"
@@ -89,6 +89,8 @@ __device__ __forceinline__ void walk(const char *base, long long e0, long long e
     }
 }
 // The same for elements [e0, e1) of a matrix with gaps, a warp a row: f(row, first and last element) of its parts.
+// (Rows longer than an eighth of a chunk leave warps without one: the norm of 8192 x 8192 bf16 takes 86 us with gaps, 60
+// without, clipping in place 61 and 47.)
 template <typename F>
 __device__ __forceinline__ void walk_rows(const GradEntry &t, long long e0, long long e1, F &&f) {
     for (long long r = e0 / t.cols + threadIdx.x / 32; r * t.cols < e1; r += kGradThreads / 32) f(r, max(e0, r * t.cols), min(e1, (r + 1) * t.cols));
@@ -262,7 +264,7 @@ __device__ __forceinline__ void scale_chunk(const GradEntry &t, long long e0, lo
     // elements [i0, i1) of runs that begin (element 0) at `from` and `to`
     auto run = [&](const char *from, char *to, long long i0, long long i1, int tid, int n) {
         const long long lead = (0 - (uintptr_t)(from + i0 * EB)) % 16 / EB;
-        if ((uintptr_t)(to + (i0 + lead) * OB) % 16) {  // vectors that are read go to no whole ones
+        if ((uintptr_t)(to + (i0 + lead) * OB) % 16) {  // vectors that are read go to no whole ones (268 M bf16 into 32 bits 988 us, else 404)
             for (long long i = i0 + tid; i < i1; i += n) store_f<OUT>(to, i, load_f<DT>(from, i) * f);
             return;
         }
@@ -312,8 +314,8 @@ size_t elements(const rar_tensor &t) { return t.rows * t.cols; }
 // Elements of a chunk: a power of two, 8192 or more (at 4096, 10 M fp16 elements took 24 us to clip, 17 at
 // 8192), so that there are at most `most` chunks, and one more a tensor.  For the norm 4096, whose sums one CTA
 // joins: 1.07 G elements bf16 take 296 us with 512 to 4096 of them, 310 with up to 16384, 334 with 65536;
-// 157 M float32 99 us with up to 4096, 102 and 191.  Clipping has nothing to join: the 1.07 G into 32 bits took
-// 1716 us with up to 512, 1473 with 2048, 1424 with 16384, 1400 with 65536, with the norm before it.
+// 157 M float32 99 us with up to 4096, 102 and 191.  Clipping has nothing to join: the 1.07 G into 32 bits take
+// 1683 us with up to 512, 1447 with 2048, 1356 with 16384, 1300 with 65536, with the norm before it.
 constexpr size_t kLeastChunk = 8192, kNormChunks = 4096, kClipChunks = 65536;
 size_t chunk_elements(const rar_tensor *tensors, size_t n, size_t most) {
     size_t total = 0, chunk = kLeastChunk;

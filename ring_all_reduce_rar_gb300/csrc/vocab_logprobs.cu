@@ -19,7 +19,8 @@
 //     through L2 to a cluster of CTAs a token.  16 tokens by 65536 x 4096 bf16: 85 us for 537 MB (6.3 TB/s), 99 us
 //     with the selection of 5 alternatives; 1 by 32768 x 2048: 26 us, 34 with 20.  By tiles 64 tokens by 32768 x
 //     2048 took 75 us with 8 alternatives, here 54 with 5; 128 by 4096 x 50021, whose accumulators leave room for one
-//     tile of rows at a time, took longer here than by tiles (160 us for the logits alone), so that is left to them.
+//     tile of rows at a time, took longer here than by tiles (160 us for the logits alone; by tiles 65 to 128 tokens by
+//     65536 x 4096 take 112 in all), so that is left to them.
 //   above, the tensor cores: tiles whose epilogues keep sums and alternatives (vocab_tiles.cuh), joined by token.  8192
 //     by 65536 x 4096 bf16 2.46 ms (1.79 PFLOP/s at the power limit), 2048 by 50021 x 2048 fp16 276 us, with 8
 //     alternatives 320: then the epilogues of a row's first tiles, whose lists fill, outlast the products.
@@ -354,10 +355,10 @@ constexpr size_t kPassTokens = 16384;
 // Rows of tiles that are worked on at a time: the most that cost little more rounds of tiles than the best
 // number (in the last round of a single group of rows a block too few costs as much as one; over several groups
 // that evens out).  Each group reads all pieces once and begins its lists anew, so 5 % more rounds are worth fewer
-// groups, and 10 % a single one: 2048 tokens by 50021 x 2048 fp16 with 8 alternatives take 332 us with 8 rows in
-// 23 rounds, 348 with 4 rows in 21; 600 by 50021 x 1024 66 us without any by 3 rows, 76 row by row; 8192 by
-// 65536 x 4096 bf16 2.41 ms with 6 rows, 2.48 with 8 (6 % more rounds).  (Alternatives have no say: with and
-// without them the sums are the same.)
+// groups, and 10 % a single one: 2048 tokens by 50021 x 2048 fp16 with 8 alternatives take 325 us with 8 rows in
+// 23 rounds, 341 with 6 in 22, 334 with 5 and 331 with 4 in 21; 600 by 50021 x 1024 66 us without any by 3 rows, 76
+// row by row; 8192 by 65536 x 4096 bf16 2.28 ms with 5 rows, which is the choice, and with 4 (109 and 108 rounds), 2.30
+// with 6 or 8 (113).  (Alternatives have no say: with and without them the sums are the same.)
 int choose_width(int tb, int nb, int pairs) {
     auto rounds = [&](int w) {
         const int groups = tb / w, rest = tb % w;

@@ -274,8 +274,8 @@ __device__ __forceinline__ uint4 narrow8_scaled(const float *v, float scale) {
 // by 1e-4 at dim 16384, so that exp(z - lse) with logits near 9000 was off by a factor of 0.4.  So
 // both passes that make logits, for a dim above that of one sum, end their accumulators
 // every 16 steps (1024 of dim) and add them up in registers: 5e-7.  It costs 8 to 10 % of
-// a long forward pass (2048 tokens by 50021 x 2048 fp16 314 us against 282, 8192 by 65536 x 4096
-// bf16 2.54 ms against 2.33), 3 to 4 % with gradients.  A dim of one sum keeps the plain form
+// a long forward pass (2048 tokens by 50021 x 2048 fp16 314 us against 282 when it came in, 285 now; 8192 by
+// 65536 x 4096 bf16 2.54 ms against 2.33), 3 to 4 % with gradients.  A dim of one sum keeps the plain form
 // and its time.  Products whose results are rounded to 16 bits do without.
 constexpr int kStepsPerSum = 16;
 
@@ -672,7 +672,8 @@ __device__ __forceinline__ void add_exp(float &m, float &s, float om, float os) 
 // row 32 columns at a time: the code of all 128 at once is four times as long, and
 // its instruction fetches showed in calls of a few tiles.
 // At most 152 registers: three warps of this kernel then leave each quarter of an SM
-// room for a warp of 32, so that a CTA of the join can wait there for the end.
+// room for a warp of 32, so that a CTA of the join can wait there for the end.  (Where the logits come as sums of 1024,
+// whose 128 registers live beside an epilogue's own, log probabilities spill 224 bytes a thread so, their G 56.)
 template <int MODE, int DT>
 __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(152)
     vocab_tile_kernel(const __grid_constant__ VocabArgs a, const __grid_constant__ VocabMaps maps, int b0, int nb) {

@@ -19,7 +19,7 @@
 //
 // Bound by the tensor cores for many tokens (8 tokens x vocab x dim operations
 // against 6 if the logits were kept): 8192 tokens by 65536 x 4096 bf16 take 2.5 ms forward
-// (1.76 PFLOP/s; 2.7 ms back to back) and 11.4 ms with gradients (1.54 PFLOP/s) at the power
+// (1.76 PFLOP/s; 2.7 ms back to back) and 10.8 ms with gradients (1.63 PFLOP/s) at the power
 // limit (1.37 kW, which leaves 1725 of 2070 MHz).  For few tokens by the fill of full tiles in two
 // uneven waves: 16 by 32768 x 2048 take 38 us, as 256 do (134 MB of weights, 3.5 TB/s).
 #include "vocab_tiles.cuh"
